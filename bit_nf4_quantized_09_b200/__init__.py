@@ -42,9 +42,14 @@ class Nf4WeightC(ctypes.Structure):
                 ("absmax", ctypes.c_void_p)]
 
 
+class Int8WeightC(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
 _lib = None
 _vp, _i64, _sz, _int, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 _wp = ctypes.POINTER(Nf4WeightC)
+_w8p = ctypes.POINTER(Int8WeightC)
 
 # name -> (restype, argtypes); names match include/qlora_nf4.h
 _SIGNATURES = {
@@ -68,6 +73,16 @@ _SIGNATURES = {
     "qlora_linear_fwd_group": (_int, [_vp, _i64, _wp, _int, _vp, _vp, _int, _f32, _vp, _vp, _vp, _sz, _vp]),
     "qlora_linear_bwd_group": (_int, [_vp, _vp, _i64, _wp, _int, _vp, _vp, _int, _f32, _vp, _vp, _vp, _vp, _vp,
                                       _sz, _vp]),
+    "qlora_expert_order": (_int, [_vp, _i64, _int, _vp, _vp, _vp]),
+    "qlora_workspace_bytes_experts": (_sz, [_int, _i64, _i64, _i64, _int, _int]),
+    "qlora_linear_fwd_experts": (_int, [_vp, _i64, _wp, _int, _vp, _vp, _vp, _int, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_linear_bwd_experts": (_int, [_vp, _vp, _i64, _wp, _int, _vp, _vp, _vp, _int, _f32, _vp, _vp, _vp, _vp, _vp,
+                                        _sz, _vp]),
+    "qlora_quantize_int8": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "qlora_quantize_int8_bf16": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "qlora_workspace_bytes_int8": (_sz, [_i64, _i64, _i64, _int]),
+    "qlora_linear_int8": (_int, [_vp, _i64, _w8p, _vp, _vp, _sz, _vp]),
+    "qlora_linear_int8_experts": (_int, [_vp, _i64, _w8p, _int, _vp, _vp, _vp, _sz, _vp]),
     "qlora_nf4_tables": (_int, [ctypes.POINTER(_f32), ctypes.POINTER(_f32)]),
     "qlora_device_status": (_int, [_vp, ctypes.POINTER(_int), _vp]),
     "qlora_status_string": (ctypes.c_char_p, [_int]),
@@ -460,6 +475,221 @@ def linear_bwd_group(dY: torch.Tensor, X: torch.Tensor, group: list, A: torch.Te
            "qlora_linear_bwd_group")
     _after_call(ws, "qlora_linear_bwd_group", M)
     return dX, dA, dB
+
+
+# ------------------------------------------------------- layers of experts ---
+
+def _want(t: torch.Tensor | None, what: str, where: str, shape: tuple, dtype, device):
+    """Raises unless t is a contiguous CUDA tensor of this shape, type and device."""
+    if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}" + (
+            "" if t.is_contiguous() else ", not contiguous")
+        raise QLoraError(-2 if t is not None and t.dtype == dtype and t.device == device else -1, where,
+                         f"{what}: a contiguous {dtype} {tuple(shape)} on {device} is wanted, got {got}")
+
+
+def _on(device, call, *args):
+    """The call with the tensors' device current, on that device's current stream."""
+    if device.type != "cuda":
+        raise QLoraError(-1, "device", f"the tensors are on {device}; a CUDA device is wanted (there is no CPU path)")
+    if device.index == torch.cuda.current_device():
+        return call(*args, _stream(device))
+    with torch.cuda.device(device):
+        return call(*args, _stream(device))
+
+
+def _ws_on(nbytes: int, device, ws: torch.Tensor | None, where: str) -> torch.Tensor:
+    if ws is not None and (ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous()):
+        raise QLoraError(-1, where, f"workspace: a contiguous uint8 tensor on {device} is wanted")
+    return _ws(nbytes, device, ws)
+
+
+def _check_on(ws: torch.Tensor, where: str, M: int):
+    if _check_device_status and M > 0:
+        with torch.cuda.device(ws.device):
+            _after_call(ws, where, M)
+
+
+def expert_weight(w: NF4Weight, e: int, E: int) -> NF4Weight:
+    """Expert e of a stacked weight of E experts (for merge_lora or the calls on
+    one layer): views of its codes and constants, copied where a slice would not
+    start on 16 bytes. With double quantisation an expert's constants must be
+    whole second-level groups: N K / 64 a multiple of 256."""
+    if not 1 <= E <= 512 or w.N % E or not 0 <= e < E:
+        raise QLoraError(-2, "expert_weight", f"expert {e} of {E}, {w.N} rows")
+    N, K = w.N // E, w.K
+    nb = N * K // 64
+
+    def part(t, n):
+        return t[e * n:(e + 1) * n] if e * n * t.element_size() % 16 == 0 else t[e * n:(e + 1) * n].clone()
+
+    codes = part(w.codes, N * K // 2)
+    if not w.double_quant:
+        return NF4Weight(codes, None, None, None, N, K, absmax=part(w.absmax, nb))
+    if nb % 256:
+        raise QLoraError(-2, "expert_weight", f"N K / 64 = {nb} is not a multiple of 256")
+    return NF4Weight(codes, part(w.qabsmax, nb), part(w.s2, nb // 256), w.mean, N, K)
+
+
+def expert_order(ids: torch.Tensor, E: int, order: torch.Tensor | None = None, offsets: torch.Tensor | None = None):
+    """(order int32 [M], offsets int32 [E + 1]) of a batch whose row m goes to
+    expert ids[m] (int32): a stable sort by id, rows with an id outside [0, E)
+    behind all others; expert e owns places [offsets[e], offsets[e + 1])."""
+    where, M = "qlora_expert_order", ids.numel()
+    _want(ids, "ids", where, (M,), torch.int32, ids.device)
+    if not 1 <= E <= 512:
+        raise QLoraError(-1, where, f"E = {E}")
+    order = order if order is not None else torch.empty(M, dtype=torch.int32, device=ids.device)
+    offsets = offsets if offsets is not None else torch.empty(E + 1, dtype=torch.int32, device=ids.device)
+    _want(order, "order", where, (M,), torch.int32, ids.device)
+    _want(offsets, "offsets", where, (E + 1,), torch.int32, ids.device)
+    _check(_on(ids.device, lib().qlora_expert_order, _ptr(ids), M, E, _ptr(order), _ptr(offsets)), where)
+    return order, offsets
+
+
+def workspace_bytes_experts(op: int, M: int, N: int, K: int, r: int, E: int) -> int:
+    """Workspace of the expert calls; N and K are one expert's."""
+    return int(lib().qlora_workspace_bytes_experts(op, M, N, K, r, E))
+
+
+def _expert_shapes(where, X, w, A, B, offsets, E):
+    """(M, N, K, r, device) of an expert call, its inputs checked."""
+    dev = X.device
+    if X.dim() != 2 or A.dim() != 2 or not 1 <= E <= 512 or w.N % E or A.shape[0] % E:
+        raise QLoraError(-2, where, f"X {tuple(X.shape)}, A {tuple(A.shape)}, weight {w.N} x {w.K}, E = {E}")
+    M, K, N, r = X.shape[0], w.K, w.N // E, A.shape[0] // E
+    _want(X, "X", where, (M, K), torch.bfloat16, dev)
+    _want(A, "A", where, (E * r, K), torch.bfloat16, dev)
+    _want(B, "B", where, (E * N, r), torch.bfloat16, dev)
+    _want(offsets, "offsets", where, (E + 1,), torch.int32, dev)
+    if w.codes.device != dev:
+        raise QLoraError(-1, where, f"the weight is on {w.codes.device}, X on {dev}")
+    return M, N, K, r, dev
+
+
+def linear_fwd_experts(X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, E: int,
+                       alpha: float, Y: torch.Tensor | None = None, sT: torch.Tensor | None = None,
+                       save_sT: bool = True, ws: torch.Tensor | None = None):
+    """(Y, sT) of E experts (w: their NF4 weights stacked, E N rows): row m in
+    [offsets[e], offsets[e + 1]) gives Y[m] = X[m] deq(W_e)^T + sT[m] B_e^T, sT[m] =
+    (alpha/r) X[m] A_e^T. A: bf16 [E r, K]; B: bf16 [E N, r]; offsets: int32 [E + 1];
+    sT: bf16 [M, 2 r], a sum of two terms. Rows of no expert keep what Y and sT
+    held (a Y or sT allocated here holds nothing there)."""
+    where = "qlora_linear_fwd_experts"
+    M, N, K, r, dev = _expert_shapes(where, X, w, A, B, offsets, E)
+    Y = Y if Y is not None else torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+    _want(Y, "Y", where, (M, N), torch.bfloat16, dev)
+    if save_sT:
+        sT = sT if sT is not None else torch.empty(M, 2 * r, dtype=torch.bfloat16, device=dev)
+        _want(sT, "sT", where, (M, 2 * r), torch.bfloat16, dev)
+    ws = _ws_on(workspace_bytes_experts(OP_FWD, M, N, K, r, E), dev, ws, where)
+    v = w.c_view()
+    _check(_on(dev, lib().qlora_linear_fwd_experts, _ptr(X), M, ctypes.byref(v), E, _ptr(offsets), _ptr(A), _ptr(B), r,
+               float(alpha), _ptr(Y), _ptr(sT) if save_sT else None, _ptr(ws), ws.numel()), where)
+    _check_on(ws, where, M)
+    return Y, (sT if save_sT else None)
+
+
+def linear_bwd_experts(dY: torch.Tensor, X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: torch.Tensor,
+                       offsets: torch.Tensor, E: int, alpha: float, sT: torch.Tensor | None = None,
+                       dX: torch.Tensor | None = None, dA: torch.Tensor | None = None,
+                       dB: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """(dX bf16 [M, K], dA fp32 [E r, K], dB fp32 [E N, r]) of linear_fwd_experts;
+    sT as it returned it, or None to recompute it. An expert without rows gets
+    zero gradients; rows of no expert keep what dX held."""
+    where = "qlora_linear_bwd_experts"
+    M, N, K, r, dev = _expert_shapes(where, X, w, A, B, offsets, E)
+    _want(dY, "dY", where, (M, N), torch.bfloat16, dev)
+    if sT is not None:
+        _want(sT, "sT", where, (M, 2 * r), torch.bfloat16, dev)
+    dX = dX if dX is not None else torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+    dA = dA if dA is not None else torch.empty(E * r, K, dtype=torch.float32, device=dev)
+    dB = dB if dB is not None else torch.empty(E * N, r, dtype=torch.float32, device=dev)
+    _want(dX, "dX", where, (M, K), torch.bfloat16, dev)
+    _want(dA, "dA", where, (E * r, K), torch.float32, dev)
+    _want(dB, "dB", where, (E * N, r), torch.float32, dev)
+    ws = _ws_on(workspace_bytes_experts(OP_BWD, M, N, K, r, E), dev, ws, where)
+    v = w.c_view()
+    _check(_on(dev, lib().qlora_linear_bwd_experts, _ptr(dY), _ptr(X), M, ctypes.byref(v), E, _ptr(offsets), _ptr(A),
+               _ptr(B), r, float(alpha), _ptr(sT), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel()), where)
+    _check_on(ws, where, M)
+    return dX, dA, dB
+
+
+# ---------------------------------------------------------- 8-bit integers ---
+
+@dataclasses.dataclass
+class Int8Weight:
+    """An N x K weight in 8-bit integers, W[n, k] = scale[n] codes[n, k]."""
+    codes: torch.Tensor  # int8 [N, K]
+    scale: torch.Tensor  # float32 [N]
+    N: int
+    K: int
+
+    def c_view(self) -> Int8WeightC:
+        key = (self.codes.data_ptr(), self.scale.data_ptr(), self.N, self.K)
+        cached = self.__dict__.get("_c_view")
+        if cached is None or cached[0] != key:
+            _want(self.codes, "codes", "Int8Weight", (self.N, self.K), torch.int8, self.codes.device)
+            _want(self.scale, "scale", "Int8Weight", (self.N,), torch.float32, self.codes.device)
+            cached = (key, Int8WeightC(_ptr(self.codes), _ptr(self.scale), self.N, self.K))
+            self.__dict__["_c_view"] = cached
+        return cached[1]
+
+
+def quantize_int8(W: torch.Tensor, out: Int8Weight | None = None) -> Int8Weight:
+    """An fp32 or bf16 [N, K] CUDA tensor in 8-bit integers, one scale per row:
+    scale = max|row| / 127, codes the nearest integers (halves to even)."""
+    where = "qlora_quantize_int8_bf16" if W.dtype == torch.bfloat16 else "qlora_quantize_int8"
+    if W.dim() != 2 or W.dtype not in (torch.float32, torch.bfloat16):
+        raise QLoraError(-2, where, f"{W.dtype} {tuple(W.shape)}")
+    N, K = W.shape
+    _want(W, "W", where, (N, K), W.dtype, W.device)
+    if out is None:
+        out = Int8Weight(torch.empty(N, K, dtype=torch.int8, device=W.device),
+                         torch.empty(N, dtype=torch.float32, device=W.device), N, K)
+    _want(out.codes, "codes", where, (N, K), torch.int8, W.device)
+    _want(out.scale, "scale", where, (N,), torch.float32, W.device)
+    _check(_on(W.device, getattr(lib(), where), _ptr(W), N, K, _ptr(out.codes), _ptr(out.scale)), where)
+    return out
+
+
+def workspace_bytes_int8(M: int, N: int, K: int, E: int = 1) -> int:
+    """Workspace of linear_int8 (E = 1) and linear_int8_experts; N and K are one expert's."""
+    return int(lib().qlora_workspace_bytes_int8(M, N, K, E))
+
+
+def _int8_call(where, X, w, E, Y, ws, *group):
+    dev = X.device
+    if X.dim() != 2 or not 1 <= E <= 512 or w.N % E:
+        raise QLoraError(-2, where, f"X {tuple(X.shape)}, weight {w.N} x {w.K}, E = {E}")
+    M, N = X.shape[0], w.N // E
+    _want(X, "X", where, (M, w.K), torch.bfloat16, dev)
+    if w.codes.device != dev:
+        raise QLoraError(-1, where, f"the weight is on {w.codes.device}, X on {dev}")
+    Y = Y if Y is not None else torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+    _want(Y, "Y", where, (M, N), torch.bfloat16, dev)
+    ws = _ws_on(workspace_bytes_int8(M, N, w.K, E), dev, ws, where)
+    v = w.c_view()
+    _check(_on(dev, getattr(lib(), where), _ptr(X), M, ctypes.byref(v), *group, _ptr(Y), _ptr(ws), ws.numel()), where)
+    _check_on(ws, where, M)
+    return Y
+
+
+def linear_int8(X: torch.Tensor, w: Int8Weight, Y: torch.Tensor | None = None,
+                ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Y bf16 [M, N] = the rows of X (bf16 [M, K]) quantised to 8 bits with a scale
+    each, times the 8-bit weight."""
+    return _int8_call("qlora_linear_int8", X, w, 1, Y, ws)
+
+
+def linear_int8_experts(X: torch.Tensor, w: Int8Weight, offsets: torch.Tensor, E: int,
+                        Y: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """linear_int8 for rows grouped by expert (w: the experts' weights stacked,
+    E N rows; offsets: int32 [E + 1]); rows of no expert keep what Y held."""
+    where = "qlora_linear_int8_experts"
+    _want(offsets, "offsets", where, (E + 1,), torch.int32, X.device)
+    return _int8_call(where, X, w, E, Y, ws, E, _ptr(offsets))
 
 
 def device_status(ws: torch.Tensor) -> int:

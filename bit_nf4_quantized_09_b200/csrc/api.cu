@@ -13,6 +13,7 @@
 
 #include "../../include/qlora_nf4.h"
 #include "kernels.h"
+#include "tiles.cuh"
 
 using namespace qlora;
 
@@ -123,6 +124,7 @@ struct DeviceState {
     bool ready = false;
     qlora_status status = QLORA_OK;
     int sms = 0;
+    int clusters[4] = {0, 0, 0, 0};  // resident clusters of 1, 2, 4, 8 of the grouped matmuls' CTAs
 };
 std::mutex g_dev_mu;
 DeviceState g_dev[64];
@@ -131,7 +133,7 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 // Checks the current device once (sm_100, 148-SM class) and opts the big
 // kernels in to their shared-memory sizes.
-qlora_status device_ready(int* sms_out) {
+qlora_status device_ready(int* sms_out, int* clusters_out = nullptr) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -150,7 +152,10 @@ qlora_status device_ready(int* sms_out) {
                            std::to_string(minor) + ")";
             d.status = QLORA_ERR_UNSUPPORTED_DEVICE;
         } else if ((e = fused_init_device()) != cudaSuccess || (e = skinny_init_device()) != cudaSuccess ||
-                   (e = gemv_mma_init_device()) != cudaSuccess || (e = merge_tc_init_device()) != cudaSuccess) {
+                   (e = gemv_mma_init_device()) != cudaSuccess || (e = merge_tc_init_device()) != cudaSuccess ||
+                   (e = expert_gemm_init_device(d.clusters)) != cudaSuccess ||
+                   (e = expert_rank_init_device()) != cudaSuccess || (e = expert_order_init_device()) != cudaSuccess ||
+                   (e = int8_init_device()) != cudaSuccess) {
             d.status = cuda_fail(e, "cudaFuncSetAttribute");
         } else if (!g_encode) {
             void* fn = nullptr;
@@ -163,6 +168,7 @@ qlora_status device_ready(int* sms_out) {
         }
     }
     if (sms_out) *sms_out = d.sms;
+    if (clusters_out) std::copy(d.clusters, d.clusters + 4, clusters_out);
     return d.status;
 }
 
@@ -173,9 +179,10 @@ struct MapKey {
     uint64_t d0, d1, row_bytes;
     uint32_t b0, b1;
     int dt, sw;
+    uint64_t d2 = 0;  // planes of a 3-D map (row_bytes * d1 apart); 0 = 2-D
     bool operator==(const MapKey& o) const {
         return base == o.base && d0 == o.d0 && d1 == o.d1 && row_bytes == o.row_bytes && b0 == o.b0 && b1 == o.b1 &&
-               dt == o.dt && sw == o.sw;
+               dt == o.dt && sw == o.sw && d2 == o.d2;
     }
 };
 constexpr int kMapCacheSize = 64;
@@ -185,10 +192,13 @@ CUtensorMap g_map_vals[kMapCacheSize];
 bool g_map_used[kMapCacheSize] = {};
 int g_map_next = 0;
 
-// 2-D tiled tensor map over a row-major [d1, d0] array (d0 contiguous).
+// 2-D tiled tensor map over a row-major [d1, d0] array (d0 contiguous), or with
+// planes > 0 a 3-D one over [planes, d1, d0] (box one plane deep), whose reads
+// past d1 are zeros and not the next plane.
 qlora_status make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t d0, uint64_t d1,
-                      uint64_t row_bytes, uint32_t b0, uint32_t b1, CUtensorMapSwizzle sw, const char* what) {
-    const MapKey key{base, d0, d1, row_bytes, b0, b1, static_cast<int>(dt), static_cast<int>(sw)};
+                      uint64_t row_bytes, uint32_t b0, uint32_t b1, CUtensorMapSwizzle sw, const char* what,
+                      uint64_t planes = 0) {
+    const MapKey key{base, d0, d1, row_bytes, b0, b1, static_cast<int>(dt), static_cast<int>(sw), planes};
     {
         std::lock_guard<std::mutex> lk(g_map_mu);
         for (int i = 0; i < kMapCacheSize; ++i)
@@ -197,11 +207,11 @@ qlora_status make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, 
                 return QLORA_OK;
             }
     }
-    const cuuint64_t dims[2] = {d0, d1};
-    const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {b0, b1};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = g_encode(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
+    const cuuint64_t dims[3] = {d0, d1, planes};
+    const cuuint64_t strides[2] = {row_bytes, row_bytes * d1};
+    const cuuint32_t box[3] = {b0, b1, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(m, dt, planes ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
@@ -1338,3 +1348,373 @@ extern "C" qlora_status qlora_quantize_nf4_noalloc(const float* W, int64_t N, in
     void* tree = static_cast<unsigned char*>(scratch) + kNoAllocAbsmaxBytes;
     return quantize_dq(W, false, N, K, codes, qabsmax, s2, mean, absmax, tree, sms, st);
 }
+
+// ================================================== layers of experts, int8 ==
+namespace {
+
+// How a grouped matmul cuts its work. Tiles of up to 256 tokens read each
+// weight tile least often; they are taken when they are at least as many as
+// the SMs. Otherwise tiles of up to 64 tokens, and clusters of S CTAs that
+// split a tile's reduction: of S = 1, 2, 4, 8 the one with the least
+// ceil(tiles / clusters) * (steps / S + a tile's fixed cost in steps).
+struct GroupPlan {
+    int cap = 64, splits = 1, ctas = 1;
+};
+GroupPlan group_plan(int64_t M, int E, int64_t tiles_w, int64_t steps, const int clusters[4]) {
+    GroupPlan p;
+    const int64_t act = std::min<int64_t>(E, M);  // experts with rows, at most
+    const int64_t avg = cdiv(M, act);
+    const int64_t big = tiles_w * act * cdiv(avg, 256);
+    if (avg > 64 && big >= clusters[0]) {
+        p.cap = 256;
+        p.ctas = clusters[0];
+        return p;
+    }
+    const int64_t tiles = tiles_w * act * cdiv(avg, 64);
+    int64_t best = -1;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t S = int64_t(1) << i;
+        if (clusters[i] < 1 || S > steps) break;
+        const int64_t cost = cdiv(tiles, clusters[i]) * (cdiv(steps, S) + (S > 1 ? 6 : 4));
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.splits = static_cast<int>(S);
+            p.ctas = clusters[i] * static_cast<int>(S);
+        }
+    }
+    return p;
+}
+
+// M rows over E experts: 32-bit row numbers and tile numbers.
+bool rows_ok(int64_t M, int E, int64_t cols) {
+    return M <= (int64_t(1) << 30) && (M / 64 + E) * cdiv(cols, 256) < (int64_t(1) << 31);
+}
+
+// Checks the experts of a stacked weight: E N rows.
+qlora_status check_experts(int64_t rows, int E, int64_t M, const int32_t* offsets, int64_t* N) {
+    if (E < 1 || E > kMaxExperts) return QLORA_ERR_INVALID_ARG;
+    if (rows % E != 0 || (rows / E) % 8 != 0) return QLORA_ERR_BAD_SHAPE;
+    if (M < 0) return QLORA_ERR_BAD_SHAPE;
+    if (M > 0 && !offsets) return QLORA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(offsets) & 3u) return QLORA_ERR_MISALIGNED;
+    *N = rows / E;
+    return QLORA_OK;
+}
+
+struct ExpertLayout {
+    size_t status = 0, sT = 0, sU = 0, total = 0;
+};
+constexpr int kTermsT = 2, kTermsU = 3;
+ExpertLayout expert_layout(int op, int64_t M, int r) {
+    ExpertLayout L;
+    L.total = 256;
+    L.sT = L.total;
+    L.total += up256(static_cast<size_t>(M) * kTermsT * r * 2);
+    if (op == QLORA_OP_BWD) {
+        L.sU = L.total;
+        L.total += up256(static_cast<size_t>(M) * kTermsU * r * 2);
+    }
+    return L;
+}
+
+// The rows' rank-r inputs: sT (b = A) or sU (b = B) as sums of bf16 terms.
+qlora_status expert_down(bool bwd, const uint16_t* act, int64_t M, int64_t red, const uint16_t* b, int E,
+                         const int32_t* offsets, int r, float scale, int terms, uint16_t* out, int* status,
+                         cudaStream_t st) {
+    const int NR = rank_pad(r);
+    CUtensorMap ta, tb;
+    QLORA_MAP(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, red, M, red * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, "X");
+    if (bwd)
+        QLORA_MAP(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b, r, red, static_cast<uint64_t>(r) * 2, NR, 64,
+                  swizzle_for_rank(NR), "B", E);
+    else
+        QLORA_MAP(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b, red, r, red * 2, 64, NR, CU_TENSOR_MAP_SWIZZLE_128B, "A", E);
+    ExpertDownArgs a{};
+    a.offsets = offsets;
+    a.E = E;
+    a.M = M;
+    a.red = red;
+    a.r = r;
+    a.NR = NR;
+    a.terms = terms;
+    a.scale = scale;
+    a.out = out;
+    a.splits = skinny_splits(cdiv(M, 128) + std::min<int64_t>(E, M) - 1, red);
+    a.status = status;
+    a.timeout_ns = timeout_ns();
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    // an expert adds at most one partial tile
+    const int64_t tiles = M / 128 + std::min<int64_t>(E, M);
+    QLORA_LAUNCH(launch_expert_down(bwd, ta, tb, a, static_cast<int>(tiles), st), 1, "expert down-projection");
+    return QLORA_OK;
+}
+
+// Y (forward) or dX of the experts' rows.
+qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_nf4_weight* w, int64_t N, int E,
+                           const int32_t* offsets, const uint16_t* rank_in, int terms, const uint16_t* rank_w, int r,
+                           uint16_t* out, int* status, const int* clusters, bool pdl, cudaStream_t st) {
+    const int64_t K = w->K, red = dx ? N : K, cols = dx ? K : N;
+    const GroupPlan p = group_plan(M, E, cdiv(cols, 256), cdiv(red, 64), clusters);
+    const uint32_t box = p.cap == 256 ? 64 : 16;
+    CUtensorMap t_act, t_codes, t_lact, t_lw;
+    QLORA_MAP(&t_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, red, M, red * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B,
+              dx ? "dY" : "X");
+    // the first term of sT (sU): bf16 as the output is
+    QLORA_MAP(&t_lact, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_in, r, M, static_cast<uint64_t>(terms) * r * 2, 64, box,
+              CU_TENSOR_MAP_SWIZZLE_128B, dx ? "sU" : "sT");
+    if (dx) {
+        QLORA_MAP(&t_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, N, K / 2, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B,
+                  "codes", E);
+        QLORA_MAP(&t_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_w, K, r, K * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "A", E);
+    } else {
+        QLORA_MAP(&t_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, N, K / 2, 32, 256, CU_TENSOR_MAP_SWIZZLE_32B,
+                  "codes", E);
+        QLORA_MAP(&t_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_w, r, N, static_cast<uint64_t>(r) * 2, 64, 256,
+                  CU_TENSOR_MAP_SWIZZLE_128B, "B", E);
+    }
+    ExpertGemmArgs a{};
+    a.offsets = offsets;
+    a.E = E;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.out_cols = cols;
+    a.red = red;
+    a.rank_cols = r;
+    a.cap = p.cap;
+    a.splits = p.splits;
+    a.ctas = p.ctas;
+    a.c = constants_of(w);
+    a.out = out;
+    a.status = status;
+    a.timeout_ns = timeout_ns();
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    QLORA_LAUNCH(launch_expert_gemm(dx, t_act, t_codes, t_lact, t_lw, a, tables(), pdl, st), 1,
+                 dx ? "expert dX" : "expert forward");
+    return QLORA_OK;
+}
+
+constexpr int64_t kInt8MaxK = 131072;  // 127 * 127 * K < 2^31
+
+qlora_status check_int8_weight(const qlora_int8_weight* w) {
+    if (!w || !w->codes || !w->scale) return QLORA_ERR_INVALID_ARG;
+    if (w->N <= 0 || w->K <= 0 || w->N % 8 != 0 || w->K % 16 != 0 || w->K > kInt8MaxK) return QLORA_ERR_BAD_SHAPE;
+    if (!aligned16(w->codes) || !aligned16(w->scale)) return QLORA_ERR_MISALIGNED;
+    return QLORA_OK;
+}
+
+size_t int8_workspace(int64_t M, int64_t K) {
+    return 256 + up256(static_cast<size_t>(M) * K) + up256(static_cast<size_t>(M) * 4);
+}
+
+qlora_status int8_impl(const uint16_t* X, int64_t M, const qlora_int8_weight* w, int64_t N, int E, const int32_t* offsets,
+                       uint16_t* Y, void* ws, size_t ws_bytes, void* stream) {
+    if (M < 0 || !rows_ok(M, E, N)) return QLORA_ERR_BAD_SHAPE;
+    if (M == 0) return QLORA_OK;
+    if (!X || !Y || !ws) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(Y) || !aligned16(ws)) return QLORA_ERR_MISALIGNED;
+    if (ws_bytes < int8_workspace(M, w->K)) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    int sms = 0, clusters[4];
+    qlora_status s = device_ready(&sms, clusters);
+    if (s != QLORA_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    int8_t* xq = reinterpret_cast<int8_t*>(base + 256);
+    float* xs = reinterpret_cast<float*>(base + 256 + up256(static_cast<size_t>(M) * w->K));
+    const int64_t K = w->K;
+    QLORA_TRY(cudaMemsetAsync(base, 0, 256, st), "clear status");
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    QLORA_LAUNCH(launch_quantize_rows(X, true, M, K, xq, xs, st), 1, "quantise tokens");
+    const GroupPlan p = group_plan(M, E, cdiv(N, 256), cdiv(K, 128), clusters);
+    CUtensorMap tx, tw;
+    QLORA_MAP(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, p.cap == 256 ? 64 : 16, CU_TENSOR_MAP_SWIZZLE_128B,
+              "token codes");
+    QLORA_MAP(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K, N, K, 128, 256, CU_TENSOR_MAP_SWIZZLE_128B, "codes", E);
+    Int8GemmArgs a{};
+    a.offsets = offsets;
+    a.E = E;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.cap = p.cap;
+    a.splits = p.splits;
+    a.ctas = p.ctas;
+    a.xs = xs;
+    a.ws = w->scale;
+    a.Y = Y;
+    a.status = reinterpret_cast<int*>(base);
+    a.timeout_ns = timeout_ns();
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    QLORA_LAUNCH(launch_int8_gemm(tx, tw, a, true, st), 1, "int8 matmul");
+    return QLORA_OK;
+}
+
+qlora_status quantize_int8_any(const void* W, bool bf16, int64_t N, int64_t K, int8_t* codes, float* scale,
+                               void* stream) {
+    if (!W || !codes || !scale) return QLORA_ERR_INVALID_ARG;
+    if (N <= 0 || K <= 0 || K % 16 != 0 || N > 0x7FFFFFFF) return QLORA_ERR_BAD_SHAPE;
+    if (!aligned16(W) || !aligned16(codes) || !aligned16(scale)) return QLORA_ERR_MISALIGNED;
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    const qlora_status s = device_ready(nullptr);
+    if (s != QLORA_OK) return s;
+    QLORA_LAUNCH(launch_quantize_rows(W, bf16, N, K, codes, scale, static_cast<cudaStream_t>(stream)), 1, "quantise rows");
+    return QLORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qlora_status qlora_expert_order(const int32_t* ids, int64_t M, int E, int32_t* order, int32_t* offsets, void* stream) {
+    if (E < 1 || E > kMaxExperts || !offsets) return QLORA_ERR_INVALID_ARG;
+    if (M < 0 || M > (int64_t(1) << 30)) return QLORA_ERR_BAD_SHAPE;
+    if (M > 0 && (!ids || !order)) return QLORA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(ids) & 3u) || (reinterpret_cast<uintptr_t>(order) & 3u) ||
+        (reinterpret_cast<uintptr_t>(offsets) & 3u))
+        return QLORA_ERR_MISALIGNED;
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    const qlora_status s = device_ready(nullptr);
+    if (s != QLORA_OK) return s;
+    QLORA_LAUNCH(launch_expert_order(ids, static_cast<int>(M), E, order, offsets, static_cast<cudaStream_t>(stream)), 1,
+                 "expert order");
+    return QLORA_OK;
+}
+
+size_t qlora_workspace_bytes_experts(int op, int64_t M, int64_t N, int64_t K, int r, int E) {
+    if (N <= 0 || N % 8 != 0 || K <= 0 || K % kBlock != 0 || E < 1 || E > kMaxExperts) return 0;
+    if ((op != QLORA_OP_FWD && op != QLORA_OP_BWD) || M < 0 || !rank_ok(r) || !rows_ok(M, E, std::max(N, K))) return 0;
+    return expert_layout(op, M, r).total;
+}
+
+qlora_status qlora_linear_fwd_experts(const uint16_t* X, int64_t M, const qlora_nf4_weight* w, int E,
+                                      const int32_t* offsets, const uint16_t* A, const uint16_t* B, int r, float alpha,
+                                      uint16_t* Y, uint16_t* sT_save, void* ws, size_t ws_bytes, void* stream) {
+    qlora_status s = check_weight(w);
+    if (s != QLORA_OK) return s;
+    int64_t N = 0;
+    if ((s = check_experts(w->N, E, M, offsets, &N)) != QLORA_OK) return s;
+    if (!rank_ok(r)) return QLORA_ERR_UNSUPPORTED_RANK;
+    if (!std::isfinite(alpha)) return QLORA_ERR_INVALID_ARG;
+    if (!rows_ok(M, E, std::max(N, w->K))) return QLORA_ERR_BAD_SHAPE;
+    if (M == 0) return QLORA_OK;
+    if (!X || !A || !B || !Y || !ws) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || !aligned16(ws) ||
+        (sT_save && !aligned16(sT_save)))
+        return QLORA_ERR_MISALIGNED;
+    const ExpertLayout L = expert_layout(QLORA_OP_FWD, M, r);
+    if (ws_bytes < L.total) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    int sms = 0, clusters[4];
+    if ((s = device_ready(&sms, clusters)) != QLORA_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    int* status = reinterpret_cast<int*>(base);
+    uint16_t* sT = sT_save ? sT_save : reinterpret_cast<uint16_t*>(base + L.sT);
+    QLORA_TRY(cudaMemsetAsync(base, 0, 256, st), "clear status");
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    if ((s = expert_down(false, X, M, w->K, A, E, offsets, r, alpha / static_cast<float>(r), kTermsT, sT, status, st)) !=
+        QLORA_OK)
+        return s;
+    return expert_matmul(false, X, M, w, N, E, offsets, sT, kTermsT, B, r, Y, status, clusters, true, st);
+}
+
+qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int64_t M, const qlora_nf4_weight* w, int E,
+                                      const int32_t* offsets, const uint16_t* A, const uint16_t* B, int r, float alpha,
+                                      const uint16_t* sT_in, uint16_t* dX, float* dA, float* dB, void* ws,
+                                      size_t ws_bytes, void* stream) {
+    qlora_status s = check_weight(w);
+    if (s != QLORA_OK) return s;
+    int64_t N = 0;
+    if ((s = check_experts(w->N, E, M, offsets, &N)) != QLORA_OK) return s;
+    if (!rank_ok(r)) return QLORA_ERR_UNSUPPORTED_RANK;
+    if (!std::isfinite(alpha)) return QLORA_ERR_INVALID_ARG;
+    if (!rows_ok(M, E, std::max(N, w->K))) return QLORA_ERR_BAD_SHAPE;
+    if (!A || !B || !dA || !dB || !ws || (M > 0 && (!dY || !X || !dX))) return QLORA_ERR_INVALID_ARG;
+    if ((M > 0 && (!aligned16(dY) || !aligned16(X) || !aligned16(dX))) || !aligned16(A) || !aligned16(B) ||
+        !aligned16(dA) || !aligned16(dB) || !aligned16(ws) || (sT_in && !aligned16(sT_in)))
+        return QLORA_ERR_MISALIGNED;
+    const ExpertLayout L = expert_layout(QLORA_OP_BWD, M, r);
+    if (ws_bytes < L.total) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    int sms = 0, clusters[4];
+    if ((s = device_ready(&sms, clusters)) != QLORA_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t K = w->K;
+    if (M == 0) {  // an empty batch: the adapter gradients are exactly zero
+        QLORA_TRY(cudaMemsetAsync(dA, 0, static_cast<size_t>(E) * r * K * 4, st), "zero dA");
+        QLORA_TRY(cudaMemsetAsync(dB, 0, static_cast<size_t>(E) * N * r * 4, st), "zero dB");
+        return QLORA_OK;
+    }
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    int* status = reinterpret_cast<int*>(base);
+    uint16_t* sU = reinterpret_cast<uint16_t*>(base + L.sU);
+    const uint16_t* sT = sT_in ? sT_in : reinterpret_cast<uint16_t*>(base + L.sT);
+    const float scale = alpha / static_cast<float>(r);
+    QLORA_TRY(cudaMemsetAsync(base, 0, 256, st), "clear status");
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    if (!sT_in && (s = expert_down(false, X, M, K, A, E, offsets, r, scale, kTermsT, reinterpret_cast<uint16_t*>(base + L.sT),
+                                   status, st)) != QLORA_OK)
+        return s;
+    if ((s = expert_down(true, dY, M, N, B, E, offsets, r, scale, kTermsU, sU, status, st)) != QLORA_OK) return s;
+    if ((s = expert_matmul(true, dY, M, w, N, E, offsets, sU, kTermsU, A, r, dX, status, clusters, false, st)) != QLORA_OK)
+        return s;
+    // dA and dB need only sU and sT: as dX's programmatic dependent their CTAs
+    // start on the SMs that dX leaves idle
+    const int NR = rank_pad(r);
+    CUtensorMap tx, tdy, tsu, tst;
+    QLORA_MAP(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, K, M, K * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "X^T");
+    QLORA_MAP(&tdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, N, M, N * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "dY^T");
+    if ((s = make_rank_map(&tsu, sU, M, kTermsU * r, kTermsU * r, NR, "sU")) != QLORA_OK) return s;
+    if ((s = make_rank_map(&tst, sT, M, kTermsT * r, kTermsT * r, NR, "sT")) != QLORA_OK) return s;
+    ExpertGradArgs g{};
+    g.offsets = offsets;
+    g.E = E;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.r = r;
+    g.NR = NR;
+    g.terms_u = kTermsU;
+    g.terms_t = kTermsT;
+    g.dA = dA;
+    g.dB = dB;
+    g.status = status;
+    g.timeout_ns = timeout_ns();
+    if (injected_failure()) return QLORA_ERR_CUDA;
+    QLORA_LAUNCH(launch_expert_grads(tx, tdy, tsu, tst, g, true, st), 1, "expert gradients");
+    return QLORA_OK;
+}
+
+qlora_status qlora_quantize_int8(const float* W, int64_t N, int64_t K, int8_t* codes, float* scale, void* stream) {
+    return quantize_int8_any(W, false, N, K, codes, scale, stream);
+}
+
+qlora_status qlora_quantize_int8_bf16(const uint16_t* W, int64_t N, int64_t K, int8_t* codes, float* scale,
+                                      void* stream) {
+    return quantize_int8_any(W, true, N, K, codes, scale, stream);
+}
+
+size_t qlora_workspace_bytes_int8(int64_t M, int64_t N, int64_t K, int E) {
+    if (N <= 0 || N % 8 != 0 || K <= 0 || K % 16 != 0 || K > kInt8MaxK || E < 1 || E > kMaxExperts) return 0;
+    if (M < 0 || !rows_ok(M, E, N)) return 0;
+    return int8_workspace(M, K);
+}
+
+qlora_status qlora_linear_int8(const uint16_t* X, int64_t M, const qlora_int8_weight* w, uint16_t* Y, void* ws,
+                               size_t ws_bytes, void* stream) {
+    const qlora_status s = check_int8_weight(w);
+    if (s != QLORA_OK) return s;
+    return int8_impl(X, M, w, w->N, 1, nullptr, Y, ws, ws_bytes, stream);
+}
+
+qlora_status qlora_linear_int8_experts(const uint16_t* X, int64_t M, const qlora_int8_weight* w, int E,
+                                       const int32_t* offsets, uint16_t* Y, void* ws, size_t ws_bytes, void* stream) {
+    qlora_status s = check_int8_weight(w);
+    if (s != QLORA_OK) return s;
+    int64_t N = 0;
+    if ((s = check_experts(w->N, E, M, offsets, &N)) != QLORA_OK) return s;
+    return int8_impl(X, M, w, N, E, offsets, Y, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

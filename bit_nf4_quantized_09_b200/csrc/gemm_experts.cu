@@ -1,0 +1,621 @@
+// Dequant-fused NF4 matmuls over rows grouped by expert (tcgen05 + TMEM + TMA).
+//
+//   forward:  Y[m]  = X[m] . deq(W_e)^T + sT[m] . B_e^T     W_e: [N, K]
+//   dX:       dX[m] = dY[m] . deq(W_e)  + sU[m] . A_e       for the rows m of expert e
+//
+// The experts' weights are one NF4 weight of E N rows; a stack of frozen 4-bit
+// experts, each with an adapter, is QLoRA's layer with the weight chosen per
+// token ("ta-paperlens QLoRA explainer", 勾配は実際どこへ行くのか: every matmul
+// restores the 4-bit blocks it needs to BF16 on the spot).
+//
+// Operands. The weight is the UMMA's M side (two M = 128 halves: 256 output
+// columns) and the tokens its N side (16 to 256, a multiple of 16), so a tile
+// costs what its expert's rows cost and not a padded 256: an expert with 40
+// rows runs N = 48. The 64-column rank-r term (sT . B_e^T, sU . A_e) is one
+// more reduction step of the same accumulators, its operands loaded by TMA.
+//
+// Roles of a persistent CTA (one per SM, 20 warps):
+//   warps 0-15  dequantisers in two groups of eight that take the reduction
+//               steps in turn (one 64-weight block per thread, the exact
+//               w_hat = bf16(level c'), through the per-block byte tables);
+//               then the epilogue
+//   warp 16     TMA producer of the token tiles
+//   warp 17     TMA producer of the packed codes
+//   warp 18     TMEM owner, UMMA issuer
+//   warp 19     block constants c' (E4M3 code, second-level scale, mean, or the
+//               fp32 constant) straight from the stored form, four reduction
+//               steps at a time; no transposed copy of an expert stack's
+//               constants is written, most of which few tokens would not use
+//
+// Few tokens. With fewer tiles than SMs a cluster of S CTAs shares a tile,
+// each taking 1/S of the reduction; the partial sums (at most 64 tokens x 256
+// columns fp32) are added in rank order through distributed shared memory and
+// written by all S CTAs. Every sum has a fixed order: results are bitwise
+// reproducible.
+#include "kernels.h"
+#include "tiles.cuh"
+
+namespace qlora {
+
+namespace {
+
+constexpr int kDeqWarps = 16;
+constexpr int kGroupWarps = 8;
+constexpr int kWarpX = 16, kWarpC = 17, kWarpMma = 18, kWarpK = 19;
+constexpr int kThreads = (kWarpK + 1) * 32;
+constexpr int kPW = 3;                       // weight stages
+constexpr uint32_t kWStage = 256 * 64 * 2;   // 32 KB
+constexpr uint32_t kCStage = 256 * 64 / 2;   // 8 KB of packed codes
+constexpr uint32_t kKStage = 1024;           // 256 block constants
+constexpr uint32_t kTmemCols = 512;
+
+// Shared memory by token capacity: 256 tokens leave room for two code stages;
+// with at most 64 the token ring shrinks and the codes run eight steps ahead.
+template <int CAP>
+struct Lay {
+    static constexpr int kPX = CAP == 256 ? 3 : 4;
+    static constexpr int kPC = CAP == 256 ? 2 : 8;
+    static constexpr int kPK = CAP == 256 ? 8 : 16;
+    static constexpr int kBoxRows = CAP == 256 ? 64 : 16;  // token rows per TMA box
+    static constexpr uint32_t kXStage = CAP * 128;
+    static constexpr uint32_t kOffW = kPX * kXStage;
+    static constexpr uint32_t kOffC = kOffW + kPW * kWStage;
+    static constexpr uint32_t kOffK = kOffC + kPC * kCStage;
+    static constexpr uint32_t kOffSched = kOffK + kPK * kKStage;
+    static constexpr uint32_t kOffBar = (kOffSched + sizeof(TileSched) + 63) / 64 * 64;
+    static constexpr uint32_t kBytes = kOffBar + 640 + 1024;
+};
+static_assert(Lay<256>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "shared memory of one CTA");
+static_assert(kPW * kWStage >= 64 * 256 * 4, "partial sums of 64 tokens fit the weight stages");
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// The reduction steps of this CTA: split rank c of S takes [c KT / S, (c + 1) KT / S).
+struct Range {
+    int lo, hi;
+};
+__device__ __forceinline__ Range split_range(int KT, int S, int c) {
+    return Range{static_cast<int>(static_cast<int64_t>(c) * KT / S), static_cast<int>(static_cast<int64_t>(c + 1) * KT / S)};
+}
+
+template <bool kTransW, bool kNoDq, int CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_gemm(const __grid_constant__ CUtensorMap tm_act, const __grid_constant__ CUtensorMap tm_codes,
+                const __grid_constant__ CUtensorMap tm_lact, const __grid_constant__ CUtensorMap tm_lw,
+                const ExpertGemmArgs a, const Nf4Tables tab) {
+    using L = Lay<CAP>;
+    asm volatile("griddepcontrol.launch_dependents;");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    TileSched& sched = *reinterpret_cast<TileSched*>(smem + L::kOffSched);
+    uint64_t* x_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+    uint64_t* x_empty = x_full + L::kPX;
+    uint64_t* w_full = x_empty + L::kPX;
+    uint64_t* w_empty = w_full + kPW;
+    uint64_t* c_full = w_empty + kPW;
+    uint64_t* c_empty = c_full + L::kPC;
+    uint64_t* k_full = c_empty + L::kPC;
+    uint64_t* k_empty = k_full + L::kPK;
+    uint64_t* acc = k_empty + L::kPK;
+    uint64_t* tmem_free = acc + 1;
+    uint64_t* drain = tmem_free + 1;
+    uint64_t* red_full = drain + 1;
+    uint64_t* red_done = red_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(red_done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((2 * L::kPX + 2 * kPW + 2 * L::kPC + 2 * L::kPK + 5) * 8 + 8 <= 640, "barriers");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = a.splits;
+    const int crank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int cl = static_cast<int>(blockIdx.x) / S, ncl = static_cast<int>(gridDim.x) / S;
+    const int KT = static_cast<int>((a.red + 63) / 64);
+    const Range kr = split_range(KT, S, crank);
+    const int nk = kr.hi - kr.lo;
+    const int steps = nk + (crank == S - 1 ? 1 : 0);  // the last split also runs the rank-r step
+    const int tiles_w = static_cast<int>((a.out_cols + 255) / 256);
+    const uint64_t tmo = a.timeout_ns;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::kPX; ++s) {
+            mbar_init(x_full + s, 1);
+            mbar_init(x_empty + s, 1);
+        }
+        for (int s = 0; s < kPW; ++s) {
+            mbar_init(w_full + s, kGroupWarps);
+            mbar_init(w_empty + s, 1);
+        }
+        for (int s = 0; s < L::kPC; ++s) {
+            mbar_init(c_full + s, 1);
+            mbar_init(c_empty + s, kGroupWarps);
+        }
+        for (int s = 0; s < L::kPK; ++s) {
+            mbar_init(k_full + s, 32);
+            mbar_init(k_empty + s, kGroupWarps);
+        }
+        mbar_init(acc, 1);
+        mbar_init(tmem_free, kDeqWarps);
+        mbar_init(drain, 1);
+        mbar_init(red_full, kDeqWarps * S);
+        mbar_init(red_done, kDeqWarps * S);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == kWarpX && lane == 0) {
+        tma_prefetch_desc(&tm_act);
+        tma_prefetch_desc(&tm_lact);
+        tma_prefetch_desc(&tm_codes);
+        tma_prefetch_desc(&tm_lw);
+    }
+    build_sched(sched, a.offsets, a.E, static_cast<int>(a.M), CAP);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (S > 1) cluster_sync();  // every CTA's barriers are initialised before remote arrivals
+    const uint32_t tmem = *tmem_slot;
+    TileIter it(sched, cl, ncl, tiles_w, a.E);
+    Tile tl;
+
+    if (warp == kWarpX) {
+        // ------------------------------------------- token-tile producer --
+        if (lane == 0) {
+            int g = 0;
+            bool waited = false, ok = true;
+            while (ok && it.next(tl)) {
+                const int boxes = (tl.rows + L::kBoxRows - 1) / L::kBoxRows;
+                for (int i = 0; i < steps; ++i, ++g) {
+                    const int s = g % L::kPX;
+                    if (g >= L::kPX && !mbar_wait(x_empty + s, static_cast<uint32_t>(g / L::kPX - 1) & 1u, tmo, a.status)) {
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                    if (*abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    const bool rank = i >= nk;
+                    if (rank && !waited) {
+                        // sT or sU of the preceding launch, of which this one
+                        // may be a programmatic dependent
+                        asm volatile("griddepcontrol.wait;" ::: "memory");
+                        waited = true;
+                    }
+                    uint8_t* st = smem + s * L::kXStage;
+                    mbar_arrive_expect_tx(x_full + s, static_cast<uint32_t>(boxes) * L::kBoxRows * 128u);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d(st + b * L::kBoxRows * 128, rank ? &tm_lact : &tm_act, x_full + s,
+                                    rank ? 0 : (kr.lo + i) * 64, tl.row0 + b * L::kBoxRows);
+                }
+            }
+            for (int j = max(0, g - L::kPX); j < g; ++j)
+                mbar_wait(x_full + j % L::kPX, static_cast<uint32_t>(j / L::kPX) & 1u, tmo, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == kWarpC) {
+        // ------------------------------------------------- code producer --
+        if (lane == 0) {
+            int g = 0;
+            bool ok = true;
+            while (ok && it.next(tl)) {
+                for (int i = 0; i < nk; ++i, ++g) {
+                    const int s = g % L::kPC;
+                    if (g >= L::kPC && !mbar_wait(c_empty + s, static_cast<uint32_t>(g / L::kPC - 1) & 1u, tmo, a.status)) {
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                    if (*abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    const int kt = kr.lo + i;
+                    mbar_arrive_expect_tx(c_full + s, kCStage);
+                    // rows past the expert's N and columns past K read as zeros
+                    if (!kTransW)
+                        tma_load_3d(smem + L::kOffC + s * kCStage, &tm_codes, c_full + s, kt * 32, tl.w0, tl.e);
+                    else
+                        tma_load_3d(smem + L::kOffC + s * kCStage, &tm_codes, c_full + s, tl.w0 / 2, kt * 64, tl.e);
+                }
+            }
+            for (int j = max(0, g - L::kPC); j < g; ++j)
+                mbar_wait(c_full + j % L::kPC, static_cast<uint32_t>(j / L::kPC) & 1u, tmo, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        // ----------------------------------------------------------- MMA --
+        if (lane == 0) {
+            int g = 0, n = 0;
+            bool ok = true;
+            while (ok && it.next(tl)) {
+                if (n > 0 && !mbar_wait(tmem_free, static_cast<uint32_t>(n - 1) & 1u, tmo, a.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t idesc = idesc_bf16(128, (tl.rows + 15) & ~15, kTransW, false);
+                for (int i = 0; i < steps; ++i, ++g) {
+                    const int sx = g % L::kPX, sw = g % kPW;
+                    if (!mbar_wait(x_full + sx, static_cast<uint32_t>(g / L::kPX) & 1u, tmo, a.status) ||
+                        !mbar_wait(w_full + sw, static_cast<uint32_t>(g / kPW) & 1u, tmo, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t xt = smem_u32(smem + sx * L::kXStage);
+                    const uint32_t wt = smem_u32(smem + L::kOffW + sw * kWStage);
+                    const int ksub = i < nk ? 4 : (a.rank_cols + 15) / 16;
+                    for (int kk = 0; kk < ksub; ++kk) {
+                        const uint64_t xd = sw128_desc(xt + kk * 32, 16, 1024);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint64_t wd = kTransW ? sw128_desc(wt + h * 16384 + kk * 2048, 8192, 1024)
+                                                        : sw128_desc(wt + h * 16384 + kk * 32, 16, 1024);
+                            umma_f16(tmem + h * 256, wd, xd, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+                        }
+                    }
+                    umma_commit(x_empty + sx);
+                    umma_commit(w_empty + sw);
+                }
+                if (ok) umma_commit(acc);
+                ++n;
+            }
+            if (!ok) *abort_flag = 1;
+            // no UMMA in flight when the TMEM is freed
+            umma_commit(drain);
+            mbar_wait(drain, 0u, tmo, nullptr);
+        }
+        __syncwarp();
+    } else if (warp >= kWarpK) {
+        // ----------------------------------------------- block constants --
+        // super-step ss: reduction steps 4 ss .. 4 ss + 3, 256 items of four
+        // constants: forward, item = weight row, four consecutive k-blocks;
+        // dX, item = reduction row, the tile's four k-blocks
+        const int KB = static_cast<int>(a.K / kBlock);
+        const bool vec = KB % 4 == 0;  // an item's constants are one aligned word (float4) of one group
+        const float mean = kNoDq ? 0.0f : __ldg(a.c.mean);
+        int g = 0;
+        bool ok = true;
+        while (ok && it.next(tl)) {
+            const int64_t erow = static_cast<int64_t>(tl.e) * a.N;
+            for (int ss = kr.lo >> 2; ok && ss <= (kr.hi - 1) >> 2; ++ss) {
+                const int k0 = max(4 * ss, kr.lo), k1 = min(4 * ss + 4, kr.hi);
+                float v[8][4];
+                const int kb0 = kTransW ? tl.w0 / kBlock : 4 * ss;
+                const int n0 = kTransW ? ss * 256 : tl.w0;
+                if (vec) {
+                    uint32_t qw[8];
+                    float sv[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int n = min(n0 + lane + 32 * j, static_cast<int>(a.N) - 1);
+                        const int64_t ib = (erow + n) * KB + kb0;
+                        if (kNoDq) {
+                            const float4 f = __ldg(reinterpret_cast<const float4*>(a.c.absmax + ib));
+                            v[j][0] = f.x;
+                            v[j][1] = f.y;
+                            v[j][2] = f.z;
+                            v[j][3] = f.w;
+                        } else {
+                            qw[j] = __ldg(reinterpret_cast<const uint32_t*>(a.c.qabsmax + ib));
+                            sv[j] = __ldg(a.c.s2 + (ib >> 8));
+                        }
+                    }
+                    if (!kNoDq) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) v[j][b] = __fmaf_rn(e4m3_to_f32(qw[j] >> (8 * b)), sv[j], mean);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int n = min(n0 + lane + 32 * j, static_cast<int>(a.N) - 1);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const int64_t ib = (erow + n) * KB + min(kb0 + b, KB - 1);
+                            v[j][b] = kNoDq ? __ldg(a.c.absmax + ib)
+                                            : __fmaf_rn(e4m3_to_f32(__ldg(a.c.qabsmax + ib)), __ldg(a.c.s2 + (ib >> 8)), mean);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int st = 0; st < 4; ++st) {
+                    const int kt = 4 * ss + st;
+                    if (kt < k0 || kt >= k1 || !ok) continue;
+                    const int s = g % L::kPK;
+                    if (g >= L::kPK &&
+                        !__all_sync(0xFFFFFFFFu, mbar_wait_sleep(k_empty + s, static_cast<uint32_t>(g / L::kPK - 1) & 1u, tmo,
+                                                                 a.status))) {
+                        *abort_flag = 1;
+                        ok = false;
+                        continue;
+                    }
+                    if (__any_sync(0xFFFFFFFFu, *abort_flag)) {
+                        ok = false;
+                        continue;
+                    }
+                    float* cs = reinterpret_cast<float*>(smem + L::kOffK + s * kKStage);
+                    if (!kTransW) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) cs[lane + 32 * j] = v[j][st];
+                    } else {
+                        // reduction row 64 kt + nl; rows past N weigh nothing
+#pragma unroll
+                        for (int jj = 0; jj < 2; ++jj) {
+                            const int nl = lane + 32 * jj;
+                            const bool live = kt * 64 + nl < a.N;
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) cs[b * 64 + nl] = live ? v[2 * st + jj][b] : 0.0f;
+                        }
+                    }
+                    mbar_arrive(k_full + s);
+                    ++g;
+                }
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+        }
+    } else {
+        // ---------------------------------------- dequantise, then epilogue --
+        const int G = warp >> 3;
+        const int t = threadIdx.x & 255;  // the thread's 64-weight block of a step
+        const bool leader = t == 0;
+        const int q = warp & 3, h = (warp >> 2) & 1;
+        bool ok = true;
+        int g = 0, gk = 0, n = 0;
+        while (ok && it.next(tl)) {
+            for (int i = 0; ok && i < steps; ++i, ++g) {
+                const int gk_i = gk;
+                if (i < nk) ++gk;
+                if ((g & 1) != G) continue;
+                const int sw = g % kPW;
+                if (g >= kPW)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(w_empty + sw, static_cast<uint32_t>(g / kPW - 1) & 1u, tmo, a.status));
+                if (!ok) break;
+                uint8_t* wst = smem + L::kOffW + sw * kWStage;
+                if (i < nk) {
+                    const int sc = gk_i % L::kPC, sk = gk_i % L::kPK;
+                    ok = __all_sync(0xFFFFFFFFu,
+                                    mbar_wait(k_full + sk, static_cast<uint32_t>(gk_i / L::kPK) & 1u, tmo, a.status) &&
+                                        mbar_wait(c_full + sc, static_cast<uint32_t>(gk_i / L::kPC) & 1u, tmo, a.status));
+                    if (!ok) break;
+                    const uint32_t codes = smem_u32(smem + L::kOffC + sc * kCStage);
+                    const float* cs = reinterpret_cast<const float*>(smem + L::kOffK + sk * kKStage);
+                    const float cprime = cs[t];
+                    uint32_t c0, c1, dst, swz;
+                    if (!kTransW) {
+                        // row t of the weight tile: 32 code bytes, 32-byte swizzle
+                        const uint32_t crow = codes + t * 32, s32 = (t >> 2) & 1;
+                        c0 = crow + ((0 ^ s32) << 4);
+                        c1 = crow + ((1 ^ s32) << 4);
+                        dst = smem_u32(wst) + t * 128;
+                        swz = t & 7;
+                    } else {
+                        // reduction row nl, k-block b of the tile's four
+                        const uint32_t nl = t & 63, b = t >> 6;
+                        const uint32_t crow = codes + nl * 128;
+                        swz = nl & 7;
+                        c0 = crow + (((2 * b) ^ swz) << 4);
+                        c1 = crow + (((2 * b + 1) ^ swz) << 4);
+                        dst = smem_u32(wst) + b * 8192 + (nl >> 3) * 1024 + (nl & 7) * 128;
+                    }
+                    const uint4 ca = lds128(c0), cb = lds128(c1);
+                    const Nf4BlockLut lut = make_block_lut(tab.level, cprime);
+                    __syncwarp();
+                    if (lane == 0) {  // codes and constants have been read
+                        mbar_arrive(c_empty + sc);
+                        mbar_arrive(k_empty + sk);
+                    }
+                    const uint32_t words[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint32_t o[4];
+                        lut_decode8_sx(lut, words[j], o);
+                        sts128(dst + ((static_cast<uint32_t>(j) ^ swz) << 4), o);
+                    }
+                    fence_proxy_async_smem();  // -> visible to the tensor core
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(w_full + sw);
+                } else {
+                    // rank-r step: B_e rows (forward) or A_e columns (dX) by TMA
+                    if (leader) {
+                        mbar_arrive_expect_tx(w_full + sw, kWStage);
+                        if (!kTransW) {
+                            tma_load_3d(wst, &tm_lw, w_full + sw, 0, tl.w0, tl.e);
+                        } else {
+                            for (int b = 0; b < 4; ++b)
+                                tma_load_3d(wst + b * 8192, &tm_lw, w_full + sw, tl.w0 + 64 * b, 0, tl.e);
+                        }
+                    } else if (lane == 0) {
+                        mbar_arrive(w_full + sw);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) break;
+
+            // ------------------------------------------------ epilogue --
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc, static_cast<uint32_t>(n) & 1u, tmo, a.status));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * 256;
+            const int nl = h * 128 + q * 32 + lane;  // tile row (output column) of this lane
+            if (S == 1) {
+                // lane = output column, register = token: two neighbouring
+                // lanes swap halves of a token pair, so each lane stores two
+                // consecutive columns of one token and a warp instruction
+                // covers two 64-byte row segments
+                const int col = tl.w0 + (nl & ~1);
+                const bool col_ok = col < a.out_cols;
+                for (int c = G * 32; c < tl.rows; c += 64) {
+                    uint32_t r[32];
+                    tmem_ld32(trow + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const uint32_t give = (lane & 1) ? r[i] : r[i + 1];
+                        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+                        const uint32_t lo = (lane & 1) ? got : r[i], hi = (lane & 1) ? r[i + 1] : got;
+                        const int tok = c + i + (lane & 1);
+                        if (col_ok && tok < tl.rows)
+                            *reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(tl.row0 + tok) * a.out_cols + col) =
+                                pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tmem_free);
+            } else {
+                // partial sums into the weight stages (idle until the next
+                // tile: every UMMA that reads them has completed, and only
+                // these warps refill them)
+                float* buf = reinterpret_cast<float*>(smem + L::kOffW);
+                for (int c = G * 32; c < tl.rows; c += 64) {
+                    uint32_t r[32];
+                    tmem_ld32(trow + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i < tl.rows) buf[(c + i) * 256 + nl] = __uint_as_float(r[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(tmem_free);
+                    for (int s = 0; s < S; ++s) mbar_arrive_remote(mapa_shared(smem_u32(red_full), s));
+                }
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(red_full, static_cast<uint32_t>(n) & 1u, tmo, a.status));
+                if (!ok) break;
+                // CTA c adds columns [c 256 / S, (c + 1) 256 / S) in rank order
+                const int per4 = 64 / S;  // four-column items per token
+                const uint32_t buf0 = smem_u32(buf);
+                for (int item = threadIdx.x; item < tl.rows * per4; item += kDeqWarps * 32) {
+                    const int tok = item / per4, nc = crank * (256 / S) + 4 * (item % per4);
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int s = 0; s < S; ++s) {
+                        const float4 x = ld_cluster_f4(mapa_shared(buf0 + static_cast<uint32_t>(tok * 256 + nc) * 4u, s));
+                        v.x += x.x;
+                        v.y += x.y;
+                        v.z += x.z;
+                        v.w += x.w;
+                    }
+                    if (tl.w0 + nc < a.out_cols)
+                        *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(tl.row0 + tok) * a.out_cols + tl.w0 + nc) =
+                            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                }
+                __syncwarp();
+                if (lane == 0)
+                    for (int s = 0; s < S; ++s) mbar_arrive_remote(mapa_shared(smem_u32(red_done), s));
+                // the weight stages are free once every CTA has read them
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(red_done, static_cast<uint32_t>(n) & 1u, tmo, a.status));
+            }
+            ++n;
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            // a rank-r tile may still be landing in a weight stage
+            if (leader && g >= 1)
+                for (int j = max(0, g - kPW); j <= g; ++j)
+                    if ((j & 1) == G) mbar_wait(w_full + j % kPW, static_cast<uint32_t>(j / kPW) & 1u, tmo, nullptr);
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (S > 1) cluster_sync();  // no CTA leaves while another may read its shared memory
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+    // launched as a programmatic dependent, the grid completes only after its primary
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <bool kTransW, bool kNoDq, int CAP>
+cudaError_t launch_one(const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact, const CUtensorMap& lw,
+                       const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Lay<CAP>::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, expert_gemm<kTransW, kNoDq, CAP>, act, codes, lact, lw, a, tab);
+}
+
+template <bool kTransW>
+cudaError_t launch_dir(const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact, const CUtensorMap& lw,
+                       const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl, cudaStream_t st) {
+    if (a.c.absmax)
+        return a.cap == 256 ? launch_one<kTransW, true, 256>(act, codes, lact, lw, a, tab, pdl, st)
+                            : launch_one<kTransW, true, 64>(act, codes, lact, lw, a, tab, pdl, st);
+    return a.cap == 256 ? launch_one<kTransW, false, 256>(act, codes, lact, lw, a, tab, pdl, st)
+                        : launch_one<kTransW, false, 64>(act, codes, lact, lw, a, tab, pdl, st);
+}
+
+template <bool kTransW, bool kNoDq>
+cudaError_t opt_in() {
+    cudaError_t e = cudaFuncSetAttribute(expert_gemm<kTransW, kNoDq, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Lay<256>::kBytes));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(expert_gemm<kTransW, kNoDq, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Lay<64>::kBytes));
+}
+
+}  // namespace
+
+cudaError_t expert_gemm_init_device(int clusters_out[4]) {
+    cudaError_t e;
+    if ((e = opt_in<false, false>()) != cudaSuccess || (e = opt_in<false, true>()) != cudaSuccess ||
+        (e = opt_in<true, false>()) != cudaSuccess || (e = opt_in<true, true>()) != cudaSuccess)
+        return e;
+    // clusters of 1, 2, 4 and 8 CTAs (one CTA per SM) that run at the same time
+    for (int i = 0; i < 4; ++i) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(1u << i);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Lay<64>::kBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << i;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if ((e = cudaOccupancyMaxActiveClusters(&clusters_out[i], expert_gemm<false, false, 64>, &cfg)) != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_expert_gemm(bool trans_w, const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact,
+                               const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl,
+                               cudaStream_t st) {
+    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 1 || a.ctas % a.splits != 0 || (a.cap != 64 && a.cap != 256))
+        return cudaErrorInvalidValue;
+    if (a.splits != 1 && (a.cap != 64 || (a.splits != 2 && a.splits != 4 && a.splits != 8))) return cudaErrorInvalidValue;
+    if (a.splits > (a.red + 63) / 64 || a.rank_cols < 1 || a.rank_cols > 64) return cudaErrorInvalidValue;
+    return trans_w ? launch_dir<true>(act, codes, lact, lw, a, tab, pdl, st)
+                   : launch_dir<false>(act, codes, lact, lw, a, tab, pdl, st);
+}
+
+}  // namespace qlora

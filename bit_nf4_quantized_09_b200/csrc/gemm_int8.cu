@@ -1,0 +1,467 @@
+// Matrix product in 8-bit integers on tcgen05 (kind::i8), dense or grouped by
+// expert:
+//
+//   Y[m, n] = bf16( xs[m] ws[n] sum_k qx[m, k] qw[n, k] )
+//
+// qx, xs: the token's row quantised by quantize_rows (one scale per token);
+// qw, ws: the weight's (one scale per output channel). This is how the 16-bit
+// weight an adapter was merged into is served in fewer bits ("ta-paperlens
+// QLoRA explainer", 落とし穴: merging into the 4-bit weight loses the update).
+// The int32 sums are exact (K <= 131072 keeps |sum| < 2^31); the only
+// roundings are the scales' product, one fp32 product and the bf16 result.
+//
+// The weight is the UMMA's M side (two M = 128 halves), the tokens its N side
+// (16 .. 256), as in the NF4 expert matmul, so ragged experts and single
+// tokens pay for the tokens they have. Persistent CTAs, one per SM:
+//   warps 0-7  epilogue (lane = output channel, register = token)
+//   warp 8     TMA producer of token codes (waits for the quantiser's launch,
+//              of which this one is the programmatic dependent)
+//   warp 9     TMA producer of weight codes (starts at once)
+//   warp 10    TMEM owner, UMMA issuer
+// With fewer tiles than SMs a cluster of S CTAs splits the reduction of a
+// tile and adds the int32 partial sums through distributed shared memory.
+#include "kernels.h"
+#include "tiles.cuh"
+
+namespace qlora {
+
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kWarpX = 8, kWarpW = 9, kWarpMma = 10;
+constexpr int kThreads = 352;
+constexpr uint32_t kWStage = 256 * 128;  // 32 KB: 256 channels x 128 codes
+constexpr uint32_t kTmemCols = 512;
+
+template <int CAP>
+struct Lay {
+    static constexpr int kStages = 3;
+    static constexpr int kBoxRows = CAP == 256 ? 64 : 16;
+    static constexpr uint32_t kXStage = CAP * 128;
+    static constexpr uint32_t kOffW = kStages * kXStage;
+    static constexpr uint32_t kOffRed = kOffW + kStages * kWStage;
+    static constexpr uint32_t kRed = CAP == 64 ? 64 * 256 * 4 : 0;  // int32 partial sums of a split
+    static constexpr uint32_t kOffXs = kOffRed + kRed;
+    static constexpr uint32_t kOffSched = kOffXs + 1024;
+    static constexpr uint32_t kOffBar = (kOffSched + sizeof(TileSched) + 63) / 64 * 64;
+    static constexpr uint32_t kBytes = kOffBar + 256 + 1024;
+};
+static_assert(Lay<256>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "shared memory of one CTA");
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor, kind::i8: signed 8-bit A and B (format 1), int32
+// accumulator (format 2), both K-major, dense, wrapping.
+__device__ __forceinline__ uint32_t idesc_i8(int M, int N) {
+    return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory"); }
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Int8GemmArgs a) {
+    using L = Lay<CAP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    TileSched& sched = *reinterpret_cast<TileSched*>(smem + L::kOffSched);
+    float* xs_s = reinterpret_cast<float*>(smem + L::kOffXs);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+    uint64_t* empty = full + L::kStages;
+    uint64_t* acc = empty + L::kStages;
+    uint64_t* tmem_free = acc + 1;
+    uint64_t* drain = tmem_free + 1;
+    uint64_t* red_full = drain + 1;
+    uint64_t* red_done = red_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(red_done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = a.splits;
+    const int crank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int cl = static_cast<int>(blockIdx.x) / S, ncl = static_cast<int>(gridDim.x) / S;
+    const int KT = static_cast<int>((a.K + 127) / 128);
+    const int k_lo = static_cast<int>(static_cast<int64_t>(crank) * KT / S);
+    const int steps = static_cast<int>(static_cast<int64_t>(crank + 1) * KT / S) - k_lo;
+    const int tiles_w = static_cast<int>((a.N + 255) / 256);
+    const uint64_t tmo = a.timeout_ns;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(full + s, 2);  // the two producers (+ their bytes)
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(acc, 1);
+        mbar_init(tmem_free, kEpiWarps);
+        mbar_init(drain, 1);
+        mbar_init(red_full, kEpiWarps * S);
+        mbar_init(red_done, kEpiWarps * S);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == kWarpX && lane == 0) {
+        tma_prefetch_desc(&tm_x);
+        tma_prefetch_desc(&tm_w);
+    }
+    build_sched(sched, a.offsets, a.E, static_cast<int>(a.M), CAP);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (S > 1) cluster_sync();
+    const uint32_t tmem = *tmem_slot;
+    TileIter it(sched, cl, ncl, tiles_w, a.E);
+    Tile tl;
+
+    if (warp == kWarpX || warp == kWarpW) {
+        if (lane == 0) {
+            const bool is_x = warp == kWarpX;
+            if (is_x) asm volatile("griddepcontrol.wait;" ::: "memory");  // the quantised tokens
+            int g = 0;
+            bool ok = true;
+            while (ok && it.next(tl)) {
+                const int boxes = (tl.rows + L::kBoxRows - 1) / L::kBoxRows;
+                for (int i = 0; i < steps; ++i, ++g) {
+                    const int s = g % L::kStages;
+                    if (g >= L::kStages &&
+                        !mbar_wait(empty + s, static_cast<uint32_t>(g / L::kStages - 1) & 1u, tmo, a.status)) {
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                    if (*abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    if (is_x) {
+                        mbar_arrive_expect_tx(full + s, static_cast<uint32_t>(boxes) * L::kBoxRows * 128u);
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(smem + s * L::kXStage + b * L::kBoxRows * 128, &tm_x, full + s, (k_lo + i) * 128,
+                                        tl.row0 + b * L::kBoxRows);
+                    } else {
+                        mbar_arrive_expect_tx(full + s, kWStage);
+                        tma_load_3d(smem + L::kOffW + s * kWStage, &tm_w, full + s, (k_lo + i) * 128, tl.w0, tl.e);
+                    }
+                }
+            }
+            for (int j = max(0, g - L::kStages); j < g; ++j)
+                mbar_wait(full + j % L::kStages, static_cast<uint32_t>(j / L::kStages) & 1u, tmo, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        if (lane == 0) {
+            int g = 0, n = 0;
+            bool ok = true;
+            while (ok && it.next(tl)) {
+                if (n > 0 && !mbar_wait(tmem_free, static_cast<uint32_t>(n - 1) & 1u, tmo, a.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t idesc = idesc_i8(128, (tl.rows + 15) & ~15);
+                for (int i = 0; i < steps; ++i, ++g) {
+                    const int s = g % L::kStages;
+                    if (!mbar_wait(full + s, static_cast<uint32_t>(g / L::kStages) & 1u, tmo, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t xt = smem_u32(smem + s * L::kXStage), wt = smem_u32(smem + L::kOffW + s * kWStage);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t xd = sw128_desc(xt + kk * 32, 16, 1024);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            umma_i8(tmem + h * 256, sw128_desc(wt + h * 16384 + kk * 32, 16, 1024), xd, idesc,
+                                    (i > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    umma_commit(empty + s);
+                }
+                if (ok) umma_commit(acc);
+                ++n;
+            }
+            if (!ok) *abort_flag = 1;
+            umma_commit(drain);
+            mbar_wait(drain, 0u, tmo, nullptr);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ epilogue --
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the token scales
+        const int q = warp & 3, h = warp >> 2;
+        const int nl = h * 128 + q * 32 + lane;
+        bool ok = true;
+        int n = 0;
+        while (ok && it.next(tl)) {
+            if (static_cast<int>(threadIdx.x) < tl.rows) xs_s[threadIdx.x] = __ldcg(a.xs + tl.row0 + threadIdx.x);
+            const int64_t wrow = static_cast<int64_t>(tl.e) * a.N;
+            const float ws = __ldg(a.ws + wrow + min(tl.w0 + nl, static_cast<int>(a.N) - 1));
+            epi_bar();
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc, static_cast<uint32_t>(n) & 1u, tmo, a.status));
+            if (!ok) *abort_flag = 1;
+            tc_fence_after();
+            const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * 256;
+            if (S == 1) {
+                const int col = tl.w0 + (nl & ~1);
+                const bool write = ok && col < a.N;
+                for (int c = 0; c < tl.rows; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(trow + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float y0 = __int2float_rn(static_cast<int>(r[i])) * (xs_s[c + i] * ws);
+                        const float y1 = __int2float_rn(static_cast<int>(r[i + 1])) * (xs_s[c + i + 1] * ws);
+                        const float got = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? y0 : y1, 1);
+                        const int tok = c + i + (lane & 1);
+                        if (write && tok < tl.rows)
+                            *reinterpret_cast<uint32_t*>(a.Y + static_cast<int64_t>(tl.row0 + tok) * a.N + col) =
+                                (lane & 1) ? pack_bf16x2(got, y1) : pack_bf16x2(y0, got);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tmem_free);
+            } else {
+                int* buf = reinterpret_cast<int*>(smem + L::kOffRed);
+                for (int c = 0; c < tl.rows; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(trow + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i < tl.rows) buf[(c + i) * 256 + nl] = static_cast<int>(r[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(tmem_free);
+                    for (int s = 0; s < S; ++s) mbar_arrive_remote(mapa_shared(smem_u32(red_full), s));
+                }
+                const bool got = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(red_full, static_cast<uint32_t>(n) & 1u, tmo, a.status));
+                ok = ok && got;
+                const int per4 = 64 / S;
+                const uint32_t buf0 = smem_u32(buf);
+                for (int item = threadIdx.x; ok && item < tl.rows * per4; item += kEpiWarps * 32) {
+                    const int tok = item / per4, nc = crank * (256 / S) + 4 * (item % per4);
+                    if (tl.w0 + nc >= a.N) continue;
+                    int v[4] = {0, 0, 0, 0};
+                    for (int s = 0; s < S; ++s) {
+                        const float4 x = ld_cluster_f4(mapa_shared(buf0 + static_cast<uint32_t>(tok * 256 + nc) * 4u, s));
+                        v[0] += __float_as_int(x.x);
+                        v[1] += __float_as_int(x.y);
+                        v[2] += __float_as_int(x.z);
+                        v[3] += __float_as_int(x.w);
+                    }
+                    float y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        y[j] = __int2float_rn(v[j]) * (xs_s[tok] * __ldg(a.ws + wrow + tl.w0 + nc + j));
+                    *reinterpret_cast<uint2*>(a.Y + static_cast<int64_t>(tl.row0 + tok) * a.N + tl.w0 + nc) =
+                        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                }
+                __syncwarp();
+                if (lane == 0)
+                    for (int s = 0; s < S; ++s) mbar_arrive_remote(mapa_shared(smem_u32(red_done), s));
+                const bool done = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(red_done, static_cast<uint32_t>(n) & 1u, tmo, a.status));
+                ok = ok && done;
+            }
+            ++n;
+            // all epilogue warps leave together (they meet at barriers); this
+            // one also ends the reads of this tile's token scales
+            int all_ok;
+            asm volatile(
+                "{\n\t.reg .pred p, r;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+                "bar.red.and.pred r, 1, %2, p;\n\tselp.s32 %0, 1, 0, r;\n\t}"
+                : "=r"(all_ok)
+                : "r"(ok ? 1 : 0), "n"(kEpiWarps * 32)
+                : "memory");
+            ok = all_ok != 0;
+        }
+        if (!ok) *abort_flag = 1;
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (S > 1) cluster_sync();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---------------------------------------------------------- quantise rows --
+// One CTA per row: a = max|x|; code = 127 x / a rounded to the nearest
+// integer, halves to even; scale = a / 127. A row of zeros gets codes 0 and
+// scale 0; a row that holds a NaN or an infinity gets codes 0 and scale NaN
+// (its products are NaN, no other row is touched).
+//
+// The code is that of the exact quotient: the fp32 product x (127 / a) is at
+// most 2.3e-5 off, so only a value within 1e-4 of a half can round the wrong
+// way, and there 254 |x| is compared with (2 j + 1) a, both exact in 64 bits.
+// Bound by reading the row once (it stays in registers up to K = 8192, is
+// read again from L2 above) and writing a byte per element.
+constexpr int kQThreads = 256;
+constexpr int kQCache = 4;  // 8-element vectors per thread kept in registers
+
+__device__ __forceinline__ int code_of(float x, float a, float inv) {
+    const float p = x * inv;
+    int k = __float2int_rn(p);
+    if (fabsf(fabsf(p - static_cast<float>(k)) - 0.5f) < 1e-4f) {
+        const int j = static_cast<int>(fabsf(p));                    // |p| is near j + 1/2, from either side
+        const double l = 254.0 * static_cast<double>(fabsf(x)), r = (2.0 * j + 1.0) * static_cast<double>(a);
+        const int m = l < r ? j : (l > r ? j + 1 : j + (j & 1));
+        k = x < 0.0f ? -m : m;
+    }
+    return k;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
+    if (kBf16) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+        const float4 x = __ldg(f), y = __ldg(f + 1);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    }
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kQThreads) quantize_rows(const void* X, int64_t K, int8_t* codes, float* scale) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int64_t row = blockIdx.x;
+    const int t = threadIdx.x, nv = static_cast<int>(K / 8);
+    __shared__ uint32_t part[kQThreads / 32];
+    float v[kQCache][8];
+    uint32_t top = 0;  // |x| as bits: a NaN is above an infinity, both above every number
+#pragma unroll
+    for (int j = 0; j < kQCache; ++j) {
+        const int i = t + j * kQThreads;
+        if (i < nv) {
+            load8<kBf16>(X, row * K + 8ll * i, v[j]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kQCache; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[j][k]) & 0x7FFFFFFFu);
+    for (int i = t + kQCache * kQThreads; i < nv; i += kQThreads) {
+        float w[8];
+        load8<kBf16>(X, row * K + 8ll * i, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(w[k]) & 0x7FFFFFFFu);
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((t & 31) == 0) part[t >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kQThreads / 32; ++i) top = max(top, part[i]);
+    const bool bad = top >= 0x7F800000u;
+    const float amax = __uint_as_float(top);
+    if (t == 0) scale[row] = bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 127.0f);
+    // tiny rows are lifted by 2^64 (exact), so that 127 / a stays finite
+    const float lift = top < 0x1F800000u ? 18446744073709551616.0f : 1.0f;
+    const float a = amax * lift;
+    const bool none = bad || top == 0u;
+    const float inv = none ? 0.0f : __fdiv_rn(127.0f, a);
+    auto store = [&](int i, const float (&x)[8]) {
+        uint32_t w[2] = {0u, 0u};
+        if (!none) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                w[k >> 2] |= (static_cast<uint32_t>(code_of(x[k] * lift, a, inv)) & 0xFFu) << (8 * (k & 3));
+        }
+        *reinterpret_cast<uint2*>(codes + row * K + 8ll * i) = make_uint2(w[0], w[1]);
+    };
+#pragma unroll
+    for (int j = 0; j < kQCache; ++j) {
+        const int i = t + j * kQThreads;
+        if (i < nv) store(i, v[j]);
+    }
+    for (int i = t + kQCache * kQThreads; i < nv; i += kQThreads) {
+        float w[8];
+        load8<kBf16>(X, row * K + 8ll * i, w);
+        store(i, w);
+    }
+}
+
+template <int CAP>
+cudaError_t launch_one(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, bool pdl, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Lay<CAP>::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, int8_gemm<CAP>, x, w, a);
+}
+
+}  // namespace
+
+cudaError_t int8_init_device() {
+    cudaError_t e = cudaFuncSetAttribute(int8_gemm<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Lay<256>::kBytes));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(int8_gemm<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Lay<64>::kBytes));
+}
+
+cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, bool pdl,
+                             cudaStream_t st) {
+    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 1 || a.ctas % a.splits != 0 || (a.cap != 64 && a.cap != 256))
+        return cudaErrorInvalidValue;
+    if (a.splits != 1 && (a.cap != 64 || (a.splits != 2 && a.splits != 4 && a.splits != 8))) return cudaErrorInvalidValue;
+    if (a.splits > (a.K + 127) / 128) return cudaErrorInvalidValue;
+    return a.cap == 256 ? launch_one<256>(x, w, a, pdl, st) : launch_one<64>(x, w, a, pdl, st);
+}
+
+cudaError_t launch_quantize_rows(const void* X, bool bf16, int64_t rows, int64_t K, int8_t* codes, float* scale,
+                                 cudaStream_t st) {
+    if (rows < 1 || rows > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const unsigned grid = static_cast<unsigned>(rows);
+    if (bf16)
+        quantize_rows<true><<<grid, kQThreads, 0, st>>>(X, K, codes, scale);
+    else
+        quantize_rows<false><<<grid, kQThreads, 0, st>>>(X, K, codes, scale);
+    return cudaGetLastError();
+}
+
+}  // namespace qlora

@@ -287,4 +287,100 @@ cudaError_t launch_merge_tc(const CUtensorMap& b_map, const CUtensorMap& a_map, 
                             cudaStream_t st);
 cudaError_t merge_tc_init_device();
 
+// -------------------------------------------------- rows grouped by expert --
+// Tiles of the grouped matmuls: 256 weight rows x up to `cap` token rows of
+// one expert (64 or 256). `offsets`: device int32 [E + 1], or nullptr for one
+// expert that owns every row. ctas = clusters * splits; clusters of `splits`
+// CTAs (1, or with cap 64 also 2, 4, 8; at most the reduction steps) share a
+// tile's reduction.
+struct ExpertGemmArgs {
+    const int* offsets;
+    int E;
+    int64_t M;            // rows of the batch
+    int64_t N, K;         // one expert's weight: N x K
+    int64_t out_cols;     // N (forward) or K (dX)
+    int64_t red;          // K (forward) or N (dX)
+    int rank_cols;        // r
+    int cap, splits, ctas;
+    BlockConstants c;     // of the stacked weight, E N rows
+    uint16_t* out;        // bf16 [M, out_cols]
+    int* status;
+    uint64_t timeout_ns;
+};
+
+// act: X or dY {red, M}, lact: sT or sU {r, M}, both box {64, 16 or 64 (cap
+// 256)} SW128; codes {K/2, N, E}: forward box {32, 256, 1} SW32, dX box
+// {128, 64, 1} SW128; lw: forward B {r, N, E} box {64, 256, 1}, dX A
+// {K, r, E} box {64, 64, 1}, SW128.
+cudaError_t launch_expert_gemm(bool trans_w, const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact,
+                               const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl,
+                               cudaStream_t st);
+// clusters_out: clusters of 1, 2, 4, 8 CTAs resident at once.
+cudaError_t expert_gemm_init_device(int clusters_out[4]);
+
+// out[m, k r + j] = term k of scale * (act[m] . B_e[:, j]) for the rows of
+// every expert: term 0 the bf16 rounding, term k that of what is left.
+struct ExpertDownArgs {
+    const int* offsets;
+    int E;
+    int64_t M, red;
+    int r, NR;            // NR: r padded to 16, 32 or 64
+    int terms;
+    float scale;
+    uint16_t* out;        // bf16 [M, terms r]
+    int splits;           // cluster size along the reduction: 1, 2, 4, 8 (at most the 64-deep steps)
+    int stages;           // set by the launcher
+    int* status;
+    uint64_t timeout_ns;
+};
+// act {red, M} box {64, 128} SW128; b: b_mn false: A {K, r, E} box {64, NR, 1}
+// SW128, true: B {r, N, E} box {NR, 64, 1} with the NR * 2-byte swizzle.
+// tiles: 128-row tiles of the grid, at least those of the batch.
+cudaError_t launch_expert_down(bool b_mn, const CUtensorMap& act, const CUtensorMap& b, ExpertDownArgs a, int tiles,
+                               cudaStream_t st);
+
+// dA[e] = (sum of sU's terms)^T X, dB[e] = dY^T (sum of sT's terms) over the
+// expert's rows, fp32.
+struct ExpertGradArgs {
+    const int* offsets;
+    int E;
+    int64_t M, N, K;
+    int r, NR;
+    int terms_u, terms_t; // terms of sU and sT
+    float* dA;            // [E r, K]
+    float* dB;            // [E N, r]
+    int stages;           // set by the launcher
+    int* status;
+    uint64_t timeout_ns;
+};
+// x {K, M}, dy {N, M} box {64, 64} SW128; su {terms_u r, M}, st {terms_t r, M}
+// box {NR, 64} with the NR * 2-byte swizzle.
+cudaError_t launch_expert_grads(const CUtensorMap& x, const CUtensorMap& dy, const CUtensorMap& su,
+                                const CUtensorMap& st_, ExpertGradArgs a, bool pdl, cudaStream_t st);
+cudaError_t expert_rank_init_device();
+
+cudaError_t launch_expert_order(const int* ids, int M, int E, int* order, int* offsets, cudaStream_t st);
+cudaError_t expert_order_init_device();
+
+// --------------------------------------------------------- 8-bit integers --
+struct Int8GemmArgs {
+    const int* offsets;   // as above
+    int E;
+    int64_t M, N, K;
+    int cap, splits, ctas;
+    const float* xs;      // [M] token scales
+    const float* ws;      // [E N] channel scales
+    uint16_t* Y;          // bf16 [M, N]
+    int* status;
+    uint64_t timeout_ns;
+};
+// x: token codes {K, M} box {128, 16 or 64 (cap 256)}, w: {K, N, E} box
+// {128, 256, 1}, both SW128.
+cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, bool pdl,
+                             cudaStream_t st);
+cudaError_t int8_init_device();
+// X: fp32 or bf16 [rows, K], K % 16 == 0.
+cudaError_t launch_quantize_rows(const void* X, bool bf16, int64_t rows, int64_t K, int8_t* codes, float* scale,
+                                 cudaStream_t st);
+
 }  // namespace qlora

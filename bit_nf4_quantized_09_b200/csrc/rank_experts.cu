@@ -1,0 +1,485 @@
+// Rank-r matmuls of a layer of experts (tcgen05): every expert's adapter over
+// its own rows [o_e, o_{e+1}) of the batch.
+//
+//   down:   sT = s X A_e^T (forward),  sU = s dY B_e (backward)
+//   grads:  dA_e = sU^T X,  dB_e = dY^T sT    (fp32, over the expert's rows)
+//
+// ("waylandz ch.26" 26.2.4 with the adapter chosen by the row's expert.)
+//
+// Precision. The tensor core takes bf16 operands, and its fp32 accumulator
+// truncates: measured on this hardware a sum over 1024 terms is about 1e-6
+// low, and the loss grows with the length (2e-5 at 16384). Two measures keep
+// the fp32 gradients at fp32 accuracy:
+//   - sT and sU leave as sums of bf16 numbers (two for sT, which is kept
+//     between the passes; three for sU), each rounding the rest of the one
+//     before: 2^-17 and 2^-25 relative instead of bf16's 2^-9; the gradients
+//     run one UMMA per term into the same accumulator, which costs little
+//     beside reading X and dY once;
+//   - every 512 reduction elements the accumulator is read out and added to
+//     fp32 registers (round to nearest), two TMEM buffers in turn, so the
+//     tensor core never waits for it.
+//
+// Both kernels are bound by reading X and dY (2 bytes per token and column).
+//   warp 0 TMA producer, warp 1 TMEM owner + UMMA issuer, warps 2-5 epilogue.
+#include <algorithm>
+
+#include "kernels.h"
+#include "tiles.cuh"
+
+namespace qlora {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kFlush = 8;             // 64-deep steps between read-outs
+constexpr uint32_t kABytes = 128 * 64 * 2;
+constexpr uint32_t kTmemCols = 128;   // two accumulators of up to 64 columns
+constexpr int kMaxStages = 8;
+constexpr uint32_t kRowBytes = 256;   // one fp32 accumulator row in the reduction buffer
+
+__device__ __forceinline__ uint64_t mn_b_desc(uint32_t addr, int NR) {
+    // [64 reduction rows, NR columns] with the NR * 2-byte swizzle: rows of
+    // NR * 2 bytes, 8-row groups 16 NR bytes apart, one atom spanning all columns
+    const uint32_t layout = NR == 16 ? 6u : (NR == 32 ? 4u : 2u);
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(1u) << 16;
+    d |= static_cast<uint64_t>((16u * static_cast<uint32_t>(NR) >> 4) & 0x3FFFu) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(layout) << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+struct Bars {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t acc_full[2], acc_free[2], tail_in, masked, drain;
+    uint32_t tmem_slot;
+    int abort_flag;
+    int tile[4];
+};
+
+__device__ __forceinline__ void init_bars(Bars* b, int stages) {
+    for (int s = 0; s < stages; ++s) {
+        mbar_init(b->full + s, 1);
+        mbar_init(b->empty + s, 1);
+    }
+    for (int p = 0; p < 2; ++p) {
+        mbar_init(b->acc_full + p, 1);
+        mbar_init(b->acc_free + p, 4);
+    }
+    mbar_init(&b->tail_in, 1);
+    mbar_init(&b->masked, 4);
+    mbar_init(&b->drain, 1);
+    b->abort_flag = 0;
+    fence_mbar_init();
+}
+
+// Adds accumulator buffer `chunk & 1` (NR columns) to this thread's row.
+__device__ __forceinline__ bool flush_acc(Bars* b, uint32_t tmem, int q, int lane, int NR, int chunk, float (&v)[64],
+                                          uint64_t tmo, int* status) {
+    const int p = chunk & 1;
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(b->acc_full + p, static_cast<uint32_t>(chunk >> 1) & 1u, tmo, status));
+    if (!ok) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int c0 = 0; c0 < 64; c0 += 16) {
+        if (c0 < NR) {
+            uint32_t r[16];
+            tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + p * 64 + c0, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[c0 + i] += __uint_as_float(r[i]);
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b->acc_free + p);
+    return true;
+}
+
+// ------------------------------------------------------------------- down --
+// One cluster of S CTAs per 128-row tile of an expert; split y takes the
+// 64-deep steps y, y + S, ...; partial sums are added in rank order through
+// distributed shared memory.
+template <bool kBMn>
+__global__ void __launch_bounds__(kThreads, 2)
+    expert_down(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                const ExpertDownArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Bars bars;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int NR = a.NR, S = a.splits, y = static_cast<int>(blockIdx.y);
+    const uint32_t b_bytes = static_cast<uint32_t>(NR) * 128u, stage = kABytes + b_bytes;
+    const int stages = a.stages;
+    const uint64_t tmo = a.timeout_ns;
+    if (warp == 0) {
+        int e = 0, row0 = 0, rows = 0;
+        const bool found = find_row_tile(a.offsets, a.E, static_cast<int>(a.M), 128, static_cast<int>(blockIdx.x), &e, &row0,
+                                         &rows);
+        if (lane == 0) {
+            bars.tile[0] = found ? rows : 0;
+            bars.tile[1] = e;
+            bars.tile[2] = row0;
+            init_bars(&bars, stages);
+            tma_prefetch_desc(&tm_a);
+            tma_prefetch_desc(&tm_b);
+        }
+    }
+    __syncthreads();
+    const int rows = bars.tile[0], e = bars.tile[1], row0 = bars.tile[2];
+    if (rows == 0) return;  // past the last tile: the whole cluster
+    if (warp == 1) {
+        tmem_alloc(&bars.tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_slot;
+    volatile int* abort_flag = &bars.abort_flag;
+    const int KT = static_cast<int>((a.red + 63) / 64);
+    const int steps = y < KT ? (KT - y + S - 1) / S : 0;
+    const int chunks = (steps + kFlush - 1) / kFlush;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int i = 0;
+            for (; i < steps; ++i) {
+                const int s = i % stages;
+                if (i >= stages && !mbar_wait(bars.empty + s, static_cast<uint32_t>(i / stages - 1) & 1u, tmo, a.status)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                if (*abort_flag) break;
+                const int k = (i * S + y) * 64;
+                uint8_t* st = smem + s * stage;
+                mbar_arrive_expect_tx(bars.full + s, stage);
+                tma_load_2d(st, &tm_a, bars.full + s, k, row0);
+                if (!kBMn)
+                    tma_load_3d(st + kABytes, &tm_b, bars.full + s, k, 0, e);
+                else
+                    tma_load_3d(st + kABytes, &tm_b, bars.full + s, 0, k, e);
+            }
+            for (int j = max(0, i - stages); j < i; ++j)
+                mbar_wait(bars.full + j % stages, static_cast<uint32_t>(j / stages) & 1u, tmo, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16(128, NR, false, kBMn);
+            bool ok = true;
+            for (int i = 0; ok && i < steps; ++i) {
+                const int s = i % stages, chunk = i / kFlush, p = chunk & 1;
+                if (i % kFlush == 0 && chunk >= 2 &&
+                    !mbar_wait(bars.acc_free + p, static_cast<uint32_t>((chunk >> 1) - 1) & 1u, tmo, a.status))
+                    ok = false;
+                if (ok && !mbar_wait(bars.full + s, static_cast<uint32_t>(i / stages) & 1u, tmo, a.status)) ok = false;
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t at = smem_u32(smem + s * stage), bt = at + kABytes;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_f16(tmem + p * 64, sw128_desc(at + kk * 32, 16, 1024),
+                             kBMn ? mn_b_desc(bt + kk * 16 * NR * 2, NR) : sw128_desc(bt + kk * 32, 16, 1024), idesc,
+                             (i % kFlush > 0 || kk > 0) ? 1u : 0u);
+                umma_commit(bars.empty + s);
+                if (i % kFlush == kFlush - 1 || i == steps - 1) umma_commit(bars.acc_full + p);
+            }
+            if (!ok) *abort_flag = 1;
+            umma_commit(&bars.drain);
+            mbar_wait(&bars.drain, 0u, tmo, nullptr);
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3, t = q * 32 + lane;
+        float v[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+        bool ok = true;
+        for (int c = 0; ok && c < chunks; ++c) ok = flush_acc(&bars, tmem, q, lane, NR, c, v, tmo, a.status);
+        if (!ok) *abort_flag = 1;
+        // this row to the reduction buffer in the first stages (idle: every
+        // copy has landed and every UMMA has completed), 16-byte chunk c at
+        // t * 256 + ((c ^ (t & 7)) << 4)
+        const uint32_t buf = smem_u32(smem) + static_cast<uint32_t>(t) * kRowBytes;
+        if (ok) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                if (4 * c < NR) {
+                    const uint32_t w4[4] = {__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                                            __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3])};
+                    sts128(buf + ((static_cast<uint32_t>(c) ^ static_cast<uint32_t>(t & 7)) << 4), w4);
+                }
+        }
+    }
+
+    tc_fence_before();
+    cluster_sync();
+    {
+        const int rank = static_cast<int>(cluster_ctarank());
+        const int rows_per = 128 / S, cols4 = a.r / 4, T = a.terms;
+        const uint32_t buf0 = smem_u32(smem);
+        for (int itm = threadIdx.x; itm < rows_per * cols4; itm += kThreads) {
+            const int t = rank * rows_per + itm / cols4, c = itm % cols4;
+            if (t >= rows) continue;
+            const uint32_t off = static_cast<uint32_t>(t) * kRowBytes + ((static_cast<uint32_t>(c) ^ (t & 7)) << 4);
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int s = 0; s < S; ++s) {
+                const float4 p = ld_cluster_f4(mapa_shared(buf0 + off, static_cast<uint32_t>(s)));
+                x[0] += p.x;
+                x[1] += p.y;
+                x[2] += p.z;
+                x[3] += p.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(a.scale, x[j]);
+            uint16_t* out = a.out + (static_cast<int64_t>(row0 + t) * T) * a.r + 4 * c;
+            for (int k = 0; k < T; ++k) {
+                const uint2 o = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+                *reinterpret_cast<uint2*>(out + k * a.r) = o;
+                // what this term leaves (exact in fp32); an infinity or a NaN
+                // is carried by the first term alone
+                const float h[4] = {__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xFFFF0000u), __uint_as_float(o.y << 16),
+                                    __uint_as_float(o.y & 0xFFFF0000u)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = isfinite(h[j]) ? x[j] - h[j] : 0.0f;
+            }
+        }
+    }
+    cluster_sync();  // no CTA leaves while another may still read its shared memory
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ grads --
+// One CTA per expert and 128 columns of X (dA) or dY (dB); the reduction runs
+// over the expert's rows, 64 at a time. The rows past its end in the last
+// step belong to other experts (or to nobody): both operands' copies of them
+// are zeroed in shared memory before the UMMA, so whatever they hold, NaN
+// included, adds nothing. An expert without rows gets zeros.
+__global__ void __launch_bounds__(kThreads, 2)
+    expert_grads(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_dy,
+                 const __grid_constant__ CUtensorMap tm_su, const __grid_constant__ CUtensorMap tm_st,
+                 const ExpertGradArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Bars bars;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tk = static_cast<int>((a.K + 127) / 128), tn = static_cast<int>((a.N + 127) / 128);
+    const int e = static_cast<int>(blockIdx.x) / (tk + tn), local = static_cast<int>(blockIdx.x) % (tk + tn);
+    const bool is_a = local < tk;
+    const int c0 = (is_a ? local : local - tk) * 128;  // first column of X or dY
+    const int NR = a.NR, r = a.r, T = is_a ? a.terms_u : a.terms_t;
+    const uint32_t b_bytes = static_cast<uint32_t>(NR) * 128u;
+    const uint32_t stage = kABytes + static_cast<uint32_t>(max(a.terms_u, a.terms_t)) * b_bytes;
+    const int stages = a.stages;
+    const uint64_t tmo = a.timeout_ns;
+    const CUtensorMap* ta = is_a ? &tm_x : &tm_dy;
+    const CUtensorMap* tb = is_a ? &tm_su : &tm_st;
+    if (warp == 0) {
+        int first, last;
+        expert_rows(a.offsets, e, static_cast<int>(a.M), &first, &last);
+        if (lane == 0) {
+            bars.tile[0] = first;
+            bars.tile[1] = last - first;
+            init_bars(&bars, stages);
+            tma_prefetch_desc(ta);
+            tma_prefetch_desc(tb);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc(&bars.tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_slot;
+    volatile int* abort_flag = &bars.abort_flag;
+    const int row0 = bars.tile[0], m = bars.tile[1];
+    const int steps = (m + 63) / 64, chunks = (steps + kFlush - 1) / kFlush;
+    const int tail = m - (steps - 1) * 64;  // rows of the last step
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int i = 0;
+            for (; i < steps; ++i) {
+                const int s = i % stages;
+                if (i >= stages && !mbar_wait(bars.empty + s, static_cast<uint32_t>(i / stages - 1) & 1u, tmo, a.status)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                if (*abort_flag) break;
+                const int row = row0 + i * 64;
+                uint8_t* st = smem + s * stage;
+                mbar_arrive_expect_tx(bars.full + s, kABytes + static_cast<uint32_t>(T) * b_bytes);
+                tma_load_2d(st, ta, bars.full + s, c0, row);
+                tma_load_2d(st + 8192, ta, bars.full + s, c0 + 64, row);
+                for (int k = 0; k < T; ++k) tma_load_2d(st + kABytes + k * b_bytes, tb, bars.full + s, k * r, row);
+            }
+            for (int j = max(0, i - stages); j < i; ++j)
+                mbar_wait(bars.full + j % stages, static_cast<uint32_t>(j / stages) & 1u, tmo, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16(128, NR, true, true);
+            bool ok = true;
+            for (int i = 0; ok && i < steps; ++i) {
+                const int s = i % stages, chunk = i / kFlush, p = chunk & 1;
+                if (i % kFlush == 0 && chunk >= 2 &&
+                    !mbar_wait(bars.acc_free + p, static_cast<uint32_t>((chunk >> 1) - 1) & 1u, tmo, a.status))
+                    ok = false;
+                if (ok && !mbar_wait(bars.full + s, static_cast<uint32_t>(i / stages) & 1u, tmo, a.status)) ok = false;
+                if (ok && i == steps - 1 && tail < 64) {
+                    mbar_arrive(&bars.tail_in);  // the epilogue warps zero the rows past the end
+                    if (!mbar_wait(&bars.masked, 0u, tmo, a.status)) ok = false;
+                }
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t at = smem_u32(smem + s * stage), bt = at + kABytes;
+                for (int kk = 0; kk < 4; ++kk)
+                    for (int k = 0; k < T; ++k)
+                        umma_f16(tmem + p * 64, sw128_desc(at + kk * 2048, 8192, 1024),
+                                 mn_b_desc(bt + k * b_bytes + kk * 16 * NR * 2, NR), idesc,
+                                 (i % kFlush > 0 || kk > 0 || k > 0) ? 1u : 0u);
+                umma_commit(bars.empty + s);
+                if (i % kFlush == kFlush - 1 || i == steps - 1) umma_commit(bars.acc_full + p);
+            }
+            if (!ok) *abort_flag = 1;
+            umma_commit(&bars.drain);
+            mbar_wait(&bars.drain, 0u, tmo, nullptr);
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3, t = q * 32 + lane;
+        float v[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+        bool ok = true;
+        for (int c = 0; ok && c < chunks; ++c) {
+            if (c == chunks - 1 && tail < 64) {
+                const int i = steps - 1, s = i % stages;
+                // the issuer has seen the last step land; its stage's barrier
+                // stays in that phase, so its parity is safe to read (these
+                // warps did not follow the phases before it)
+                ok = __all_sync(0xFFFFFFFFu,
+                                mbar_wait(&bars.tail_in, 0u, tmo, a.status) &&
+                                    mbar_wait(bars.full + s, static_cast<uint32_t>(i / stages) & 1u, tmo, a.status));
+                if (!ok) break;
+                const uint32_t st = smem_u32(smem + s * stage);
+                const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+                // A: rows of 128 bytes in two boxes; B: rows of 2 NR bytes per term
+                const int na = (64 - tail) * 8, nb = (64 - tail) * NR / 8;
+                for (int x = t; x < 2 * na; x += 128)
+                    sts128(st + (x / na) * 8192 + tail * 128 + (x % na) * 16, zero);
+                for (int x = t; x < T * nb; x += 128)
+                    sts128(st + kABytes + (x / nb) * b_bytes + tail * NR * 2 + (x % nb) * 16, zero);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.masked);
+            }
+            ok = flush_acc(&bars, tmem, q, lane, NR, c, v, tmo, a.status);
+        }
+        if (!ok) *abort_flag = 1;
+        if (ok && is_a) {
+            if (c0 + t < a.K) {
+                float* out = a.dA + static_cast<int64_t>(e) * r * a.K + c0 + t;
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    if (j < r) out[static_cast<int64_t>(j) * a.K] = v[j];
+            }
+        } else if (ok) {
+            if (c0 + t < a.N) {
+                float4* out = reinterpret_cast<float4*>(a.dB + (static_cast<int64_t>(e) * a.N + c0 + t) * r);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (4 * j < r) out[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+constexpr size_t kDownSmem(int NR, int stages) { return static_cast<size_t>(stages) * (kABytes + NR * 128) + 1024; }
+constexpr size_t kGradSmem(int NR, int terms, int stages) {
+    return static_cast<size_t>(stages) * (kABytes + terms * NR * 128) + 1024;
+}
+constexpr int kDownStages = 4;                 // 72-96 KB: two CTAs per SM
+constexpr size_t kGradBudget = 112 * 1024;     // per CTA, two per SM
+
+}  // namespace
+
+cudaError_t expert_rank_init_device() {
+    cudaError_t e;
+    const int down = static_cast<int>(kDownSmem(64, kDownStages));
+    if ((e = cudaFuncSetAttribute(expert_down<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, down)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(expert_down<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, down)) != cudaSuccess)
+        return e;
+    return cudaFuncSetAttribute(expert_grads, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kGradBudget));
+}
+
+cudaError_t launch_expert_down(bool b_mn, const CUtensorMap& act, const CUtensorMap& b, ExpertDownArgs a, int tiles,
+                               cudaStream_t st) {
+    const int S = a.splits;
+    if ((S != 1 && S != 2 && S != 4 && S != 8) || tiles < 1 || a.NR < a.r || a.terms < 1) return cudaErrorInvalidValue;
+    a.stages = kDownStages;
+    static_assert(kDownStages * kABytes >= 128 * kRowBytes, "the reduction buffer lies in the stages");
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(S));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kDownSmem(a.NR, a.stages);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = static_cast<unsigned>(S);
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return b_mn ? cudaLaunchKernelEx(&cfg, expert_down<true>, act, b, a)
+                : cudaLaunchKernelEx(&cfg, expert_down<false>, act, b, a);
+}
+
+cudaError_t launch_expert_grads(const CUtensorMap& x, const CUtensorMap& dy, const CUtensorMap& su, const CUtensorMap& st_,
+                                ExpertGradArgs a, bool pdl, cudaStream_t st) {
+    const int terms = std::max(a.terms_u, a.terms_t);
+    a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kGradBudget - 1024) / (kABytes + terms * a.NR * 128)));
+    if (a.stages < 2) return cudaErrorInvalidValue;
+    const int64_t tiles = static_cast<int64_t>(a.E) * ((a.K + 127) / 128 + (a.N + 127) / 128);
+    if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kGradSmem(a.NR, terms, a.stages);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, expert_grads, x, dy, su, st_, a);
+}
+
+}  // namespace qlora

@@ -276,6 +276,87 @@ qlora_status qlora_linear_bwd_group(const uint16_t* dY, const uint16_t* X, int64
                                     uint16_t* dX, float* dA, float* dB,
                                     void* ws, size_t ws_bytes, void* stream);
 
+/* Layers of experts: the weight and the adapter chosen per token row ["waylandz
+ * LLM book ch.26", 26.2.4 and 26.7.3, with a frozen 4-bit weight per expert].
+ *
+ * Rows stand grouped by expert: offsets (device int32 [E + 1], not decreasing)
+ * give expert e the rows [offsets[e], offsets[e + 1]); an expert may have none.
+ * Offsets are read on the device only, so nothing waits for a router's counts;
+ * there they are clamped to [0, M] and to their running maximum. Rows before
+ * offsets[0] and from offsets[E] on belong to no expert: their outputs (Y, sT,
+ * dX) are left as they were, and whatever their inputs hold reaches no result.
+ * 1 <= E <= 512. */
+
+/* Row order of a batch by expert id: a stable counting sort.
+ *   order[j]: the row at place j when rows stand by id, rows of one id in their
+ *             own order, rows whose id is outside [0, E) behind all others
+ *   offsets:  [E + 1] as above (offsets[E] = rows whose id names an expert)
+ * ids: int32 [M], order: int32 [M], offsets: int32 [E + 1], device, 4-byte
+ * aligned; M >= 0 (an empty batch writes zero offsets). The grouped calls take
+ * X gathered by order. One launch, no workspace. */
+qlora_status qlora_expert_order(const int32_t* ids, int64_t M, int E, int32_t* order, int32_t* offsets, void* stream);
+
+/* Forward and backward of E experts of N x K, for the rows m of expert e:
+ *   sT[m] = (alpha/r) X[m] A_e^T     (saved as the sum of two bf16 numbers)
+ *   Y[m]  = bf16( X[m] deq(W_e)^T + sT[m] B_e^T )
+ *   sU[m] = (alpha/r) dY[m] B_e
+ *   dX[m] = bf16( dY[m] deq(W_e) + sU[m] A_e )
+ *   dA_e  = fp32( sum over its rows of sU[m]^T X[m] ),  dB_e = fp32( dY[m]^T sT[m] )
+ * w: the experts' weights stacked, one qlora_nf4_weight of E N rows (quantised
+ * in one call; N % 8 == 0). A: bf16 [E r, K] (the A_e stacked); B: bf16 [E N, r];
+ * r in {8, 16, 32, 64}. X: bf16 [M, K]; Y, dY: bf16 [M, N]; dX: bf16 [M, K].
+ * sT_save (may be NULL): bf16 [M, 2 r]: columns [0, r) the rounding of sT,
+ * columns [r, 2 r) that of what it leaves, so that dB keeps fp32 accuracy; the
+ * rank-r terms of Y and dX use the first. The backward takes the forward's
+ * sT_save as sT, or NULL to recompute it.
+ * dA: fp32 [E r, K], dB: fp32 [E N, r], overwritten; zeros for an expert
+ * without rows. M == 0: the forward is a no-op, the backward writes zeros.
+ * The workspace size comes from qlora_workspace_bytes_experts (N, K of one
+ * expert). Sums have a fixed order: equal calls give equal bits. Errors,
+ * asynchrony and ownership as for qlora_linear_fwd/bwd. */
+size_t qlora_workspace_bytes_experts(int op, int64_t M, int64_t N, int64_t K, int r, int E);
+qlora_status qlora_linear_fwd_experts(const uint16_t* X, int64_t M, const qlora_nf4_weight* w, int E,
+                                      const int32_t* offsets, const uint16_t* A, const uint16_t* B, int r, float alpha,
+                                      uint16_t* Y, uint16_t* sT_save, void* ws, size_t ws_bytes, void* stream);
+qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int64_t M, const qlora_nf4_weight* w, int E,
+                                      const int32_t* offsets, const uint16_t* A, const uint16_t* B, int r, float alpha,
+                                      const uint16_t* sT, uint16_t* dX, float* dA, float* dB, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/* A weight in 8-bit integers, W[n, k] = scale[n] * codes[n, k]: the form to
+ * serve a merged weight in [explainer 落とし穴: the merge goes to the 16-bit
+ * weight; its update is lost in 4 bits]. N x K row-major codes in [-127, 127];
+ * N % 8 == 0, K % 16 == 0, K <= 131072. */
+typedef struct {
+    const int8_t* codes;
+    const float*  scale;
+    int64_t       N;
+    int64_t       K;
+} qlora_int8_weight;
+
+/* Quantise the rows of W (fp32 or bf16 [N, K], device; K % 16 == 0) to 8 bits:
+ *   scale[n] = fp32( a / 127 ),  codes[n, k] = 127 W[n, k] / a  rounded to the
+ * nearest integer, halves to even (of the exact quotient), a = max_k |W[n, k]|.
+ * A row of zeros has scale 0 and codes 0; a row that holds a NaN or an infinity
+ * has scale NaN and codes 0. One launch, no workspace. */
+qlora_status qlora_quantize_int8(const float* W, int64_t N, int64_t K, int8_t* codes, float* scale, void* stream);
+qlora_status qlora_quantize_int8_bf16(const uint16_t* W, int64_t N, int64_t K, int8_t* codes, float* scale,
+                                      void* stream);
+
+/* Y = bf16( xs[m] scale[n] sum_k qx[m, k] codes[n, k] ), qx and xs the rows of X
+ * (bf16 [M, K]) quantised as above, one scale per token; the integer sums are
+ * exact. A token row with a NaN or an infinity gives a NaN row of Y and touches
+ * no other. qlora_linear_int8_experts: w stacks the weights of E experts (E N
+ * rows, N % 8 == 0), rows of X and Y grouped by offsets as above; rows of no
+ * expert are left as they were. Workspace: qlora_workspace_bytes_int8 (N, K of
+ * one expert; E = 1 for qlora_linear_int8); it holds the quantised tokens, so
+ * two calls that may overlap need one each. M == 0 is a no-op. */
+size_t qlora_workspace_bytes_int8(int64_t M, int64_t N, int64_t K, int E);
+qlora_status qlora_linear_int8(const uint16_t* X, int64_t M, const qlora_int8_weight* w, uint16_t* Y, void* ws,
+                               size_t ws_bytes, void* stream);
+qlora_status qlora_linear_int8_experts(const uint16_t* X, int64_t M, const qlora_int8_weight* w, int E,
+                                       const int32_t* offsets, uint16_t* Y, void* ws, size_t ws_bytes, void* stream);
+
 /* Host copies of the library's own NF4 tables: levels[16] (fp32, ascending)
  * and thresholds[15] (the fp32 decision points between neighbouring levels).
  * Computed on the host at load time, independently of any test code. */
