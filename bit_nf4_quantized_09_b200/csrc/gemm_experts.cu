@@ -15,10 +15,10 @@
 // more reduction step of the same accumulators, its operands loaded by TMA.
 //
 // Roles of a persistent CTA (one per SM, 20 warps):
-//   warps 0-15  dequantisers in two groups of eight that take the reduction
-//               steps in turn (one 64-weight block per thread, the exact
-//               w_hat = bf16(level c'), through the per-block byte tables);
-//               then the epilogue
+//   warps 0-15  dequantisers in four groups of four that take the reduction
+//               steps in turn, each with a weight stage of its own (two
+//               64-weight blocks per thread, the exact w_hat = bf16(level c')
+//               through the per-block byte tables); then the epilogue
 //   warp 16     TMA producer of the token tiles
 //   warp 17     TMA producer of the packed codes
 //   warp 18     TMEM owner, UMMA issuer
@@ -40,32 +40,38 @@ namespace qlora {
 namespace {
 
 constexpr int kDeqWarps = 16;
-constexpr int kGroupWarps = 8;
+constexpr int kGroups = 4, kGroupWarps = 4;
 constexpr int kWarpX = 16, kWarpC = 17, kWarpMma = 18, kWarpK = 19;
 constexpr int kThreads = (kWarpK + 1) * 32;
-constexpr int kPW = 3;                       // weight stages
+constexpr int kPW = kGroups;                 // weight stages: one per group
 constexpr uint32_t kWStage = 256 * 64 * 2;   // 32 KB
 constexpr uint32_t kCStage = 256 * 64 / 2;   // 8 KB of packed codes
 constexpr uint32_t kKStage = 1024;           // 256 block constants
 constexpr uint32_t kTmemCols = 512;
 
-// Shared memory by token capacity: 256 tokens leave room for two code stages;
-// with at most 64 the token ring shrinks and the codes run eight steps ahead.
+// Shared memory by token capacity: 256 tokens leave room for two token and
+// three code stages; with at most 64 there are four of each.
 template <int CAP>
 struct Lay {
-    static constexpr int kPX = CAP == 256 ? 3 : 4;
-    static constexpr int kPC = CAP == 256 ? 2 : 8;
-    static constexpr int kPK = CAP == 256 ? 8 : 16;
+    static constexpr int kPX = CAP == 256 ? 2 : 4;
+    static constexpr int kPC = CAP == 256 ? 3 : 4;
     static constexpr int kBoxRows = CAP == 256 ? 64 : 16;  // token rows per TMA box
     static constexpr uint32_t kXStage = CAP * 128;
     static constexpr uint32_t kOffW = kPX * kXStage;
     static constexpr uint32_t kOffC = kOffW + kPW * kWStage;
     static constexpr uint32_t kOffK = kOffC + kPC * kCStage;
-    static constexpr uint32_t kOffSched = kOffK + kPK * kKStage;
+    static constexpr uint32_t kOffSched = kOffK + kPC * kKStage;
     static constexpr uint32_t kOffBar = (kOffSched + sizeof(TileSched) + 63) / 64 * 64;
-    static constexpr uint32_t kBytes = kOffBar + 640 + 1024;
+    static constexpr uint32_t kBytes = kOffBar + 512 + 1024;
 };
 static_assert(Lay<256>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "shared memory of one CTA");
+// Code stages are a ring over all reduction steps, but each group waits on
+// barriers of its own (two, by the parity of its steps): it has not seen the
+// ring's other steps, and a phase parity is only safe to one who has seen the
+// phase before. Two steps of one barrier lie at least four reduction steps
+// apart (at the least when every second step is a rank-r step), so with at
+// most four stages the first has been consumed before the second is loaded.
+static_assert(Lay<256>::kPC <= 4 && Lay<64>::kPC <= 4, "code stages");
 static_assert(kPW * kWStage >= 64 * 256 * 4, "partial sums of 64 tokens fit the weight stages");
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
@@ -99,17 +105,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* w_full = x_empty + L::kPX;
     uint64_t* w_empty = w_full + kPW;
     uint64_t* c_full = w_empty + kPW;
-    uint64_t* c_empty = c_full + L::kPC;
-    uint64_t* k_full = c_empty + L::kPC;
-    uint64_t* k_empty = k_full + L::kPK;
-    uint64_t* acc = k_empty + L::kPK;
+    uint64_t* c_empty = c_full + 2 * kGroups;
+    uint64_t* acc = c_empty + L::kPC;
     uint64_t* tmem_free = acc + 1;
     uint64_t* drain = tmem_free + 1;
     uint64_t* red_full = drain + 1;
     uint64_t* red_done = red_full + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(red_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * L::kPX + 2 * kPW + 2 * L::kPC + 2 * L::kPK + 5) * 8 + 8 <= 640, "barriers");
+    static_assert((2 * L::kPX + 2 * kPW + 2 * kGroups + L::kPC + 5) * 8 + 8 <= 512, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = a.splits;
@@ -131,14 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(w_full + s, kGroupWarps);
             mbar_init(w_empty + s, 1);
         }
-        for (int s = 0; s < L::kPC; ++s) {
-            mbar_init(c_full + s, 1);
-            mbar_init(c_empty + s, kGroupWarps);
-        }
-        for (int s = 0; s < L::kPK; ++s) {
-            mbar_init(k_full + s, 32);
-            mbar_init(k_empty + s, kGroupWarps);
-        }
+        for (int s = 0; s < 2 * kGroups; ++s) mbar_init(c_full + s, 2);  // the code producer (+ its bytes) and the constants
+        for (int s = 0; s < L::kPC; ++s) mbar_init(c_empty + s, kGroupWarps);
         mbar_init(acc, 1);
         mbar_init(tmem_free, kDeqWarps);
         mbar_init(drain, 1);
@@ -205,11 +203,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kWarpC) {
         // ------------------------------------------------- code producer --
         if (lane == 0) {
-            int g = 0;
+            int g = 0, g0 = 0;
+            uint32_t par = 0;  // per group, parity of its reduction steps so far
             bool ok = true;
-            while (ok && it.next(tl)) {
+            for (; ok && it.next(tl); g0 += steps) {
                 for (int i = 0; i < nk; ++i, ++g) {
-                    const int s = g % L::kPC;
+                    const int s = g % L::kPC, G = (g0 + i) & (kGroups - 1);
+                    uint64_t* bar = c_full + 2 * G + ((par >> G) & 1u);
                     if (g >= L::kPC && !mbar_wait(c_empty + s, static_cast<uint32_t>(g / L::kPC - 1) & 1u, tmo, a.status)) {
                         *abort_flag = 1;
                         ok = false;
@@ -220,122 +220,142 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     const int kt = kr.lo + i;
-                    mbar_arrive_expect_tx(c_full + s, kCStage);
+                    par ^= 1u << G;
+                    mbar_arrive_expect_tx(bar, kCStage);
                     // rows past the expert's N and columns past K read as zeros
                     if (!kTransW)
-                        tma_load_3d(smem + L::kOffC + s * kCStage, &tm_codes, c_full + s, kt * 32, tl.w0, tl.e);
+                        tma_load_3d(smem + L::kOffC + s * kCStage, &tm_codes, bar, kt * 32, tl.w0, tl.e);
                     else
-                        tma_load_3d(smem + L::kOffC + s * kCStage, &tm_codes, c_full + s, tl.w0 / 2, kt * 64, tl.e);
+                        tma_load_3d(smem + L::kOffC + s * kCStage, &tm_codes, bar, tl.w0 / 2, kt * 64, tl.e);
                 }
             }
-            for (int j = max(0, g - L::kPC); j < g; ++j)
-                mbar_wait(c_full + j % L::kPC, static_cast<uint32_t>(j / L::kPC) & 1u, tmo, nullptr);
+            // after an abort copies may still be landing: every stage's last
+            // copy is over once its barrier has been consumed, or (bounded)
+            // once the time limit has passed
+            if (!ok)
+                for (int j = max(0, g - L::kPC); j < g; ++j)
+                    mbar_wait(c_empty + j % L::kPC, static_cast<uint32_t>(j / L::kPC) & 1u, tmo, nullptr);
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
         // ----------------------------------------------------------- MMA --
-        if (lane == 0) {
-            int g = 0, n = 0;
-            bool ok = true;
-            while (ok && it.next(tl)) {
-                if (n > 0 && !mbar_wait(tmem_free, static_cast<uint32_t>(n - 1) & 1u, tmo, a.status)) {
-                    ok = false;
-                    break;
-                }
+        const bool leader = elect_one();
+        // descriptors of stage 0; later stages and steps add their byte offset / 16
+        const uint64_t xd0 = sw128_desc(smem_u32(smem), 16, 1024);
+        const uint64_t wd0 = kTransW ? sw128_desc(smem_u32(smem + L::kOffW), 8192, 1024)
+                                     : sw128_desc(smem_u32(smem + L::kOffW), 16, 1024);
+        constexpr uint32_t kWk = (kTransW ? 2048 : 32) / 16;
+        int g = 0, n = 0;
+        bool ok = true;
+        while (ok && it.next(tl)) {
+            if (n > 0 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(tmem_free, static_cast<uint32_t>(n - 1) & 1u, tmo, a.status))))
+                break;
+            tc_fence_after();
+            const uint32_t idesc = idesc_bf16(128, (tl.rows + 15) & ~15, kTransW, false);
+            for (int i = 0; i < steps; ++i, ++g) {
+                const int sx = g % L::kPX, sw = g % kPW;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(x_full + sx, static_cast<uint32_t>(g / L::kPX) & 1u, tmo, a.status) &&
+                                                 mbar_wait(w_full + sw, static_cast<uint32_t>(g / kPW) & 1u, tmo, a.status));
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t idesc = idesc_bf16(128, (tl.rows + 15) & ~15, kTransW, false);
-                for (int i = 0; i < steps; ++i, ++g) {
-                    const int sx = g % L::kPX, sw = g % kPW;
-                    if (!mbar_wait(x_full + sx, static_cast<uint32_t>(g / L::kPX) & 1u, tmo, a.status) ||
-                        !mbar_wait(w_full + sw, static_cast<uint32_t>(g / kPW) & 1u, tmo, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t xt = smem_u32(smem + sx * L::kXStage);
-                    const uint32_t wt = smem_u32(smem + L::kOffW + sw * kWStage);
-                    const int ksub = i < nk ? 4 : (a.rank_cols + 15) / 16;
-                    for (int kk = 0; kk < ksub; ++kk) {
-                        const uint64_t xd = sw128_desc(xt + kk * 32, 16, 1024);
+                if (leader) {
+                    const uint64_t xd = xd0 + static_cast<uint32_t>(sx) * (L::kXStage / 16);
+                    const uint64_t wd = wd0 + static_cast<uint32_t>(sw) * (kWStage / 16);
+                    if (i < nk) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint64_t wd = kTransW ? sw128_desc(wt + h * 16384 + kk * 2048, 8192, 1024)
-                                                        : sw128_desc(wt + h * 16384 + kk * 32, 16, 1024);
-                            umma_f16(tmem + h * 256, wd, xd, idesc, (i > 0 || kk > 0) ? 1u : 0u);
-                        }
+                        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                umma_f16(tmem + h * 256, wd + h * (16384 / 16) + kk * kWk, xd + kk * 2, idesc,
+                                         (i > 0 || kk > 0) ? 1u : 0u);
+                    } else {
+                        for (int kk = 0; kk < (a.rank_cols + 15) / 16; ++kk)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                umma_f16(tmem + h * 256, wd + h * (16384 / 16) + kk * kWk, xd + kk * 2, idesc, 1u);
                     }
                     umma_commit(x_empty + sx);
                     umma_commit(w_empty + sw);
+                    if (i == steps - 1) umma_commit(acc);
                 }
-                if (ok) umma_commit(acc);
-                ++n;
+                __syncwarp();
             }
-            if (!ok) *abort_flag = 1;
-            // no UMMA in flight when the TMEM is freed
-            umma_commit(drain);
-            mbar_wait(drain, 0u, tmo, nullptr);
+            ++n;
         }
+        if (!ok) *abort_flag = 1;
+        // no UMMA in flight when the TMEM is freed
+        if (leader) umma_commit(drain);
+        mbar_wait(drain, 0u, tmo, nullptr);
         __syncwarp();
     } else if (warp >= kWarpK) {
         // ----------------------------------------------- block constants --
         // super-step ss: reduction steps 4 ss .. 4 ss + 3, 256 items of four
         // constants: forward, item = weight row, four consecutive k-blocks;
-        // dX, item = reduction row, the tile's four k-blocks
+        // dX, item = reduction row, the tile's four k-blocks. The next
+        // super-step's words are loaded before this one's are written.
         const int KB = static_cast<int>(a.K / kBlock);
         const bool vec = KB % 4 == 0;  // an item's constants are one aligned word (float4) of one group
         const float mean = kNoDq ? 0.0f : __ldg(a.c.mean);
-        int g = 0;
-        bool ok = true;
-        while (ok && it.next(tl)) {
-            const int64_t erow = static_cast<int64_t>(tl.e) * a.N;
-            for (int ss = kr.lo >> 2; ok && ss <= (kr.hi - 1) >> 2; ++ss) {
-                const int k0 = max(4 * ss, kr.lo), k1 = min(4 * ss + 4, kr.hi);
+        const int ss_lo = kr.lo >> 2, ss_hi = (kr.hi - 1) >> 2;
+        uint32_t qw[8];
+        float sv[8];
+        auto index = [&](const Tile& tile, int ss, int j) {  // first constant of item lane + 32 j
+            const int n = min((kTransW ? ss * 256 : tile.w0) + lane + 32 * j, static_cast<int>(a.N) - 1);
+            return (static_cast<int64_t>(tile.e) * a.N + n) * KB + (kTransW ? tile.w0 / kBlock : 4 * ss);
+        };
+        auto load = [&](const Tile& tile, int ss) {
+            if (kNoDq || !vec) return;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t ib = index(tile, ss, j);
+                qw[j] = __ldg(reinterpret_cast<const uint32_t*>(a.c.qabsmax + ib));
+                sv[j] = __ldg(a.c.s2 + (ib >> 8));
+            }
+        };
+        int g = 0, g0 = 0;
+        uint32_t par = 0;
+        bool ok = true, more = it.next(tl);
+        if (more) load(tl, ss_lo);
+        while (ok && more) {
+            for (int ss = ss_lo; ok && ss <= ss_hi; ++ss) {
                 float v[8][4];
-                const int kb0 = kTransW ? tl.w0 / kBlock : 4 * ss;
-                const int n0 = kTransW ? ss * 256 : tl.w0;
-                if (vec) {
-                    uint32_t qw[8];
-                    float sv[8];
+                if (kNoDq && vec) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const int n = min(n0 + lane + 32 * j, static_cast<int>(a.N) - 1);
-                        const int64_t ib = (erow + n) * KB + kb0;
-                        if (kNoDq) {
-                            const float4 f = __ldg(reinterpret_cast<const float4*>(a.c.absmax + ib));
-                            v[j][0] = f.x;
-                            v[j][1] = f.y;
-                            v[j][2] = f.z;
-                            v[j][3] = f.w;
-                        } else {
-                            qw[j] = __ldg(reinterpret_cast<const uint32_t*>(a.c.qabsmax + ib));
-                            sv[j] = __ldg(a.c.s2 + (ib >> 8));
-                        }
+                        const float4 f = __ldg(reinterpret_cast<const float4*>(a.c.absmax + index(tl, ss, j)));
+                        v[j][0] = f.x;
+                        v[j][1] = f.y;
+                        v[j][2] = f.z;
+                        v[j][3] = f.w;
                     }
-                    if (!kNoDq) {
+                } else if (vec) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
+                    for (int j = 0; j < 8; ++j)
 #pragma unroll
-                            for (int b = 0; b < 4; ++b) v[j][b] = __fmaf_rn(e4m3_to_f32(qw[j] >> (8 * b)), sv[j], mean);
-                    }
+                        for (int b = 0; b < 4; ++b) v[j][b] = __fmaf_rn(e4m3_to_f32(qw[j] >> (8 * b)), sv[j], mean);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const int n = min(n0 + lane + 32 * j, static_cast<int>(a.N) - 1);
+                        const int64_t i0 = index(tl, ss, j);
+                        const int kb0 = kTransW ? tl.w0 / kBlock : 4 * ss;
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
-                            const int64_t ib = (erow + n) * KB + min(kb0 + b, KB - 1);
+                            const int64_t ib = i0 + min(b, KB - 1 - kb0);
                             v[j][b] = kNoDq ? __ldg(a.c.absmax + ib)
                                             : __fmaf_rn(e4m3_to_f32(__ldg(a.c.qabsmax + ib)), __ldg(a.c.s2 + (ib >> 8)), mean);
                         }
                     }
                 }
+                const int nss = ss < ss_hi ? ss + 1 : ss_lo;
+                if (ss == ss_hi) more = it.next(tl);
+                if (more) load(tl, nss);
 #pragma unroll
                 for (int st = 0; st < 4; ++st) {
                     const int kt = 4 * ss + st;
-                    if (kt < k0 || kt >= k1 || !ok) continue;
-                    const int s = g % L::kPK;
-                    if (g >= L::kPK &&
-                        !__all_sync(0xFFFFFFFFu, mbar_wait_sleep(k_empty + s, static_cast<uint32_t>(g / L::kPK - 1) & 1u, tmo,
+                    if (kt < kr.lo || kt >= kr.hi || !ok) continue;
+                    const int s = g % L::kPC;
+                    if (g >= L::kPC &&
+                        !__all_sync(0xFFFFFFFFu, mbar_wait_sleep(c_empty + s, static_cast<uint32_t>(g / L::kPC - 1) & 1u, tmo,
                                                                  a.status))) {
                         *abort_flag = 1;
                         ok = false;
@@ -359,90 +379,105 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int b = 0; b < 4; ++b) cs[b * 64 + nl] = live ? v[2 * st + jj][b] : 0.0f;
                         }
                     }
-                    mbar_arrive(k_full + s);
+                    __syncwarp();
+                    const int G = (g0 + kt - kr.lo) & (kGroups - 1);
+                    if (lane == 0) mbar_arrive(c_full + 2 * G + ((par >> G) & 1u));
+                    par ^= 1u << G;
                     ++g;
                 }
             }
+            g0 += steps;
             ok = __all_sync(0xFFFFFFFFu, ok);
         }
     } else {
         // ---------------------------------------- dequantise, then epilogue --
-        const int G = warp >> 3;
-        const int t = threadIdx.x & 255;  // the thread's 64-weight block of a step
+        const int G = warp >> 2;            // group, and its weight stage
+        const int t = threadIdx.x & 127;    // the thread's two 64-weight blocks of a step: t and t + 128
         const bool leader = t == 0;
-        const int q = warp & 3, h = (warp >> 2) & 1;
+        const int q = warp & 3, h = (warp >> 2) & 1, part = warp >> 3;
+        uint8_t* wst = smem + L::kOffW + G * kWStage;
         bool ok = true;
-        int g = 0, gk = 0, n = 0;
+        int g0 = 0, gk0 = 0, n = 0;  // steps and reduction steps before this tile
+        int jobs = 0, kjobs = 0;     // steps and reduction steps of this group
         while (ok && it.next(tl)) {
-            for (int i = 0; ok && i < steps; ++i, ++g) {
-                const int gk_i = gk;
-                if (i < nk) ++gk;
-                if ((g & 1) != G) continue;
-                const int sw = g % kPW;
-                if (g >= kPW)
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(w_empty + sw, static_cast<uint32_t>(g / kPW - 1) & 1u, tmo, a.status));
-                if (!ok) break;
-                uint8_t* wst = smem + L::kOffW + sw * kWStage;
+            for (int i = (G - g0) & (kGroups - 1); ok && i < steps; i += kGroups, ++jobs) {
+                // the weight stage is taken as late as possible: codes and
+                // constants are read before the wait
+                auto wait_stage = [&]() {
+                    return jobs == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(w_empty + G, static_cast<uint32_t>(jobs - 1) & 1u, tmo,
+                                                                          a.status));
+                };
                 if (i < nk) {
-                    const int sc = gk_i % L::kPC, sk = gk_i % L::kPK;
-                    ok = __all_sync(0xFFFFFFFFu,
-                                    mbar_wait(k_full + sk, static_cast<uint32_t>(gk_i / L::kPK) & 1u, tmo, a.status) &&
-                                        mbar_wait(c_full + sc, static_cast<uint32_t>(gk_i / L::kPC) & 1u, tmo, a.status));
+                    const int gk = gk0 + i, sc = gk % L::kPC;
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(c_full + 2 * G + (kjobs & 1), static_cast<uint32_t>(kjobs >> 1) & 1u, tmo,
+                                                           a.status));
                     if (!ok) break;
+                    ++kjobs;
                     const uint32_t codes = smem_u32(smem + L::kOffC + sc * kCStage);
-                    const float* cs = reinterpret_cast<const float*>(smem + L::kOffK + sk * kKStage);
-                    const float cprime = cs[t];
-                    uint32_t c0, c1, dst, swz;
+                    const float* cs = reinterpret_cast<const float*>(smem + L::kOffK + sc * kKStage);
+                    const float cp[2] = {cs[t], cs[t + 128]};
+                    uint4 ca[2], cb[2];
+                    uint32_t dst[2], swz;
                     if (!kTransW) {
-                        // row t of the weight tile: 32 code bytes, 32-byte swizzle
-                        const uint32_t crow = codes + t * 32, s32 = (t >> 2) & 1;
-                        c0 = crow + ((0 ^ s32) << 4);
-                        c1 = crow + ((1 ^ s32) << 4);
-                        dst = smem_u32(wst) + t * 128;
+                        // rows t and t + 128 of the weight tile: 32 code bytes, 32-byte swizzle
+                        const uint32_t s32 = (t >> 2) & 1;
                         swz = t & 7;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const uint32_t crow = codes + (t + 128 * u) * 32;
+                            ca[u] = lds128(crow + ((0 ^ s32) << 4));
+                            cb[u] = lds128(crow + ((1 ^ s32) << 4));
+                            dst[u] = smem_u32(wst) + (t + 128 * u) * 128;
+                        }
                     } else {
-                        // reduction row nl, k-block b of the tile's four
+                        // reduction row nl, k-blocks b and b + 2 of the tile's four
                         const uint32_t nl = t & 63, b = t >> 6;
                         const uint32_t crow = codes + nl * 128;
                         swz = nl & 7;
-                        c0 = crow + (((2 * b) ^ swz) << 4);
-                        c1 = crow + (((2 * b + 1) ^ swz) << 4);
-                        dst = smem_u32(wst) + b * 8192 + (nl >> 3) * 1024 + (nl & 7) * 128;
-                    }
-                    const uint4 ca = lds128(c0), cb = lds128(c1);
-                    const Nf4BlockLut lut = make_block_lut(tab.level, cprime);
-                    __syncwarp();
-                    if (lane == 0) {  // codes and constants have been read
-                        mbar_arrive(c_empty + sc);
-                        mbar_arrive(k_empty + sk);
-                    }
-                    const uint32_t words[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        uint32_t o[4];
-                        lut_decode8_sx(lut, words[j], o);
-                        sts128(dst + ((static_cast<uint32_t>(j) ^ swz) << 4), o);
+                        for (int u = 0; u < 2; ++u) {
+                            ca[u] = lds128(crow + (((2 * b + 4 * u) ^ swz) << 4));
+                            cb[u] = lds128(crow + (((2 * b + 4 * u + 1) ^ swz) << 4));
+                            dst[u] = smem_u32(wst) + (b + 2 * u) * 8192 + (nl >> 3) * 1024 + (nl & 7) * 128;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(c_empty + sc);  // codes and constants have been read
+                    if (!(ok = wait_stage())) break;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const Nf4BlockLut lut = make_block_lut(tab.level, cp[u]);
+                        const uint32_t words[8] = {ca[u].x, ca[u].y, ca[u].z, ca[u].w, cb[u].x, cb[u].y, cb[u].z, cb[u].w};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            uint32_t o[4];
+                            lut_decode8_sx(lut, words[j], o);
+                            sts128(dst[u] + ((static_cast<uint32_t>(j) ^ swz) << 4), o);
+                        }
                     }
                     fence_proxy_async_smem();  // -> visible to the tensor core
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(w_full + sw);
+                    if (lane == 0) mbar_arrive(w_full + G);
                 } else {
                     // rank-r step: B_e rows (forward) or A_e columns (dX) by TMA
+                    if (!(ok = wait_stage())) break;
                     if (leader) {
-                        mbar_arrive_expect_tx(w_full + sw, kWStage);
+                        mbar_arrive_expect_tx(w_full + G, kWStage);
                         if (!kTransW) {
-                            tma_load_3d(wst, &tm_lw, w_full + sw, 0, tl.w0, tl.e);
+                            tma_load_3d(wst, &tm_lw, w_full + G, 0, tl.w0, tl.e);
                         } else {
                             for (int b = 0; b < 4; ++b)
-                                tma_load_3d(wst + b * 8192, &tm_lw, w_full + sw, tl.w0 + 64 * b, 0, tl.e);
+                                tma_load_3d(wst + b * 8192, &tm_lw, w_full + G, tl.w0 + 64 * b, 0, tl.e);
                         }
                     } else if (lane == 0) {
-                        mbar_arrive(w_full + sw);
+                        mbar_arrive(w_full + G);
                     }
                     __syncwarp();
                 }
             }
             if (!ok) break;
+            g0 += steps;
+            gk0 += nk;
 
             // ------------------------------------------------ epilogue --
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc, static_cast<uint32_t>(n) & 1u, tmo, a.status));
@@ -457,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // covers two 64-byte row segments
                 const int col = tl.w0 + (nl & ~1);
                 const bool col_ok = col < a.out_cols;
-                for (int c = G * 32; c < tl.rows; c += 64) {
+                for (int c = part * 32; c < tl.rows; c += 64) {
                     uint32_t r[32];
                     tmem_ld32(trow + c, r);
                     tmem_ld_wait();
@@ -480,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // tile: every UMMA that reads them has completed, and only
                 // these warps refill them)
                 float* buf = reinterpret_cast<float*>(smem + L::kOffW);
-                for (int c = G * 32; c < tl.rows; c += 64) {
+                for (int c = part * 32; c < tl.rows; c += 64) {
                     uint32_t r[32];
                     tmem_ld32(trow + c, r);
                     tmem_ld_wait();
@@ -523,10 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) {
             *abort_flag = 1;
-            // a rank-r tile may still be landing in a weight stage
-            if (leader && g >= 1)
-                for (int j = max(0, g - kPW); j <= g; ++j)
-                    if ((j & 1) == G) mbar_wait(w_full + j % kPW, static_cast<uint32_t>(j / kPW) & 1u, tmo, nullptr);
+            // a rank-r tile may still be landing in the weight stage
+            if (leader)
+                for (int j = max(0, jobs - 1); j <= jobs; ++j) mbar_wait(w_full + G, static_cast<uint32_t>(j) & 1u, tmo, nullptr);
         }
         __syncwarp();
     }
