@@ -22,10 +22,9 @@
 //   warp 16     TMA producer of the token tiles
 //   warp 17     TMA producer of the packed codes
 //   warp 18     TMEM owner, UMMA issuer
-//   warp 19     block constants c' (E4M3 code, second-level scale, mean, or the
-//               fp32 constant) straight from the stored form, four reduction
-//               steps at a time; no transposed copy of an expert stack's
-//               constants is written, most of which few tokens would not use
+// Block constants are read from the stored form by the threads that use them;
+// no transposed copy of an expert stack's constants is written, most of which
+// few tokens would not use.
 //
 // Few tokens. With fewer tiles than SMs a cluster of S CTAs shares a tile,
 // each taking 1/S of the reduction; the partial sums (at most 64 tokens x 256
@@ -41,12 +40,11 @@ namespace {
 
 constexpr int kDeqWarps = 16;
 constexpr int kGroups = 4, kGroupWarps = 4;
-constexpr int kWarpX = 16, kWarpC = 17, kWarpMma = 18, kWarpK = 19;
-constexpr int kThreads = (kWarpK + 1) * 32;
+constexpr int kWarpX = 16, kWarpC = 17, kWarpMma = 18;
+constexpr int kThreads = (kWarpMma + 1) * 32;
 constexpr int kPW = kGroups;                 // weight stages: one per group
 constexpr uint32_t kWStage = 256 * 64 * 2;   // 32 KB
 constexpr uint32_t kCStage = 256 * 64 / 2;   // 8 KB of packed codes
-constexpr uint32_t kKStage = 1024;           // 256 block constants
 constexpr uint32_t kTmemCols = 512;
 
 // Shared memory by token capacity: 256 tokens leave room for two token and
@@ -59,8 +57,7 @@ struct Lay {
     static constexpr uint32_t kXStage = CAP * 128;
     static constexpr uint32_t kOffW = kPX * kXStage;
     static constexpr uint32_t kOffC = kOffW + kPW * kWStage;
-    static constexpr uint32_t kOffK = kOffC + kPC * kCStage;
-    static constexpr uint32_t kOffSched = kOffK + kPC * kKStage;
+    static constexpr uint32_t kOffSched = kOffC + kPC * kCStage;
     static constexpr uint32_t kOffBar = (kOffSched + sizeof(TileSched) + 63) / 64 * 64;
     static constexpr uint32_t kBytes = kOffBar + 512 + 1024;
 };
@@ -115,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     static_assert((2 * L::kPX + 2 * kPW + 2 * kGroups + L::kPC + 5) * 8 + 8 <= 512, "barriers");
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int S = a.splits;
     const int crank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int cl = static_cast<int>(blockIdx.x) / S, ncl = static_cast<int>(gridDim.x) / S;
@@ -135,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(w_full + s, kGroupWarps);
             mbar_init(w_empty + s, 1);
         }
-        for (int s = 0; s < 2 * kGroups; ++s) mbar_init(c_full + s, 2);  // the code producer (+ its bytes) and the constants
+        for (int s = 0; s < 2 * kGroups; ++s) mbar_init(c_full + s, 1);
         for (int s = 0; s < L::kPC; ++s) mbar_init(c_empty + s, kGroupWarps);
         mbar_init(acc, 1);
         mbar_init(tmem_free, kDeqWarps);
@@ -247,15 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kWk = (kTransW ? 2048 : 32) / 16;
         int g = 0, n = 0;
         bool ok = true;
-        while (ok && it.next(tl)) {
+        while (ok && uniform(it.next(tl))) {
             if (n > 0 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(tmem_free, static_cast<uint32_t>(n - 1) & 1u, tmo, a.status))))
                 break;
             tc_fence_after();
-            const uint32_t idesc = idesc_bf16(128, (tl.rows + 15) & ~15, kTransW, false);
+            const uint32_t idesc = idesc_bf16(128, uniform((tl.rows + 15) & ~15), kTransW, false);
             for (int i = 0; i < steps; ++i, ++g) {
                 const int sx = g % L::kPX, sw = g % kPW;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(x_full + sx, static_cast<uint32_t>(g / L::kPX) & 1u, tmo, a.status) &&
-                                                 mbar_wait(w_full + sw, static_cast<uint32_t>(g / kPW) & 1u, tmo, a.status));
+                ok = wait_both(x_full + sx, static_cast<uint32_t>(g / L::kPX) & 1u, w_full + sw,
+                               static_cast<uint32_t>(g / kPW) & 1u, tmo, a.status);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
@@ -287,108 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) umma_commit(drain);
         mbar_wait(drain, 0u, tmo, nullptr);
         __syncwarp();
-    } else if (warp >= kWarpK) {
-        // ----------------------------------------------- block constants --
-        // super-step ss: reduction steps 4 ss .. 4 ss + 3, 256 items of four
-        // constants: forward, item = weight row, four consecutive k-blocks;
-        // dX, item = reduction row, the tile's four k-blocks. The next
-        // super-step's words are loaded before this one's are written.
-        const int KB = static_cast<int>(a.K / kBlock);
-        const bool vec = KB % 4 == 0;  // an item's constants are one aligned word (float4) of one group
-        const float mean = kNoDq ? 0.0f : __ldg(a.c.mean);
-        const int ss_lo = kr.lo >> 2, ss_hi = (kr.hi - 1) >> 2;
-        uint32_t qw[8];
-        float sv[8];
-        auto index = [&](const Tile& tile, int ss, int j) {  // first constant of item lane + 32 j
-            const int n = min((kTransW ? ss * 256 : tile.w0) + lane + 32 * j, static_cast<int>(a.N) - 1);
-            return (static_cast<int64_t>(tile.e) * a.N + n) * KB + (kTransW ? tile.w0 / kBlock : 4 * ss);
-        };
-        auto load = [&](const Tile& tile, int ss) {
-            if (kNoDq || !vec) return;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t ib = index(tile, ss, j);
-                qw[j] = __ldg(reinterpret_cast<const uint32_t*>(a.c.qabsmax + ib));
-                sv[j] = __ldg(a.c.s2 + (ib >> 8));
-            }
-        };
-        int g = 0, g0 = 0;
-        uint32_t par = 0;
-        bool ok = true, more = it.next(tl);
-        if (more) load(tl, ss_lo);
-        while (ok && more) {
-            for (int ss = ss_lo; ok && ss <= ss_hi; ++ss) {
-                float v[8][4];
-                if (kNoDq && vec) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float4 f = __ldg(reinterpret_cast<const float4*>(a.c.absmax + index(tl, ss, j)));
-                        v[j][0] = f.x;
-                        v[j][1] = f.y;
-                        v[j][2] = f.z;
-                        v[j][3] = f.w;
-                    }
-                } else if (vec) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) v[j][b] = __fmaf_rn(e4m3_to_f32(qw[j] >> (8 * b)), sv[j], mean);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int64_t i0 = index(tl, ss, j);
-                        const int kb0 = kTransW ? tl.w0 / kBlock : 4 * ss;
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const int64_t ib = i0 + min(b, KB - 1 - kb0);
-                            v[j][b] = kNoDq ? __ldg(a.c.absmax + ib)
-                                            : __fmaf_rn(e4m3_to_f32(__ldg(a.c.qabsmax + ib)), __ldg(a.c.s2 + (ib >> 8)), mean);
-                        }
-                    }
-                }
-                const int nss = ss < ss_hi ? ss + 1 : ss_lo;
-                if (ss == ss_hi) more = it.next(tl);
-                if (more) load(tl, nss);
-#pragma unroll
-                for (int st = 0; st < 4; ++st) {
-                    const int kt = 4 * ss + st;
-                    if (kt < kr.lo || kt >= kr.hi || !ok) continue;
-                    const int s = g % L::kPC;
-                    if (g >= L::kPC &&
-                        !__all_sync(0xFFFFFFFFu, mbar_wait_sleep(c_empty + s, static_cast<uint32_t>(g / L::kPC - 1) & 1u, tmo,
-                                                                 a.status))) {
-                        *abort_flag = 1;
-                        ok = false;
-                        continue;
-                    }
-                    if (__any_sync(0xFFFFFFFFu, *abort_flag)) {
-                        ok = false;
-                        continue;
-                    }
-                    float* cs = reinterpret_cast<float*>(smem + L::kOffK + s * kKStage);
-                    if (!kTransW) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) cs[lane + 32 * j] = v[j][st];
-                    } else {
-                        // reduction row 64 kt + nl; rows past N weigh nothing
-#pragma unroll
-                        for (int jj = 0; jj < 2; ++jj) {
-                            const int nl = lane + 32 * jj;
-                            const bool live = kt * 64 + nl < a.N;
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) cs[b * 64 + nl] = live ? v[2 * st + jj][b] : 0.0f;
-                        }
-                    }
-                    __syncwarp();
-                    const int G = (g0 + kt - kr.lo) & (kGroups - 1);
-                    if (lane == 0) mbar_arrive(c_full + 2 * G + ((par >> G) & 1u));
-                    par ^= 1u << G;
-                    ++g;
-                }
-            }
-            g0 += steps;
-            ok = __all_sync(0xFFFFFFFFu, ok);
-        }
     } else {
         // ---------------------------------------- dequantise, then epilogue --
         const int G = warp >> 2;            // group, and its weight stage
@@ -396,13 +291,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool leader = t == 0;
         const int q = warp & 3, h = (warp >> 2) & 1, part = warp >> 3;
         uint8_t* wst = smem + L::kOffW + G * kWStage;
+        // Block constants come from the stored form in global memory, loaded
+        // one step of this group (four of the CTA) ahead as they stand: E4M3
+        // code and second-level scale, or the fp32 constant. `pit`, `ptl` and
+        // `pi` walk that step's position.
+        const int KB = static_cast<int>(a.K / kBlock);
+        const float mean = kNoDq ? 0.0f : __ldg(a.c.mean);
+        TileIter pit(sched, cl, ncl, tiles_w, a.E);
+        Tile ptl;
+        int pi = G;
+        bool plive = pit.next(ptl);
+        uint32_t raw_q[2] = {0u, 0u};
+        float raw_s[2] = {0.0f, 0.0f};
+        auto load_constants = [&]() {
+            while (plive && pi >= steps) {
+                pi -= steps;
+                plive = pit.next(ptl);
+            }
+            if (!plive || pi >= nk) return;  // nothing left, or the rank-r step
+            const int kt = kr.lo + pi;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                // weight row n and k-block of block u; past the edges of the
+                // expert's weight the nearest one inside (not used: codes 0
+                // there meet zeros of dY or columns that are not written)
+                const int n = min(kTransW ? kt * 64 + (t & 63) : ptl.w0 + t + 128 * u, static_cast<int>(a.N) - 1);
+                const int kb = min(kTransW ? ptl.w0 / kBlock + (t >> 6) + 2 * u : kt, KB - 1);
+                const int64_t ib = (static_cast<int64_t>(ptl.e) * a.N + n) * KB + kb;
+                if (kNoDq) {
+                    raw_s[u] = __ldg(a.c.absmax + ib);
+                } else {
+                    raw_q[u] = __ldg(a.c.qabsmax + ib);
+                    raw_s[u] = __ldg(a.c.s2 + (ib >> 8));
+                }
+            }
+        };
+        load_constants();
         bool ok = true;
         int g0 = 0, gk0 = 0, n = 0;  // steps and reduction steps before this tile
         int jobs = 0, kjobs = 0;     // steps and reduction steps of this group
         while (ok && it.next(tl)) {
             for (int i = (G - g0) & (kGroups - 1); ok && i < steps; i += kGroups, ++jobs) {
-                // the weight stage is taken as late as possible: codes and
-                // constants are read before the wait
+                // the weight stage is taken as late as possible: the codes
+                // are read before the wait
                 auto wait_stage = [&]() {
                     return jobs == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(w_empty + G, static_cast<uint32_t>(jobs - 1) & 1u, tmo,
                                                                           a.status));
@@ -414,8 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     ++kjobs;
                     const uint32_t codes = smem_u32(smem + L::kOffC + sc * kCStage);
-                    const float* cs = reinterpret_cast<const float*>(smem + L::kOffK + sc * kKStage);
-                    const float cp[2] = {cs[t], cs[t + 128]};
+                    const float cp[2] = {kNoDq ? raw_s[0] : __fmaf_rn(e4m3_to_f32(raw_q[0]), raw_s[0], mean),
+                                         kNoDq ? raw_s[1] : __fmaf_rn(e4m3_to_f32(raw_q[1]), raw_s[1], mean)};
+                    pi += kGroups;
+                    load_constants();
                     uint4 ca[2], cb[2];
                     uint32_t dst[2], swz;
                     if (!kTransW) {
@@ -442,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(c_empty + sc);  // codes and constants have been read
+                    if (lane == 0) mbar_arrive(c_empty + sc);  // the codes have been read
                     if (!(ok = wait_stage())) break;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
@@ -460,6 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(w_full + G);
                 } else {
                     // rank-r step: B_e rows (forward) or A_e columns (dX) by TMA
+                    pi += kGroups;
+                    load_constants();
                     if (!(ok = wait_stage())) break;
                     if (leader) {
                         mbar_arrive_expect_tx(w_full + G, kWStage);

@@ -19,11 +19,22 @@ namespace qlora {
 
 constexpr int kMaxExperts = 512;
 
-// One lane of a converged warp. The UMMA issuers of the grouped kernels run
-// their loop with the whole warp and issue under this predicate: descriptors
-// then stay in uniform registers, where a branch on a lane number would move
-// each one there before every UMMA (measured 125 cycles per UMMA, 1000 per
-// 64-deep step of eight).
+// The UMMA issuers of the grouped kernels run their loop with the whole warp
+// and issue under elect_one(). Warp number, loop conditions and tile sizes are
+// broadcast (uniform), so that the compiler keeps counters and descriptors in
+// uniform registers: as per-thread values each one is moved there before every
+// UMMA, which cost about 1000 cycles per 64-deep step of eight UMMAs.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+__device__ __forceinline__ int warp_index() { return uniform(static_cast<int>(threadIdx.x >> 5)); }
+
+// Both phases complete (whole warp, uniform result): one look at each, then
+// the bounded waits.
+__device__ __forceinline__ bool wait_both(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t tmo, int* status) {
+    const bool r0 = mbar_try_wait(smem_u32(b0), p0), r1 = mbar_try_wait(smem_u32(b1), p1);
+    if (__all_sync(0xFFFFFFFFu, r0 && r1)) return true;
+    return __all_sync(0xFFFFFFFFu, mbar_wait(b0, p0, tmo, status) && mbar_wait(b1, p1, tmo, status));
+}
+
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile(
