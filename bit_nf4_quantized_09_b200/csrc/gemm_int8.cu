@@ -311,108 +311,180 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------- quantise rows --
-// One CTA per row: a = max|x|; code = 127 x / a rounded to the nearest
-// integer, halves to even; scale = a / 127. A row of zeros gets codes 0 and
-// scale 0; a row that holds a NaN or an infinity gets codes 0 and scale NaN
-// (its products are NaN, no other row is touched).
+// Per row: a = max|x|; code = 127 x / a rounded to the nearest integer, halves
+// to even; scale = a / 127. A row of zeros gets codes 0 and scale 0; a row
+// that holds a NaN or an infinity gets codes 0 and scale NaN (its products are
+// NaN, no other row is touched).
 //
-// The code is that of the exact quotient: the fp32 product x (127 / a) is at
-// most 2.3e-5 off, so only a value within 1e-4 of a half can round the wrong
-// way, and there 254 |x| is compared with (2 j + 1) a, both exact in 64 bits.
-// Bound by reading the row once (it stays in registers up to K = 8192, is
-// read again from L2 above) and writing a byte per element.
-constexpr int kQThreads = 256;
-constexpr int kQCache = 4;  // 8-element vectors per thread kept in registers
+// The code is that of the exact quotient: the fp32 product p = x (127 / a) is
+// at most 1.6e-5 off, so only a value within 2e-5 of a half j + 1/2 can round
+// the wrong way, and there the sign of 127 |x| - (j + 1/2) a decides: both
+// products as a rounded number and its remainder (fma), whose differences are
+// exact (one look per eight values). Rounding adds and subtracts 1.5 * 2^23
+// (its low byte is the code): the conversion instructions run at a quarter of
+// the rate.
+//
+// Bound by reading the row once and writing a byte per element. One CTA per
+// row, whose values stay in registers between the two passes over them (4
+// vectors of 8 per thread; the rest of a longer row is read again from L2):
+// 128 threads up to 4096 columns, 256 above. A warp per row, with no barrier,
+// was 1.6 times slower on 8192 x 4096 (too few rows in flight), a CTA loading
+// its next row while it works on one 1.3 times (registers).
 
-__device__ __forceinline__ int code_of(float x, float a, float inv) {
-    const float p = x * inv;
-    int k = __float2int_rn(p);
-    if (fabsf(fabsf(p - static_cast<float>(k)) - 0.5f) < 1e-4f) {
-        const int j = static_cast<int>(fabsf(p));                    // |p| is near j + 1/2, from either side
-        const double l = 254.0 * static_cast<double>(fabsf(x)), r = (2.0 * j + 1.0) * static_cast<double>(a);
-        const int m = l < r ? j : (l > r ? j + 1 : j + (j & 1));
-        k = x < 0.0f ? -m : m;
+// Codes of eight values, four to a word.
+__device__ __forceinline__ void codes_of(const float (&x)[8], float a, float inv, uint32_t (&w)[2]) {
+    uint32_t q[8];
+    float off = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float p = x[k] * inv, r = p + 12582912.0f;
+        q[k] = __float_as_uint(r);
+        off = fmaxf(off, fabsf(p - (r - 12582912.0f)));
     }
-    return k;
+    if (off > 0.49998f) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float p = x[k] * inv, ax = fabsf(x[k]);
+            if (fabsf(p - ((p + 12582912.0f) - 12582912.0f)) > 0.49998f) {
+                const float j = truncf(fabsf(p)), h = j + 0.5f;  // |p| is next to h, on either side
+                const float p1 = __fmul_rn(127.0f, ax), h1 = __fmul_rn(h, a);
+                const float d = (p1 - h1) + (__fmaf_rn(127.0f, ax, -p1) - __fmaf_rn(h, a, -h1));
+                const int ji = static_cast<int>(j);
+                const int m = ji + (d > 0.0f || (d == 0.0f && (ji & 1)) ? 1 : 0);
+                q[k] = static_cast<uint32_t>(x[k] < 0.0f ? -m : m);
+            }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        w[h] = __byte_perm(__byte_perm(q[4 * h], q[4 * h + 1], 0x0040), __byte_perm(q[4 * h + 2], q[4 * h + 3], 0x0040), 0x5410);
 }
 
+// Eight consecutive values as they are stored.
 template <bool kBf16>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
-    if (kBf16) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Vec8 {
+    uint4 w[kBf16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
+        if (kBf16) {
+            w[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
+        } else {
+            const uint4* f = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
+            w[0] = __ldg(f);
+            w[kBf16 ? 0 : 1] = __ldg(f + 1);
+        }
+    }
+    __device__ __forceinline__ void zero() {
+        w[0] = w[kBf16 ? 0 : 1] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t a[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+        if (kBf16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(a[i] << 16);
+                v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+            }
+        } else {
+            const uint4 q = w[kBf16 ? 0 : 1];
+            const uint32_t b[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = __uint_as_float(a[i]);
+                v[4 + i] = __uint_as_float(b[i]);
+            }
+        }
+    }
+    // Largest |x| so far as bits of the stored type (bf16 pairwise): a NaN is
+    // above an infinity, both above every number.
+    __device__ __forceinline__ uint32_t top(uint32_t m) const {
+        const uint32_t a[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+        const uint4 q = w[kBf16 ? 0 : 1];
+        const uint32_t b[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            if (kBf16) {
+                m = __vmaxu2(m, a[i] & 0x7FFF7FFFu);
+            } else {
+                m = max(m, a[i] & 0x7FFFFFFFu);
+                m = max(m, b[i] & 0x7FFFFFFFu);
+            }
         }
-    } else {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-        const float4 x = __ldg(f), y = __ldg(f + 1);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+        return m;
     }
-}
+};
 
-template <bool kBf16>
-__global__ void __launch_bounds__(kQThreads) quantize_rows(const void* X, int64_t K, int8_t* codes, float* scale) {
+constexpr int kCache = 4;
+
+template <bool kBf16, int TPR>
+__global__ void __launch_bounds__(TPR, kBf16 ? 1280 / TPR : 1024 / TPR)
+    quantize_rows(const void* X, int64_t K, int8_t* codes, float* scale) {
     asm volatile("griddepcontrol.launch_dependents;");
     const int64_t row = blockIdx.x;
     const int t = threadIdx.x, nv = static_cast<int>(K / 8);
-    __shared__ uint32_t part[kQThreads / 32];
-    float v[kQCache][8];
-    uint32_t top = 0;  // |x| as bits: a NaN is above an infinity, both above every number
+    __shared__ uint32_t part[TPR / 32];
+    Vec8<kBf16> c[kCache];
+    uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < kQCache; ++j) {
-        const int i = t + j * kQThreads;
-        if (i < nv) {
-            load8<kBf16>(X, row * K + 8ll * i, v[j]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
-        }
+    for (int j = 0; j < kCache; ++j) {
+        const int i = t + j * TPR;
+        if (i < nv)
+            c[j].load(X, row * K + 8ll * i);
+        else
+            c[j].zero();
     }
 #pragma unroll
-    for (int j = 0; j < kQCache; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[j][k]) & 0x7FFFFFFFu);
-    for (int i = t + kQCache * kQThreads; i < nv; i += kQThreads) {
-        float w[8];
-        load8<kBf16>(X, row * K + 8ll * i, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(w[k]) & 0x7FFFFFFFu);
+    for (int j = 0; j < kCache; ++j) top = c[j].top(top);
+    for (int i = t + kCache * TPR; i < nv; i += TPR) {
+        Vec8<kBf16> v;
+        v.load(X, row * K + 8ll * i);
+        top = v.top(top);
     }
+    if (kBf16) top = max(top << 16, top & 0x7FFF0000u);  // the larger half, as fp32 bits
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if ((t & 31) == 0) part[t >> 5] = top;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kQThreads / 32; ++i) top = max(top, part[i]);
+    for (int i = 0; i < TPR / 32; ++i) top = max(top, part[i]);
     const bool bad = top >= 0x7F800000u;
     const float amax = __uint_as_float(top);
     if (t == 0) scale[row] = bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 127.0f);
-    // tiny rows are lifted by 2^64 (exact), so that 127 / a stays finite
-    const float lift = top < 0x1F800000u ? 18446744073709551616.0f : 1.0f;
+    // tiny rows are lifted by 2^64 and huge ones lowered, so that 127 / a, its
+    // products and their remainders are normal numbers (what a lowered element
+    // loses is far below half a code)
+    const float lift = top < 0x2F800000u ? 18446744073709551616.0f
+                                         : (top >= 0x6F800000u ? 5.42101086242752217e-20f : 1.0f);
     const float a = amax * lift;
     const bool none = bad || top == 0u;
     const float inv = none ? 0.0f : __fdiv_rn(127.0f, a);
-    auto store = [&](int i, const float (&x)[8]) {
+    auto store = [&](int i, const Vec8<kBf16>& vec) {
         uint32_t w[2] = {0u, 0u};
         if (!none) {
+            float x[8];
+            vec.get(x);
+            if (lift != 1.0f) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                w[k >> 2] |= (static_cast<uint32_t>(code_of(x[k] * lift, a, inv)) & 0xFFu) << (8 * (k & 3));
+                for (int k = 0; k < 8; ++k) x[k] *= lift;
+            }
+            codes_of(x, a, inv, w);
         }
         *reinterpret_cast<uint2*>(codes + row * K + 8ll * i) = make_uint2(w[0], w[1]);
     };
 #pragma unroll
-    for (int j = 0; j < kQCache; ++j) {
-        const int i = t + j * kQThreads;
-        if (i < nv) store(i, v[j]);
+    for (int j = 0; j < kCache; ++j) {
+        const int i = t + j * TPR;
+        if (i < nv) store(i, c[j]);
     }
-    for (int i = t + kQCache * kQThreads; i < nv; i += kQThreads) {
-        float w[8];
-        load8<kBf16>(X, row * K + 8ll * i, w);
-        store(i, w);
+    for (int i = t + kCache * TPR; i < nv; i += TPR) {
+        Vec8<kBf16> v;
+        v.load(X, row * K + 8ll * i);
+        store(i, v);
     }
+}
+
+template <bool kBf16, int TPR>
+cudaError_t launch_quantize(const void* X, int64_t rows, int64_t K, int8_t* codes, float* scale, cudaStream_t st) {
+    quantize_rows<kBf16, TPR><<<static_cast<unsigned>(rows), TPR, 0, st>>>(X, K, codes, scale);
+    return cudaGetLastError();
 }
 
 template <int CAP>
@@ -456,12 +528,11 @@ cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const I
 cudaError_t launch_quantize_rows(const void* X, bool bf16, int64_t rows, int64_t K, int8_t* codes, float* scale,
                                  cudaStream_t st) {
     if (rows < 1 || rows > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    const unsigned grid = static_cast<unsigned>(rows);
-    if (bf16)
-        quantize_rows<true><<<grid, kQThreads, 0, st>>>(X, K, codes, scale);
-    else
-        quantize_rows<false><<<grid, kQThreads, 0, st>>>(X, K, codes, scale);
-    return cudaGetLastError();
+    if (K <= 4096)
+        return bf16 ? launch_quantize<true, 128>(X, rows, K, codes, scale, st)
+                    : launch_quantize<false, 128>(X, rows, K, codes, scale, st);
+    return bf16 ? launch_quantize<true, 256>(X, rows, K, codes, scale, st)
+                : launch_quantize<false, 256>(X, rows, K, codes, scale, st);
 }
 
 }  // namespace qlora
