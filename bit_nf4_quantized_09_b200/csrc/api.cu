@@ -124,7 +124,6 @@ struct DeviceState {
     bool ready = false;
     qlora_status status = QLORA_OK;
     int sms = 0;
-    int clusters[4] = {0, 0, 0, 0};  // resident clusters of 1, 2, 4, 8 of the grouped matmuls' CTAs
 };
 std::mutex g_dev_mu;
 DeviceState g_dev[64];
@@ -133,7 +132,7 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 // Checks the current device once (sm_100, 148-SM class) and opts the big
 // kernels in to their shared-memory sizes.
-qlora_status device_ready(int* sms_out, int* clusters_out = nullptr) {
+qlora_status device_ready(int* sms_out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -153,7 +152,7 @@ qlora_status device_ready(int* sms_out, int* clusters_out = nullptr) {
             d.status = QLORA_ERR_UNSUPPORTED_DEVICE;
         } else if ((e = fused_init_device()) != cudaSuccess || (e = skinny_init_device()) != cudaSuccess ||
                    (e = gemv_mma_init_device()) != cudaSuccess || (e = merge_tc_init_device()) != cudaSuccess ||
-                   (e = expert_gemm_init_device(d.clusters)) != cudaSuccess ||
+                   (e = expert_gemm_init_device()) != cudaSuccess ||
                    (e = expert_rank_init_device()) != cudaSuccess || (e = expert_order_init_device()) != cudaSuccess ||
                    (e = int8_init_device()) != cudaSuccess) {
             d.status = cuda_fail(e, "cudaFuncSetAttribute");
@@ -168,7 +167,6 @@ qlora_status device_ready(int* sms_out, int* clusters_out = nullptr) {
         }
     }
     if (sms_out) *sms_out = d.sms;
-    if (clusters_out) std::copy(d.clusters, d.clusters + 4, clusters_out);
     return d.status;
 }
 
@@ -1352,36 +1350,33 @@ extern "C" qlora_status qlora_quantize_nf4_noalloc(const float* W, int64_t N, in
 // ================================================== layers of experts, int8 ==
 namespace {
 
-// How a grouped matmul cuts its work. Tiles of up to 256 tokens read each
-// weight tile least often; they are taken when they are at least as many as
-// the SMs. Otherwise tiles of up to 64 tokens, and clusters of S CTAs that
-// split a tile's reduction: of S = 1, 2, 4, 8 the one with the least
-// ceil(tiles / clusters) * (steps / S + a tile's fixed cost in steps).
+// How a grouped matmul cuts its rows: tiles of up to 256 tokens read (and
+// decode) each weight tile least often, but are taken whole, one round of the
+// SMs after another; tiles of 64 can share out their last round (tiles.cuh).
+// Taken is what should end first, by the tiles that evenly filled experts would
+// have: a step costs what decoding its weight tile costs (C, 0.7 us) or, with
+// more than about 190 tokens, its UMMAs. Measured, of the matmul alone: 8192
+// rows over 8 experts 722 us in tiles of 256, 1543 rows over 13 experts 70 us
+// (100 us in tiles of 64), 777 rows over 7 narrow experts 54 us (28 us in tiles
+// of 64).
 struct GroupPlan {
-    int cap = 64, splits = 1, ctas = 1;
+    int cap = 64, part_rows = 0;
+    size_t tickets_bytes = 0, part_bytes = 0;
 };
-GroupPlan group_plan(int64_t M, int E, int64_t tiles_w, int64_t steps, const int clusters[4]) {
+GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps) {
     GroupPlan p;
-    const int64_t act = std::min<int64_t>(E, M);  // experts with rows, at most
-    const int64_t avg = cdiv(M, act);
-    const int64_t big = tiles_w * act * cdiv(avg, 256);
-    if (avg > 64 && big >= clusters[0]) {
-        p.cap = 256;
-        p.ctas = clusters[0];
-        return p;
-    }
-    const int64_t tiles = tiles_w * act * cdiv(avg, 64);
-    int64_t best = -1;
-    for (int i = 0; i < 4; ++i) {
-        const int64_t S = int64_t(1) << i;
-        if (clusters[i] < 1 || S > steps) break;
-        const int64_t cost = cdiv(tiles, clusters[i]) * (cdiv(steps, S) + (S > 1 ? 6 : 4));
-        if (best < 0 || cost < best) {
-            best = cost;
-            p.splits = static_cast<int>(S);
-            p.ctas = clusters[i] * static_cast<int>(S);
-        }
-    }
+    const int64_t act = std::max<int64_t>(1, std::min<int64_t>(E, M));  // experts with rows, at most
+    const int64_t avg = std::max<int64_t>(1, cdiv(M, act)), tiles_w = cdiv(cols, 256);
+    const int64_t t64 = tiles_w * act * cdiv(avg, 64), per256 = cdiv(avg, 256), t256 = tiles_w * act * per256;
+    const double step256 = std::max(1.0, static_cast<double>(avg) / per256 / 190.0);
+    const double whole64 = static_cast<double>(cdiv(t64, kPlanSms) * steps);
+    const double cost64 = std::min(whole64, static_cast<double>(t64) * steps / kPlanSms + kFixUp);
+    const double cost256 = static_cast<double>(cdiv(t256, kPlanSms) * steps) * step256;
+    p.cap = avg > 64 && cost256 <= cost64 ? 256 : 64;
+    // an expert adds at most one partly filled token tile
+    p.tickets_bytes = p.cap == 64 ? up256(static_cast<size_t>((M / 64 + act) * tiles_w) * 4) : 0;
+    p.part_rows = p.cap == 64 ? static_cast<int>(std::min<int64_t>(M, 64)) : 0;
+    p.part_bytes = up256(static_cast<size_t>(2 * kPlanSms) * p.part_rows * 256 * 4);
     return p;
 }
 
@@ -1401,15 +1396,21 @@ qlora_status check_experts(int64_t rows, int E, int64_t M, const int32_t* offset
     return QLORA_OK;
 }
 
+// Workspace of an expert call: status word and tickets (cleared per call),
+// partial sums, sT and sU.
 struct ExpertLayout {
-    size_t status = 0, sT = 0, sU = 0, total = 0;
+    size_t header = 0, tickets = 0, part = 0, sT = 0, sU = 0, total = 0;
+    GroupPlan plan;
 };
 constexpr int kTermsT = 2, kTermsU = 3;
-ExpertLayout expert_layout(int op, int64_t M, int r) {
+ExpertLayout expert_layout(int op, int64_t M, int64_t N, int64_t K, int r, int E) {
     ExpertLayout L;
-    L.total = 256;
-    L.sT = L.total;
-    L.total += up256(static_cast<size_t>(M) * kTermsT * r * 2);
+    L.plan = op == QLORA_OP_BWD ? group_plan(M, E, K, cdiv(N, 64)) : group_plan(M, E, N, K / kBlock);
+    L.tickets = 256;
+    L.header = L.tickets + L.plan.tickets_bytes;
+    L.part = L.header;
+    L.sT = L.part + L.plan.part_bytes;
+    L.total = L.sT + up256(static_cast<size_t>(M) * kTermsT * r * 2);
     if (op == QLORA_OP_BWD) {
         L.sU = L.total;
         L.total += up256(static_cast<size_t>(M) * kTermsU * r * 2);
@@ -1421,21 +1422,13 @@ ExpertLayout expert_layout(int op, int64_t M, int r) {
 qlora_status expert_down(bool bwd, const uint16_t* act, int64_t M, int64_t red, const uint16_t* b, int E,
                          const int32_t* offsets, int r, float scale, int terms, uint16_t* out, int* status,
                          cudaStream_t st) {
-    const int NR = rank_pad(r);
-    CUtensorMap ta, tb;
-    QLORA_MAP(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, red, M, red * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, "X");
-    if (bwd)
-        QLORA_MAP(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b, r, red, static_cast<uint64_t>(r) * 2, NR, 64,
-                  swizzle_for_rank(NR), "B", E);
-    else
-        QLORA_MAP(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b, red, r, red * 2, 64, NR, CU_TENSOR_MAP_SWIZZLE_128B, "A", E);
     ExpertDownArgs a{};
     a.offsets = offsets;
     a.E = E;
     a.M = M;
     a.red = red;
     a.r = r;
-    a.NR = NR;
+    a.NR = rank_pad(r);
     a.terms = terms;
     a.scale = scale;
     a.out = out;
@@ -1443,6 +1436,18 @@ qlora_status expert_down(bool bwd, const uint16_t* act, int64_t M, int64_t red, 
     a.status = status;
     a.timeout_ns = timeout_ns();
     if (injected_failure()) return QLORA_ERR_CUDA;
+    if (!bwd && M <= kDownFewRows) {
+        QLORA_LAUNCH(launch_expert_down_few(act, b, a, st), 1, "expert down-projection");
+        return QLORA_OK;
+    }
+    const int NR = a.NR;
+    CUtensorMap ta, tb;
+    QLORA_MAP(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, red, M, red * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, "X");
+    if (bwd)
+        QLORA_MAP(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b, r, red, static_cast<uint64_t>(r) * 2, NR, 64,
+                  swizzle_for_rank(NR), "B", E);
+    else
+        QLORA_MAP(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b, red, r, red * 2, 64, NR, CU_TENSOR_MAP_SWIZZLE_128B, "A", E);
     // an expert adds at most one partial tile
     const int64_t tiles = M / 128 + std::min<int64_t>(E, M);
     QLORA_LAUNCH(launch_expert_down(bwd, ta, tb, a, static_cast<int>(tiles), st), 1, "expert down-projection");
@@ -1452,9 +1457,9 @@ qlora_status expert_down(bool bwd, const uint16_t* act, int64_t M, int64_t red, 
 // Y (forward) or dX of the experts' rows.
 qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_nf4_weight* w, int64_t N, int E,
                            const int32_t* offsets, const uint16_t* rank_in, int terms, const uint16_t* rank_w, int r,
-                           uint16_t* out, int* status, const int* clusters, bool pdl, cudaStream_t st) {
+                           uint16_t* out, uint8_t* base, const ExpertLayout& L, int sms, bool pdl, cudaStream_t st) {
     const int64_t K = w->K, red = dx ? N : K, cols = dx ? K : N;
-    const GroupPlan p = group_plan(M, E, cdiv(cols, 256), cdiv(red, 64), clusters);
+    const GroupPlan& p = L.plan;
     const uint32_t box = p.cap == 256 ? 64 : 16;
     CUtensorMap t_act, t_codes, t_lact, t_lw;
     QLORA_MAP(&t_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, red, M, red * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1482,11 +1487,13 @@ qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_
     a.red = red;
     a.rank_cols = r;
     a.cap = p.cap;
-    a.splits = p.splits;
-    a.ctas = p.ctas;
+    a.ctas = std::min(sms, kPlanSms);
     a.c = constants_of(w);
     a.out = out;
-    a.status = status;
+    a.part = reinterpret_cast<float*>(base + L.part);
+    a.part_rows = p.part_rows;
+    a.tickets = reinterpret_cast<int*>(base + L.tickets);
+    a.status = reinterpret_cast<int*>(base);
     a.timeout_ns = timeout_ns();
     if (injected_failure()) return QLORA_ERR_CUDA;
     QLORA_LAUNCH(launch_expert_gemm(dx, t_act, t_codes, t_lact, t_lw, a, tables(), pdl, st), 1,
@@ -1503,8 +1510,22 @@ qlora_status check_int8_weight(const qlora_int8_weight* w) {
     return QLORA_OK;
 }
 
-size_t int8_workspace(int64_t M, int64_t K) {
-    return 256 + up256(static_cast<size_t>(M) * K) + up256(static_cast<size_t>(M) * 4);
+// Workspace of an int8 call: status word and tickets (cleared per call),
+// partial sums, the tokens' codes and scales.
+struct Int8Layout {
+    size_t header = 0, tickets = 0, part = 0, xq = 0, xs = 0, total = 0;
+    GroupPlan plan;
+};
+Int8Layout int8_layout(int64_t M, int64_t N, int64_t K, int E) {
+    Int8Layout L;
+    L.plan = group_plan(M, E, N, cdiv(K, 128));
+    L.tickets = 256;
+    L.header = L.tickets + L.plan.tickets_bytes;
+    L.part = L.header;
+    L.xq = L.part + L.plan.part_bytes;
+    L.xs = L.xq + up256(static_cast<size_t>(M) * K);
+    L.total = L.xs + up256(static_cast<size_t>(M) * 4);
+    return L;
 }
 
 qlora_status int8_impl(const uint16_t* X, int64_t M, const qlora_int8_weight* w, int64_t N, int E, const int32_t* offsets,
@@ -1513,20 +1534,21 @@ qlora_status int8_impl(const uint16_t* X, int64_t M, const qlora_int8_weight* w,
     if (M == 0) return QLORA_OK;
     if (!X || !Y || !ws) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(X) || !aligned16(Y) || !aligned16(ws)) return QLORA_ERR_MISALIGNED;
-    if (ws_bytes < int8_workspace(M, w->K)) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+    const Int8Layout L = int8_layout(M, N, w->K, E);
+    if (ws_bytes < L.total) return QLORA_ERR_WORKSPACE_TOO_SMALL;
     if (injected_failure()) return QLORA_ERR_CUDA;
-    int sms = 0, clusters[4];
-    qlora_status s = device_ready(&sms, clusters);
+    int sms = 0;
+    qlora_status s = device_ready(&sms);
     if (s != QLORA_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t* base = static_cast<uint8_t*>(ws);
-    int8_t* xq = reinterpret_cast<int8_t*>(base + 256);
-    float* xs = reinterpret_cast<float*>(base + 256 + up256(static_cast<size_t>(M) * w->K));
+    int8_t* xq = reinterpret_cast<int8_t*>(base + L.xq);
+    float* xs = reinterpret_cast<float*>(base + L.xs);
     const int64_t K = w->K;
-    QLORA_TRY(cudaMemsetAsync(base, 0, 256, st), "clear status");
+    QLORA_TRY(cudaMemsetAsync(base, 0, L.header, st), "clear status and tickets");
     if (injected_failure()) return QLORA_ERR_CUDA;
     QLORA_LAUNCH(launch_quantize_rows(X, true, M, K, xq, xs, st), 1, "quantise tokens");
-    const GroupPlan p = group_plan(M, E, cdiv(N, 256), cdiv(K, 128), clusters);
+    const GroupPlan& p = L.plan;
     CUtensorMap tx, tw;
     QLORA_MAP(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, p.cap == 256 ? 64 : 16, CU_TENSOR_MAP_SWIZZLE_128B,
               "token codes");
@@ -1538,11 +1560,13 @@ qlora_status int8_impl(const uint16_t* X, int64_t M, const qlora_int8_weight* w,
     a.N = N;
     a.K = K;
     a.cap = p.cap;
-    a.splits = p.splits;
-    a.ctas = p.ctas;
+    a.ctas = std::min(sms, kPlanSms);
     a.xs = xs;
     a.ws = w->scale;
     a.Y = Y;
+    a.part = reinterpret_cast<int*>(base + L.part);
+    a.part_rows = p.part_rows;
+    a.tickets = reinterpret_cast<int*>(base + L.tickets);
     a.status = reinterpret_cast<int*>(base);
     a.timeout_ns = timeout_ns();
     if (injected_failure()) return QLORA_ERR_CUDA;
@@ -1584,7 +1608,7 @@ qlora_status qlora_expert_order(const int32_t* ids, int64_t M, int E, int32_t* o
 size_t qlora_workspace_bytes_experts(int op, int64_t M, int64_t N, int64_t K, int r, int E) {
     if (N <= 0 || N % 8 != 0 || K <= 0 || K % kBlock != 0 || E < 1 || E > kMaxExperts) return 0;
     if ((op != QLORA_OP_FWD && op != QLORA_OP_BWD) || M < 0 || !rank_ok(r) || !rows_ok(M, E, std::max(N, K))) return 0;
-    return expert_layout(op, M, r).total;
+    return expert_layout(op, M, N, K, r, E).total;
 }
 
 qlora_status qlora_linear_fwd_experts(const uint16_t* X, int64_t M, const qlora_nf4_weight* w, int E,
@@ -1602,21 +1626,21 @@ qlora_status qlora_linear_fwd_experts(const uint16_t* X, int64_t M, const qlora_
     if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || !aligned16(ws) ||
         (sT_save && !aligned16(sT_save)))
         return QLORA_ERR_MISALIGNED;
-    const ExpertLayout L = expert_layout(QLORA_OP_FWD, M, r);
+    const ExpertLayout L = expert_layout(QLORA_OP_FWD, M, N, w->K, r, E);
     if (ws_bytes < L.total) return QLORA_ERR_WORKSPACE_TOO_SMALL;
     if (injected_failure()) return QLORA_ERR_CUDA;
-    int sms = 0, clusters[4];
-    if ((s = device_ready(&sms, clusters)) != QLORA_OK) return s;
+    int sms = 0;
+    if ((s = device_ready(&sms)) != QLORA_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t* base = static_cast<uint8_t*>(ws);
     int* status = reinterpret_cast<int*>(base);
     uint16_t* sT = sT_save ? sT_save : reinterpret_cast<uint16_t*>(base + L.sT);
-    QLORA_TRY(cudaMemsetAsync(base, 0, 256, st), "clear status");
+    QLORA_TRY(cudaMemsetAsync(base, 0, L.header, st), "clear status and tickets");
     if (injected_failure()) return QLORA_ERR_CUDA;
     if ((s = expert_down(false, X, M, w->K, A, E, offsets, r, alpha / static_cast<float>(r), kTermsT, sT, status, st)) !=
         QLORA_OK)
         return s;
-    return expert_matmul(false, X, M, w, N, E, offsets, sT, kTermsT, B, r, Y, status, clusters, true, st);
+    return expert_matmul(false, X, M, w, N, E, offsets, sT, kTermsT, B, r, Y, base, L, sms, true, st);
 }
 
 qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int64_t M, const qlora_nf4_weight* w, int E,
@@ -1634,11 +1658,11 @@ qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int
     if ((M > 0 && (!aligned16(dY) || !aligned16(X) || !aligned16(dX))) || !aligned16(A) || !aligned16(B) ||
         !aligned16(dA) || !aligned16(dB) || !aligned16(ws) || (sT_in && !aligned16(sT_in)))
         return QLORA_ERR_MISALIGNED;
-    const ExpertLayout L = expert_layout(QLORA_OP_BWD, M, r);
+    const ExpertLayout L = expert_layout(QLORA_OP_BWD, M, N, w->K, r, E);
     if (ws_bytes < L.total) return QLORA_ERR_WORKSPACE_TOO_SMALL;
     if (injected_failure()) return QLORA_ERR_CUDA;
-    int sms = 0, clusters[4];
-    if ((s = device_ready(&sms, clusters)) != QLORA_OK) return s;
+    int sms = 0;
+    if ((s = device_ready(&sms)) != QLORA_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t K = w->K;
     if (M == 0) {  // an empty batch: the adapter gradients are exactly zero
@@ -1651,13 +1675,13 @@ qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int
     uint16_t* sU = reinterpret_cast<uint16_t*>(base + L.sU);
     const uint16_t* sT = sT_in ? sT_in : reinterpret_cast<uint16_t*>(base + L.sT);
     const float scale = alpha / static_cast<float>(r);
-    QLORA_TRY(cudaMemsetAsync(base, 0, 256, st), "clear status");
+    QLORA_TRY(cudaMemsetAsync(base, 0, L.header, st), "clear status and tickets");
     if (injected_failure()) return QLORA_ERR_CUDA;
     if (!sT_in && (s = expert_down(false, X, M, K, A, E, offsets, r, scale, kTermsT, reinterpret_cast<uint16_t*>(base + L.sT),
                                    status, st)) != QLORA_OK)
         return s;
     if ((s = expert_down(true, dY, M, N, B, E, offsets, r, scale, kTermsU, sU, status, st)) != QLORA_OK) return s;
-    if ((s = expert_matmul(true, dY, M, w, N, E, offsets, sU, kTermsU, A, r, dX, status, clusters, false, st)) != QLORA_OK)
+    if ((s = expert_matmul(true, dY, M, w, N, E, offsets, sU, kTermsU, A, r, dX, base, L, sms, false, st)) != QLORA_OK)
         return s;
     // dA and dB need only sU and sT: as dX's programmatic dependent their CTAs
     // start on the SMs that dX leaves idle
@@ -1698,7 +1722,7 @@ qlora_status qlora_quantize_int8_bf16(const uint16_t* W, int64_t N, int64_t K, i
 size_t qlora_workspace_bytes_int8(int64_t M, int64_t N, int64_t K, int E) {
     if (N <= 0 || N % 8 != 0 || K <= 0 || K % 16 != 0 || K > kInt8MaxK || E < 1 || E > kMaxExperts) return 0;
     if (M < 0 || !rows_ok(M, E, N)) return 0;
-    return int8_workspace(M, K);
+    return int8_layout(M, N, K, E).total;
 }
 
 qlora_status qlora_linear_int8(const uint16_t* X, int64_t M, const qlora_int8_weight* w, uint16_t* Y, void* ws,

@@ -26,10 +26,8 @@
 // no transposed copy of an expert stack's constants is written, most of which
 // few tokens would not use.
 //
-// Few tokens. With fewer tiles than SMs a cluster of S CTAs shares a tile,
-// each taking 1/S of the reduction; the partial sums (at most 64 tokens x 256
-// columns fp32) are added in rank order through distributed shared memory and
-// written by all S CTAs. Every sum has a fixed order: results are bitwise
+// The work is dealt out in equal ranges of reduction steps (tiles.cuh); parts
+// of a tile meet in global memory, in a fixed order: results are bitwise
 // reproducible.
 #include "kernels.h"
 #include "tiles.cuh"
@@ -69,7 +67,6 @@ static_assert(Lay<256>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "
 // apart (at the least when every second step is a rank-r step), so with at
 // most four stages the first has been consumed before the second is loaded.
 static_assert(Lay<256>::kPC <= 4 && Lay<64>::kPC <= 4, "code stages");
-static_assert(kPW * kWStage >= 64 * 256 * 4, "partial sums of 64 tokens fit the weight stages");
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
     asm volatile(
@@ -77,14 +74,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
             smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
         : "memory");
-}
-
-// The reduction steps of this CTA: split rank c of S takes [c KT / S, (c + 1) KT / S).
-struct Range {
-    int lo, hi;
-};
-__device__ __forceinline__ Range split_range(int KT, int S, int c) {
-    return Range{static_cast<int>(static_cast<int64_t>(c) * KT / S), static_cast<int>(static_cast<int64_t>(c + 1) * KT / S)};
 }
 
 template <bool kTransW, bool kNoDq, int CAP>
@@ -106,20 +95,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* acc = c_empty + L::kPC;
     uint64_t* tmem_free = acc + 1;
     uint64_t* drain = tmem_free + 1;
-    uint64_t* red_full = drain + 1;
-    uint64_t* red_done = red_full + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(red_done + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * L::kPX + 2 * kPW + 2 * kGroups + L::kPC + 5) * 8 + 8 <= 512, "barriers");
+    SharedTiles* pending = reinterpret_cast<SharedTiles*>(const_cast<int*>(abort_flag) + 1);
+    static_assert((2 * L::kPX + 2 * kPW + 2 * kGroups + L::kPC + 3) * 8 + 8 + sizeof(SharedTiles) <= 512, "barriers");
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
-    const int S = a.splits;
-    const int crank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int cl = static_cast<int>(blockIdx.x) / S, ncl = static_cast<int>(gridDim.x) / S;
     const int KT = static_cast<int>((a.red + 63) / 64);
-    const Range kr = split_range(KT, S, crank);
-    const int nk = kr.hi - kr.lo;
-    const int steps = nk + (crank == S - 1 ? 1 : 0);  // the last split also runs the rank-r step
     const int tiles_w = static_cast<int>((a.out_cols + 255) / 256);
     const uint64_t tmo = a.timeout_ns;
 
@@ -137,9 +119,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(acc, 1);
         mbar_init(tmem_free, kDeqWarps);
         mbar_init(drain, 1);
-        mbar_init(red_full, kDeqWarps * S);
-        mbar_init(red_done, kDeqWarps * S);
         *abort_flag = 0;
+        pending->n = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
@@ -156,10 +137,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (S > 1) cluster_sync();  // every CTA's barriers are initialised before remote arrivals
     const uint32_t tmem = *tmem_slot;
-    TileIter it(sched, cl, ncl, tiles_w, a.E);
+    const Ranges ranges(sched.base[a.E] * tiles_w, KT, static_cast<int>(gridDim.x), CAP == 64);
+    SegIter it(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
     Tile tl;
+    // steps of a segment: its reduction steps, and the rank-r step behind a tile's last
+    auto steps_of = [&](const Tile& s) { return s.k_hi - s.k_lo + (s.k_hi == KT ? 1 : 0); };
 
     if (warp == kWarpX) {
         // ------------------------------------------- token-tile producer --
@@ -167,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int g = 0;
             bool waited = false, ok = true;
             while (ok && it.next(tl)) {
-                const int boxes = (tl.rows + L::kBoxRows - 1) / L::kBoxRows;
+                const int boxes = (tl.rows + L::kBoxRows - 1) / L::kBoxRows, nk = tl.k_hi - tl.k_lo, steps = steps_of(tl);
                 for (int i = 0; i < steps; ++i, ++g) {
                     const int s = g % L::kPX;
                     if (g >= L::kPX && !mbar_wait(x_empty + s, static_cast<uint32_t>(g / L::kPX - 1) & 1u, tmo, a.status)) {
@@ -190,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(x_full + s, static_cast<uint32_t>(boxes) * L::kBoxRows * 128u);
                     for (int b = 0; b < boxes; ++b)
                         tma_load_2d(st + b * L::kBoxRows * 128, rank ? &tm_lact : &tm_act, x_full + s,
-                                    rank ? 0 : (kr.lo + i) * 64, tl.row0 + b * L::kBoxRows);
+                                    rank ? 0 : (tl.k_lo + i) * 64, tl.row0 + b * L::kBoxRows);
                 }
             }
             for (int j = max(0, g - L::kPX); j < g; ++j)
@@ -203,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int g = 0, g0 = 0;
             uint32_t par = 0;  // per group, parity of its reduction steps so far
             bool ok = true;
-            for (; ok && it.next(tl); g0 += steps) {
+            for (; ok && it.next(tl); g0 += steps_of(tl)) {
+                const int nk = tl.k_hi - tl.k_lo;
                 for (int i = 0; i < nk; ++i, ++g) {
                     const int s = g % L::kPC, G = (g0 + i) & (kGroups - 1);
                     uint64_t* bar = c_full + 2 * G + ((par >> G) & 1u);
@@ -216,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    const int kt = kr.lo + i;
+                    const int kt = tl.k_lo + i;
                     par ^= 1u << G;
                     mbar_arrive_expect_tx(bar, kCStage);
                     // rows past the expert's N and columns past K read as zeros
@@ -248,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n > 0 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(tmem_free, static_cast<uint32_t>(n - 1) & 1u, tmo, a.status))))
                 break;
             tc_fence_after();
+            const int nk = uniform(tl.k_hi - tl.k_lo), steps = uniform(steps_of(tl));
             const uint32_t idesc = idesc_bf16(128, uniform((tl.rows + 15) & ~15), kTransW, false);
             for (int i = 0; i < steps; ++i, ++g) {
                 const int sx = g % L::kPX, sw = g % kPW;
@@ -297,19 +282,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // `pi` walk that step's position.
         const int KB = static_cast<int>(a.K / kBlock);
         const float mean = kNoDq ? 0.0f : __ldg(a.c.mean);
-        TileIter pit(sched, cl, ncl, tiles_w, a.E);
+        SegIter pit(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
         Tile ptl;
         int pi = G;
         bool plive = pit.next(ptl);
         uint32_t raw_q[2] = {0u, 0u};
         float raw_s[2] = {0.0f, 0.0f};
         auto load_constants = [&]() {
-            while (plive && pi >= steps) {
-                pi -= steps;
+            while (plive && pi >= steps_of(ptl)) {
+                pi -= steps_of(ptl);
                 plive = pit.next(ptl);
             }
-            if (!plive || pi >= nk) return;  // nothing left, or the rank-r step
-            const int kt = kr.lo + pi;
+            if (!plive || pi >= ptl.k_hi - ptl.k_lo) return;  // nothing left, or the rank-r step
+            const int kt = ptl.k_lo + pi;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 // weight row n and k-block of block u; past the edges of the
@@ -331,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int g0 = 0, gk0 = 0, n = 0;  // steps and reduction steps before this tile
         int jobs = 0, kjobs = 0;     // steps and reduction steps of this group
         while (ok && it.next(tl)) {
+            const int nk = tl.k_hi - tl.k_lo, steps = steps_of(tl);
             for (int i = (G - g0) & (kGroups - 1); ok && i < steps; i += kGroups, ++jobs) {
                 // the weight stage is taken as late as possible: the codes
                 // are read before the wait
@@ -410,23 +396,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
             }
-            if (!ok) break;
             g0 += steps;
             gk0 += nk;
 
             // ------------------------------------------------ epilogue --
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc, static_cast<uint32_t>(n) & 1u, tmo, a.status));
-            if (!ok) break;
+            // (a warp whose wait ran out skips the work but meets the others
+            // at the barriers; they leave together)
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc, static_cast<uint32_t>(n) & 1u, tmo, a.status)) && ok;
             tc_fence_after();
             const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * 256;
             const int nl = h * 128 + q * 32 + lane;  // tile row (output column) of this lane
-            if (S == 1) {
+            if (CAP != 64 || nk == KT) {
                 // lane = output column, register = token: two neighbouring
                 // lanes swap halves of a token pair, so each lane stores two
                 // consecutive columns of one token and a warp instruction
                 // covers two 64-byte row segments
                 const int col = tl.w0 + (nl & ~1);
-                const bool col_ok = col < a.out_cols;
+                const bool write = ok && col < a.out_cols;
                 for (int c = part * 32; c < tl.rows; c += 64) {
                     uint32_t r[32];
                     tmem_ld32(trow + c, r);
@@ -437,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
                         const uint32_t lo = (lane & 1) ? got : r[i], hi = (lane & 1) ? r[i + 1] : got;
                         const int tok = c + i + (lane & 1);
-                        if (col_ok && tok < tl.rows)
+                        if (write && tok < tl.rows)
                             *reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(tl.row0 + tok) * a.out_cols + col) =
                                 pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
                     }
@@ -445,51 +431,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(tmem_free);
-            } else {
-                // partial sums into the weight stages (idle until the next
-                // tile: every UMMA that reads them has completed, and only
-                // these warps refill them)
-                float* buf = reinterpret_cast<float*>(smem + L::kOffW);
+            } else if (CAP == 64) {
+                // partial sums [token][256 columns] to this CTA's slot
+                const int slot_floats = a.part_rows * 256;
+                float* mine = a.part + ranges.slot(static_cast<int>(blockIdx.x), tl.id) * slot_floats + nl;
                 for (int c = part * 32; c < tl.rows; c += 64) {
                     uint32_t r[32];
                     tmem_ld32(trow + c, r);
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (c + i < tl.rows) buf[(c + i) * 256 + nl] = __uint_as_float(r[i]);
+                        if (ok && c + i < tl.rows) mine[(c + i) * 256] = __uint_as_float(r[i]);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(tmem_free);
-                    for (int s = 0; s < S; ++s) mbar_arrive_remote(mapa_shared(smem_u32(red_full), s));
-                }
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(red_full, static_cast<uint32_t>(n) & 1u, tmo, a.status));
-                if (!ok) break;
-                // CTA c adds columns [c 256 / S, (c + 1) 256 / S) in rank order
-                const int per4 = 64 / S;  // four-column items per token
-                const uint32_t buf0 = smem_u32(buf);
-                for (int item = threadIdx.x; item < tl.rows * per4; item += kDeqWarps * 32) {
-                    const int tok = item / per4, nc = crank * (256 / S) + 4 * (item % per4);
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int s = 0; s < S; ++s) {
-                        const float4 x = ld_cluster_f4(mapa_shared(buf0 + static_cast<uint32_t>(tok * 256 + nc) * 4u, s));
-                        v.x += x.x;
-                        v.y += x.y;
-                        v.z += x.z;
-                        v.w += x.w;
-                    }
-                    if (tl.w0 + nc < a.out_cols)
-                        *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(tl.row0 + tok) * a.out_cols + tl.w0 + nc) =
-                            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-                }
-                __syncwarp();
-                if (lane == 0)
-                    for (int s = 0; s < S; ++s) mbar_arrive_remote(mapa_shared(smem_u32(red_done), s));
-                // the weight stages are free once every CTA has read them
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(red_done, static_cast<uint32_t>(n) & 1u, tmo, a.status));
+                if (lane == 0) mbar_arrive(tmem_free);
+                if (threadIdx.x == 0) pending->push(tl);
             }
             ++n;
+            ok = all_ok(ok, kDeqWarps * 32);
+        }
+        // The tiles shared with other CTAs, once the loop (and the registers
+        // it needs) is over: their last CTA to come here finishes them.
+        if (CAP == 64) {
+            __threadfence();  // the parts are visible before the tickets
+            ok = all_ok(ok, kDeqWarps * 32);
+            if (threadIdx.x == 0) pending->take_tickets(ranges, a.tickets, ok);
+            all_ok(true, kDeqWarps * 32);
+            __threadfence();
+            for (int k = 0; k < pending->n; ++k) {
+                if (!pending->last[k]) continue;
+                const Tile p = pending->tile[k];
+                uint16_t* out = a.out + static_cast<int64_t>(p.row0) * a.out_cols + p.w0;
+                const int c0 = ranges.first_cta(p.id);
+                add_parts<float4>(a.part, a.part_rows * 256, ranges.slot(c0, p.id), c0, ranges.last_cta(p.id), p.rows,
+                                  static_cast<int>(a.out_cols) - p.w0, static_cast<int>(threadIdx.x), kDeqWarps * 32,
+                                  [&](int tok, int nc, const float4& v) {
+                                      *reinterpret_cast<uint2*>(out + tok * a.out_cols + nc) =
+                                          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                                  });
+            }
         }
         if (!ok) {
             *abort_flag = 1;
@@ -502,7 +483,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (S > 1) cluster_sync();  // no CTA leaves while another may read its shared memory
     if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
@@ -519,15 +499,11 @@ cudaError_t launch_one(const CUtensorMap& act, const CUtensorMap& codes, const C
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Lay<CAP>::kBytes;
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 2 : 1;
+    cfg.numAttrs = pdl ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, expert_gemm<kTransW, kNoDq, CAP>, act, codes, lact, lw, a, tab);
 }
 
@@ -552,37 +528,19 @@ cudaError_t opt_in() {
 
 }  // namespace
 
-cudaError_t expert_gemm_init_device(int clusters_out[4]) {
+cudaError_t expert_gemm_init_device() {
     cudaError_t e;
     if ((e = opt_in<false, false>()) != cudaSuccess || (e = opt_in<false, true>()) != cudaSuccess ||
-        (e = opt_in<true, false>()) != cudaSuccess || (e = opt_in<true, true>()) != cudaSuccess)
+        (e = opt_in<true, false>()) != cudaSuccess)
         return e;
-    // clusters of 1, 2, 4 and 8 CTAs (one CTA per SM) that run at the same time
-    for (int i = 0; i < 4; ++i) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(1u << i);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = Lay<64>::kBytes;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 1u << i;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if ((e = cudaOccupancyMaxActiveClusters(&clusters_out[i], expert_gemm<false, false, 64>, &cfg)) != cudaSuccess)
-            return e;
-    }
-    return cudaSuccess;
+    return opt_in<true, true>();
 }
 
 cudaError_t launch_expert_gemm(bool trans_w, const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact,
                                const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl,
                                cudaStream_t st) {
-    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 1 || a.ctas % a.splits != 0 || (a.cap != 64 && a.cap != 256))
+    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 1 || (a.cap != 64 && a.cap != 256) || a.rank_cols < 1 || a.rank_cols > 64)
         return cudaErrorInvalidValue;
-    if (a.splits != 1 && (a.cap != 64 || (a.splits != 2 && a.splits != 4 && a.splits != 8))) return cudaErrorInvalidValue;
-    if (a.splits > (a.red + 63) / 64 || a.rank_cols < 1 || a.rank_cols > 64) return cudaErrorInvalidValue;
     return trans_w ? launch_dir<true>(act, codes, lact, lw, a, tab, pdl, st)
                    : launch_dir<false>(act, codes, lact, lw, a, tab, pdl, st);
 }

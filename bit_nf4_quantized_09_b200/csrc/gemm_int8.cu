@@ -18,8 +18,8 @@
 //              of which this one is the programmatic dependent)
 //   warp 9     TMA producer of weight codes (starts at once)
 //   warp 10    TMEM owner, UMMA issuer
-// With fewer tiles than SMs a cluster of S CTAs splits the reduction of a
-// tile and adds the int32 partial sums through distributed shared memory.
+// The work is dealt out in equal ranges of reduction steps (tiles.cuh); the
+// int32 parts of a tile meet in global memory.
 #include "kernels.h"
 #include "tiles.cuh"
 
@@ -35,13 +35,11 @@ constexpr uint32_t kTmemCols = 512;
 
 template <int CAP>
 struct Lay {
-    static constexpr int kStages = 3;
+    static constexpr int kStages = CAP == 256 ? 3 : 5;
     static constexpr int kBoxRows = CAP == 256 ? 64 : 16;
     static constexpr uint32_t kXStage = CAP * 128;
     static constexpr uint32_t kOffW = kStages * kXStage;
-    static constexpr uint32_t kOffRed = kOffW + kStages * kWStage;
-    static constexpr uint32_t kRed = CAP == 64 ? 64 * 256 * 4 : 0;  // int32 partial sums of a split
-    static constexpr uint32_t kOffXs = kOffRed + kRed;
+    static constexpr uint32_t kOffXs = kOffW + kStages * kWStage;
     static constexpr uint32_t kOffSched = kOffXs + 1024;
     static constexpr uint32_t kOffBar = (kOffSched + sizeof(TileSched) + 63) / 64 * 64;
     static constexpr uint32_t kBytes = kOffBar + 256 + 1024;
@@ -72,8 +70,6 @@ __device__ __forceinline__ uint32_t idesc_i8(int M, int N) {
     return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory"); }
-
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Int8GemmArgs a) {
@@ -87,18 +83,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* acc = empty + L::kStages;
     uint64_t* tmem_free = acc + 1;
     uint64_t* drain = tmem_free + 1;
-    uint64_t* red_full = drain + 1;
-    uint64_t* red_done = red_full + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(red_done + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    SharedTiles* pending = reinterpret_cast<SharedTiles*>(const_cast<int*>(abort_flag) + 1);
+    static_assert((2 * L::kStages + 3) * 8 + 8 + sizeof(SharedTiles) <= 256, "barriers");
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = a.splits;
-    const int crank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int cl = static_cast<int>(blockIdx.x) / S, ncl = static_cast<int>(gridDim.x) / S;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int KT = static_cast<int>((a.K + 127) / 128);
-    const int k_lo = static_cast<int>(static_cast<int64_t>(crank) * KT / S);
-    const int steps = static_cast<int>(static_cast<int64_t>(crank + 1) * KT / S) - k_lo;
     const int tiles_w = static_cast<int>((a.N + 255) / 256);
     const uint64_t tmo = a.timeout_ns;
 
@@ -110,9 +101,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(acc, 1);
         mbar_init(tmem_free, kEpiWarps);
         mbar_init(drain, 1);
-        mbar_init(red_full, kEpiWarps * S);
-        mbar_init(red_done, kEpiWarps * S);
         *abort_flag = 0;
+        pending->n = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
@@ -127,9 +117,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (S > 1) cluster_sync();
     const uint32_t tmem = *tmem_slot;
-    TileIter it(sched, cl, ncl, tiles_w, a.E);
+    const Ranges ranges(sched.base[a.E] * tiles_w, KT, static_cast<int>(gridDim.x), CAP == 64);
+    SegIter it(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
     Tile tl;
 
     if (warp == kWarpX || warp == kWarpW) {
@@ -140,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             while (ok && it.next(tl)) {
                 const int boxes = (tl.rows + L::kBoxRows - 1) / L::kBoxRows;
-                for (int i = 0; i < steps; ++i, ++g) {
+                for (int k = tl.k_lo; k < tl.k_hi; ++k, ++g) {
                     const int s = g % L::kStages;
                     if (g >= L::kStages &&
                         !mbar_wait(empty + s, static_cast<uint32_t>(g / L::kStages - 1) & 1u, tmo, a.status)) {
@@ -155,11 +145,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (is_x) {
                         mbar_arrive_expect_tx(full + s, static_cast<uint32_t>(boxes) * L::kBoxRows * 128u);
                         for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(smem + s * L::kXStage + b * L::kBoxRows * 128, &tm_x, full + s, (k_lo + i) * 128,
+                            tma_load_2d(smem + s * L::kXStage + b * L::kBoxRows * 128, &tm_x, full + s, k * 128,
                                         tl.row0 + b * L::kBoxRows);
                     } else {
                         mbar_arrive_expect_tx(full + s, kWStage);
-                        tma_load_3d(smem + L::kOffW + s * kWStage, &tm_w, full + s, (k_lo + i) * 128, tl.w0, tl.e);
+                        tma_load_3d(smem + L::kOffW + s * kWStage, &tm_w, full + s, k * 128, tl.w0, tl.e);
                     }
                 }
             }
@@ -168,41 +158,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
-        if (lane == 0) {
-            int g = 0, n = 0;
-            bool ok = true;
-            while (ok && it.next(tl)) {
-                if (n > 0 && !mbar_wait(tmem_free, static_cast<uint32_t>(n - 1) & 1u, tmo, a.status)) {
-                    ok = false;
-                    break;
-                }
+        const bool leader = elect_one();
+        const uint64_t xd0 = sw128_desc(smem_u32(smem), 16, 1024), wd0 = sw128_desc(smem_u32(smem + L::kOffW), 16, 1024);
+        int g = 0, n = 0;
+        bool ok = true;
+        while (ok && uniform(it.next(tl))) {
+            if (n > 0 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(tmem_free, static_cast<uint32_t>(n - 1) & 1u, tmo, a.status))))
+                break;
+            tc_fence_after();
+            const int steps = uniform(tl.k_hi - tl.k_lo);
+            const uint32_t idesc = idesc_i8(128, uniform((tl.rows + 15) & ~15));
+            for (int i = 0; i < steps; ++i, ++g) {
+                const int s = g % L::kStages;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + s, static_cast<uint32_t>(g / L::kStages) & 1u, tmo, a.status));
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t idesc = idesc_i8(128, (tl.rows + 15) & ~15);
-                for (int i = 0; i < steps; ++i, ++g) {
-                    const int s = g % L::kStages;
-                    if (!mbar_wait(full + s, static_cast<uint32_t>(g / L::kStages) & 1u, tmo, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t xt = smem_u32(smem + s * L::kXStage), wt = smem_u32(smem + L::kOffW + s * kWStage);
+                if (leader) {
+                    const uint64_t xd = xd0 + static_cast<uint32_t>(s) * (L::kXStage / 16);
+                    const uint64_t wd = wd0 + static_cast<uint32_t>(s) * (kWStage / 16);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t xd = sw128_desc(xt + kk * 32, 16, 1024);
+                    for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            umma_i8(tmem + h * 256, sw128_desc(wt + h * 16384 + kk * 32, 16, 1024), xd, idesc,
+                            umma_i8(tmem + h * 256, wd + h * (16384 / 16) + kk * 2, xd + kk * 2, idesc,
                                     (i > 0 || kk > 0) ? 1u : 0u);
-                    }
                     umma_commit(empty + s);
+                    if (i == steps - 1) umma_commit(acc);
                 }
-                if (ok) umma_commit(acc);
-                ++n;
+                __syncwarp();
             }
-            if (!ok) *abort_flag = 1;
-            umma_commit(drain);
-            mbar_wait(drain, 0u, tmo, nullptr);
+            ++n;
         }
+        if (!ok) *abort_flag = 1;
+        if (leader) umma_commit(drain);
+        mbar_wait(drain, 0u, tmo, nullptr);
         __syncwarp();
     } else {
         // ------------------------------------------------------ epilogue --
@@ -215,12 +204,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (static_cast<int>(threadIdx.x) < tl.rows) xs_s[threadIdx.x] = __ldcg(a.xs + tl.row0 + threadIdx.x);
             const int64_t wrow = static_cast<int64_t>(tl.e) * a.N;
             const float ws = __ldg(a.ws + wrow + min(tl.w0 + nl, static_cast<int>(a.N) - 1));
-            epi_bar();
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc, static_cast<uint32_t>(n) & 1u, tmo, a.status));
-            if (!ok) *abort_flag = 1;
+            ok = all_ok(ok, kEpiWarps * 32);
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc, static_cast<uint32_t>(n) & 1u, tmo, a.status)) && ok;
             tc_fence_after();
             const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * 256;
-            if (S == 1) {
+            if (CAP != 64 || tl.k_hi - tl.k_lo == KT) {
                 const int col = tl.w0 + (nl & ~1);
                 const bool write = ok && col < a.N;
                 for (int c = 0; c < tl.rows; c += 32) {
@@ -241,68 +229,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(tmem_free);
-            } else {
-                int* buf = reinterpret_cast<int*>(smem + L::kOffRed);
+            } else if (CAP == 64) {
+                // int32 sums [token][256 channels] to this CTA's slot
+                const int slot_ints = a.part_rows * 256;
+                int* mine = a.part + ranges.slot(static_cast<int>(blockIdx.x), tl.id) * slot_ints + nl;
                 for (int c = 0; c < tl.rows; c += 32) {
                     uint32_t r[32];
                     tmem_ld32(trow + c, r);
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (c + i < tl.rows) buf[(c + i) * 256 + nl] = static_cast<int>(r[i]);
+                        if (ok && c + i < tl.rows) mine[(c + i) * 256] = static_cast<int>(r[i]);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(tmem_free);
-                    for (int s = 0; s < S; ++s) mbar_arrive_remote(mapa_shared(smem_u32(red_full), s));
-                }
-                const bool got = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(red_full, static_cast<uint32_t>(n) & 1u, tmo, a.status));
-                ok = ok && got;
-                const int per4 = 64 / S;
-                const uint32_t buf0 = smem_u32(buf);
-                for (int item = threadIdx.x; ok && item < tl.rows * per4; item += kEpiWarps * 32) {
-                    const int tok = item / per4, nc = crank * (256 / S) + 4 * (item % per4);
-                    if (tl.w0 + nc >= a.N) continue;
-                    int v[4] = {0, 0, 0, 0};
-                    for (int s = 0; s < S; ++s) {
-                        const float4 x = ld_cluster_f4(mapa_shared(buf0 + static_cast<uint32_t>(tok * 256 + nc) * 4u, s));
-                        v[0] += __float_as_int(x.x);
-                        v[1] += __float_as_int(x.y);
-                        v[2] += __float_as_int(x.z);
-                        v[3] += __float_as_int(x.w);
-                    }
-                    float y[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        y[j] = __int2float_rn(v[j]) * (xs_s[tok] * __ldg(a.ws + wrow + tl.w0 + nc + j));
-                    *reinterpret_cast<uint2*>(a.Y + static_cast<int64_t>(tl.row0 + tok) * a.N + tl.w0 + nc) =
-                        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-                }
-                __syncwarp();
-                if (lane == 0)
-                    for (int s = 0; s < S; ++s) mbar_arrive_remote(mapa_shared(smem_u32(red_done), s));
-                const bool done = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(red_done, static_cast<uint32_t>(n) & 1u, tmo, a.status));
-                ok = ok && done;
+                if (lane == 0) mbar_arrive(tmem_free);
+                if (threadIdx.x == 0) pending->push(tl);
             }
             ++n;
-            // all epilogue warps leave together (they meet at barriers); this
-            // one also ends the reads of this tile's token scales
-            int all_ok;
-            asm volatile(
-                "{\n\t.reg .pred p, r;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-                "bar.red.and.pred r, 1, %2, p;\n\tselp.s32 %0, 1, 0, r;\n\t}"
-                : "=r"(all_ok)
-                : "r"(ok ? 1 : 0), "n"(kEpiWarps * 32)
-                : "memory");
-            ok = all_ok != 0;
+            // the warps leave together (they meet at barriers); this one also
+            // ends the reads of this tile's token scales
+            ok = all_ok(ok, kEpiWarps * 32);
+        }
+        // the tiles shared with other CTAs: their last CTA to come here finishes them
+        if (CAP == 64) {
+            __threadfence();  // the parts are visible before the tickets
+            ok = all_ok(ok, kEpiWarps * 32);
+            if (threadIdx.x == 0) pending->take_tickets(ranges, a.tickets, ok);
+            all_ok(true, kEpiWarps * 32);
+            __threadfence();
+            for (int k = 0; k < pending->n; ++k) {
+                if (!pending->last[k]) continue;
+                const Tile p = pending->tile[k];
+                uint16_t* out = a.Y + static_cast<int64_t>(p.row0) * a.N + p.w0;
+                const float* ws = a.ws + static_cast<int64_t>(p.e) * a.N + p.w0;
+                const int c0 = ranges.first_cta(p.id);
+                add_parts<int4>(a.part, a.part_rows * 256, ranges.slot(c0, p.id), c0, ranges.last_cta(p.id), p.rows,
+                                static_cast<int>(a.N) - p.w0, static_cast<int>(threadIdx.x), kEpiWarps * 32,
+                                [&](int tok, int nc, const int4& v) {
+                                    const float4 w4 = make_float4(__ldg(ws + nc), __ldg(ws + nc + 1), __ldg(ws + nc + 2),
+                                                                  __ldg(ws + nc + 3));
+                                    const float x = __ldcg(a.xs + p.row0 + tok);
+                                    *reinterpret_cast<uint2*>(out + tok * a.N + nc) =
+                                        make_uint2(pack_bf16x2(__int2float_rn(v.x) * (x * w4.x), __int2float_rn(v.y) * (x * w4.y)),
+                                                   pack_bf16x2(__int2float_rn(v.z) * (x * w4.z), __int2float_rn(v.w) * (x * w4.w)));
+                                });
+            }
         }
         if (!ok) *abort_flag = 1;
     }
 
     tc_fence_before();
     __syncthreads();
-    if (S > 1) cluster_sync();
     if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
@@ -494,15 +472,11 @@ cudaError_t launch_one(const CUtensorMap& x, const CUtensorMap& w, const Int8Gem
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Lay<CAP>::kBytes;
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 2 : 1;
+    cfg.numAttrs = pdl ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, int8_gemm<CAP>, x, w, a);
 }
 
@@ -518,10 +492,7 @@ cudaError_t int8_init_device() {
 
 cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, bool pdl,
                              cudaStream_t st) {
-    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 1 || a.ctas % a.splits != 0 || (a.cap != 64 && a.cap != 256))
-        return cudaErrorInvalidValue;
-    if (a.splits != 1 && (a.cap != 64 || (a.splits != 2 && a.splits != 4 && a.splits != 8))) return cudaErrorInvalidValue;
-    if (a.splits > (a.K + 127) / 128) return cudaErrorInvalidValue;
+    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 1 || (a.cap != 64 && a.cap != 256)) return cudaErrorInvalidValue;
     return a.cap == 256 ? launch_one<256>(x, w, a, pdl, st) : launch_one<64>(x, w, a, pdl, st);
 }
 

@@ -290,9 +290,10 @@ cudaError_t merge_tc_init_device();
 // -------------------------------------------------- rows grouped by expert --
 // Tiles of the grouped matmuls: 256 weight rows x up to `cap` token rows of
 // one expert (64 or 256). `offsets`: device int32 [E + 1], or nullptr for one
-// expert that owns every row. ctas = clusters * splits; clusters of `splits`
-// CTAs (1, or with cap 64 also 2, 4, 8; at most the reduction steps) share a
-// tile's reduction.
+// expert that owns every row. With cap 64 the tiles of the last round may be
+// shared among the `ctas` CTAs; a shared tile goes through `part`, 2 ctas slots
+// of part_rows x 256 words (part_rows at least the rows of a tile), and
+// `tickets`, one per tile, zero before the launch.
 struct ExpertGemmArgs {
     const int* offsets;
     int E;
@@ -301,9 +302,12 @@ struct ExpertGemmArgs {
     int64_t out_cols;     // N (forward) or K (dX)
     int64_t red;          // K (forward) or N (dX)
     int rank_cols;        // r
-    int cap, splits, ctas;
+    int cap, ctas;
     BlockConstants c;     // of the stacked weight, E N rows
     uint16_t* out;        // bf16 [M, out_cols]
+    float* part;
+    int part_rows;
+    int* tickets;
     int* status;
     uint64_t timeout_ns;
 };
@@ -315,8 +319,7 @@ struct ExpertGemmArgs {
 cudaError_t launch_expert_gemm(bool trans_w, const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact,
                                const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl,
                                cudaStream_t st);
-// clusters_out: clusters of 1, 2, 4, 8 CTAs resident at once.
-cudaError_t expert_gemm_init_device(int clusters_out[4]);
+cudaError_t expert_gemm_init_device();
 
 // out[m, k r + j] = term k of scale * (act[m] . B_e[:, j]) for the rows of
 // every expert: term 0 the bf16 rounding, term k that of what is left.
@@ -338,6 +341,10 @@ struct ExpertDownArgs {
 // tiles: 128-row tiles of the grid, at least those of the batch.
 cudaError_t launch_expert_down(bool b_mn, const CUtensorMap& act, const CUtensorMap& b, ExpertDownArgs a, int tiles,
                                cudaStream_t st);
+// The same with b = A for at most kDownFewRows rows, without tensor cores (the
+// tile fields of the arguments are not read).
+constexpr int kDownFewRows = 128;
+cudaError_t launch_expert_down_few(const uint16_t* X, const uint16_t* A, const ExpertDownArgs& a, cudaStream_t st);
 
 // dA[e] = (sum of sU's terms)^T X, dB[e] = dY^T (sum of sT's terms) over the
 // expert's rows, fp32.
@@ -367,10 +374,13 @@ struct Int8GemmArgs {
     const int* offsets;   // as above
     int E;
     int64_t M, N, K;
-    int cap, splits, ctas;
+    int cap, ctas;
     const float* xs;      // [M] token scales
     const float* ws;      // [E N] channel scales
     uint16_t* Y;          // bf16 [M, N]
+    int* part;
+    int part_rows;
+    int* tickets;
     int* status;
     uint64_t timeout_ns;
 };

@@ -264,6 +264,65 @@ __global__ void __launch_bounds__(kThreads, 2)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// A few rows: X A_e^T on the CUDA cores, a CTA per row and eight columns, its
+// eight warps splitting the reduction. Bound by the latency of one pass over
+// 18 K bytes, with every load of a thread in flight at K = 4096. The matmul
+// that depends on this launch gets an SM when this one's CTAs leave it: the
+// tensor-core kernel above holds its SMs 10 us (K = 4096) to 17 us (11008).
+constexpr int kFewThreads = 256;
+__global__ void __launch_bounds__(kFewThreads)
+    expert_down_few(const uint16_t* __restrict__ X, const uint16_t* __restrict__ A, const ExpertDownArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ float part[kFewThreads / 32][8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = static_cast<int>(blockIdx.x), j0 = static_cast<int>(blockIdx.y) * 8;
+    int e = 0, row0 = 0, rows = 0;
+    // the row's expert: tiles of one row, of which the first stands at offset o_0
+    const int first = min(max(__ldg(a.offsets), 0), static_cast<int>(a.M));
+    if (row < first || !find_row_tile(a.offsets, a.E, static_cast<int>(a.M), 1, row - first, &e, &row0, &rows)) return;
+    const int K8 = static_cast<int>(a.red / 8);
+    const uint4* x = reinterpret_cast<const uint4*>(X + static_cast<int64_t>(row) * a.red);
+    const uint4* w = reinterpret_cast<const uint4*>(A + (static_cast<int64_t>(e) * a.r + j0) * a.red);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int i = static_cast<int>(threadIdx.x); i < K8; i += kFewThreads) {
+        const uint4 xv = __ldg(x + i);
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+        uint4 wv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wv[j] = __ldg(w + static_cast<int64_t>(j) * K8 + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t ww[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[j] = __fmaf_rn(__uint_as_float(xw[k] << 16), __uint_as_float(ww[k] << 16), acc[j]);
+                acc[j] = __fmaf_rn(__uint_as_float(xw[k] & 0xFFFF0000u), __uint_as_float(ww[k] & 0xFFFF0000u), acc[j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], d);
+        if (lane == j) part[warp][j] = acc[j];
+    }
+    __syncthreads();
+    if (warp == 0 && lane < 8) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kFewThreads / 32; ++i) v += part[i][lane];
+        v = __fmul_rn(a.scale, v);
+        uint16_t* out = a.out + (static_cast<int64_t>(row) * a.terms) * a.r + j0 + lane;
+        for (int k = 0; k < a.terms; ++k) {
+            const uint32_t h = pack_bf16x2(v, 0.0f) & 0xFFFFu;
+            out[k * a.r] = static_cast<uint16_t>(h);
+            const float hf = __uint_as_float(h << 16);
+            v = isfinite(hf) ? v - hf : 0.0f;
+        }
+    }
+}
+
 // ------------------------------------------------------------------ grads --
 // One CTA per expert and 128 columns of X (dA) or dY (dB); the reduction runs
 // over the expert's rows, 64 at a time. The rows past its end in the last
@@ -460,6 +519,12 @@ cudaError_t launch_expert_down(bool b_mn, const CUtensorMap& act, const CUtensor
     cfg.numAttrs = 1;
     return b_mn ? cudaLaunchKernelEx(&cfg, expert_down<true>, act, b, a)
                 : cudaLaunchKernelEx(&cfg, expert_down<false>, act, b, a);
+}
+
+cudaError_t launch_expert_down_few(const uint16_t* X, const uint16_t* A, const ExpertDownArgs& a, cudaStream_t st) {
+    if (a.M < 1 || a.M > kDownFewRows || a.red % 8 != 0 || a.r % 8 != 0) return cudaErrorInvalidValue;
+    expert_down_few<<<dim3(static_cast<unsigned>(a.M), static_cast<unsigned>(a.r / 8)), kFewThreads, 0, st>>>(X, A, a);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_expert_grads(const CUtensorMap& x, const CUtensorMap& dy, const CUtensorMap& su, const CUtensorMap& st_,

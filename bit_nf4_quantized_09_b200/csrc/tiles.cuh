@@ -8,6 +8,19 @@
 // by weight tile, then by token tile: CTAs that run at the same time share a
 // weight tile's bytes and an expert's rows through L2.
 //
+// CTA c takes the whole tiles c, c + P, c + 2 P, ... of the full rounds of P
+// tiles (neighbouring tiles run at the same time and share rows and weights
+// through L2: dealing each CTA one contiguous range of all tiles instead was
+// 1.3 times slower on 8192 rows). The tiles left over, fewer than P, would
+// leave SMs idle for a round: where it pays, their reduction steps are dealt
+// out in equal contiguous ranges, one per CTA. A CTA that has only part of a
+// tile's steps leaves its partial sums in a slot of global memory and takes a
+// ticket; the last one to come adds the parts in CTA order (whoever it is, the
+// order is the same) and writes the tile. Nobody waits for another CTA. Tiles
+// of 256 tokens are always taken whole: a part of 256 KB costs more to write
+// and read than a round left partly idle (722 us whole, 756 us shared on 8192
+// rows).
+//
 // Offsets are read on the device only, so they are made safe there: clamped to
 // [0, M] and to their running maximum. Rows outside [o_0, o_E) belong to no
 // tile and are never written.
@@ -104,19 +117,79 @@ struct Tile {
     int e;           // expert
     int row0, rows;  // its token rows: 1 <= rows <= cap
     int w0;          // first row of the weight tile
+    int id;          // its place in the list
+    int k_lo, k_hi;  // reduction steps of this segment
 };
 
-// Walks the tiles first, first + stride, ... of a launch.
-struct TileIter {
+// Meeting in memory costs a CTA about 5 us at the end of its range (the parts
+// written and fenced, the ticket, the parts read): eight reduction steps. A
+// range of fewer than four steps is not worth a CTA.
+constexpr int kFixUp = 8, kMinSteps = 4;
+
+// The share-out: `tiles` tiles of `steps` reduction steps over P CTAs. Tiles
+// below `whole` are taken whole; the steps of the others (units in all) go in
+// ranges to Q CTAs, each with at least one step, so that all of the CTAs
+// between the first and the last of a tile hold a part of it.
+struct Ranges {
+    int tiles, steps, P, whole;
+    uint32_t Q, units;  // 32 bits: at most P - 1 tiles, and tiles of 65536 steps or more are taken whole
+    // share: whether tiles may be shared at all
+    __device__ Ranges(int tiles_, int steps_, int ctas, bool share) : tiles(tiles_), steps(steps_), P(ctas) {
+        const int rest = tiles % P;
+        whole = tiles;
+        units = 0;
+        Q = 0;
+        if (share && rest > 0 && steps < 65536 && P <= 256) {
+            const int u = rest * steps;
+            const int q = min(P, max(u / kMinSteps, rest));
+            if ((u + q - 1) / q + kFixUp < steps) {
+                whole = tiles - rest;
+                units = static_cast<uint32_t>(u);
+                Q = static_cast<uint32_t>(q);
+            }
+        }
+    }
+    __device__ int begin(int c) const { return static_cast<int>(static_cast<uint32_t>(c) * units / Q); }
+    __device__ int cta_of(int u) const { return static_cast<int>(((static_cast<uint32_t>(u) + 1u) * Q - 1u) / units); }
+    // The CTAs that share tile `id`, and the slot in which one of them leaves
+    // its part: each touches at most two tiles in part, the one its range
+    // begins in and the one it ends in.
+    __device__ int first_cta(int id) const { return cta_of((id - whole) * steps); }
+    __device__ int last_cta(int id) const { return cta_of((id - whole) * steps + steps - 1); }
+    __device__ int slot(int c, int id) const { return 2 * c + (begin(c) >= (id - whole) * steps ? 0 : 1); }
+};
+static_assert(256ull * 255 * 65536 < (1ull << 32), "32-bit products");
+
+// Walks the segments of CTA c: its whole tiles, then its range.
+struct SegIter {
     const TileSched& s;
-    int t, stride, tiles_w, E, e;
-    __device__ TileIter(const TileSched& sched, int first, int stride_, int tiles_w_, int E_)
-        : s(sched), t(first), stride(stride_), tiles_w(tiles_w_), E(E_), e(0) {}
+    const Ranges& r;
+    int tile, tiles_w, e, u, u1;
+    __device__ SegIter(const TileSched& sched, const Ranges& ranges, int c, int tiles_w_)
+        : s(sched), r(ranges), tile(c), tiles_w(tiles_w_), e(0), u(0), u1(0) {
+        if (static_cast<uint32_t>(c) < r.Q) {
+            u = r.begin(c);
+            u1 = r.begin(c + 1);
+        }
+    }
     __device__ bool next(Tile& out) {
-        if (t >= s.base[E] * tiles_w) return false;
-        while (t >= s.base[e + 1] * tiles_w) ++e;
+        if (tile < r.whole) {
+            out.id = tile;
+            out.k_lo = 0;
+            out.k_hi = r.steps;
+            tile += r.P;
+        } else if (u < u1) {
+            const int local = u / r.steps;
+            out.id = r.whole + local;
+            out.k_lo = u - local * r.steps;
+            out.k_hi = min(r.steps, out.k_lo + u1 - u);
+            u += out.k_hi - out.k_lo;
+        } else {
+            return false;
+        }
+        while (out.id >= s.base[e + 1] * tiles_w) ++e;
         const int n = s.base[e + 1] - s.base[e];  // token tiles of this expert, at least 1
-        const int local = t - s.base[e] * tiles_w;
+        const int local = out.id - s.base[e] * tiles_w;
         const int m = s.off[e + 1] - s.off[e];
         const int per = ((m + n - 1) / n + 15) & ~15;
         const int j = local % n;
@@ -124,10 +197,77 @@ struct TileIter {
         out.w0 = local / n * 256;
         out.row0 = s.off[e] + j * per;
         out.rows = min(per, s.off[e + 1] - out.row0);
-        t += stride;
         return true;
     }
 };
+
+// The tiles a CTA has left a part of (in shared memory; one thread writes).
+struct SharedTiles {
+    int n;
+    int last[2];   // whether this CTA is the last to come, and finishes the tile
+    Tile tile[2];
+    __device__ void push(const Tile& t) { tile[n++] = t; }
+    __device__ void take_tickets(const Ranges& r, int* tickets, bool ok) {
+        for (int k = 0; k < n; ++k)
+            last[k] = ok && atomicAdd(tickets + tile[k].id, 1) == r.last_cta(tile[k].id) - r.first_cta(tile[k].id);
+    }
+};
+
+// Adds the parts of a shared tile (rows x 256 words each) in CTA order and
+// hands every four columns to `put(token, column, sums)`; `threads` threads,
+// this one `t`. The parts lie in slot `slot0` (CTA c0's) and, for the CTAs
+// after it, whose ranges begin inside the tile, in slots 2 c. Eight loads per
+// thread are in flight (four tokens, two parts).
+template <typename T4, typename Put>
+__device__ __forceinline__ void add_parts(const void* part, int slot_words, int slot0, int c0, int c1, int rows, int cols,
+                                          int t, int threads, Put put) {
+    const int nc = 4 * (t & 63);  // threads is a multiple of 64
+    if (nc >= cols) return;
+    const int tstep = threads >> 6;
+    for (int tok = t >> 6; tok < rows; tok += 4 * tstep) {
+        T4 v[4];
+        memset(v, 0, sizeof(v));
+        for (int c = c0; c <= c1; c += 2) {
+            T4 x[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (c + j > c1) break;
+                const T4* src = reinterpret_cast<const T4*>(static_cast<const uint32_t*>(part) +
+                                                            (c + j == c0 ? slot0 : 2 * (c + j)) * slot_words + nc);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (tok + k * tstep < rows) x[j][k] = __ldcg(src + (tok + k * tstep) * 64);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (c + j <= c1) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        v[k].x += x[j][k].x;
+                        v[k].y += x[j][k].y;
+                        v[k].z += x[j][k].z;
+                        v[k].w += x[j][k].w;
+                    }
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (tok + k * tstep < rows) put(tok + k * tstep, nc, v[k]);
+    }
+}
+
+// A barrier of `threads` threads (named barrier 1) that also says whether `ok`
+// held for all of them.
+__device__ __forceinline__ bool all_ok(bool ok, int threads) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, r;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+        "bar.red.and.pred r, 1, %2, p;\n\tselp.s32 %0, 1, 0, r;\n\t}"
+        : "=r"(r)
+        : "r"(ok ? 1 : 0), "r"(threads)
+        : "memory");
+    return r != 0;
+}
 
 // Finds tile `x` of the list of `cap`-row token tiles without keeping the list
 // (one warp; per-expert tiles of exactly cap rows, the last one shorter).

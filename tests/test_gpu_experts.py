@@ -167,13 +167,18 @@ def test_one_expert_equals_a_layer_of_its_own(q, counts):
         off = torch.tensor([0] * (e + 1) + [counts[e]] * (t["E"] - e), dtype=torch.int32, device="cuda")
         Y, sT = q.linear_fwd_experts(t["X"][m].cuda(), w, t["A"].cuda(), t["B"].cuda(), off, t["E"], t["alpha"])
         torch.cuda.synchronize()
-        # another batch may split the reduction another way: both results are
-        # one bf16 rounding off sums that differ by their accumulation errors
-        size = np.abs(f64(t["X"][m])) @ np.abs(What[e * t["N"]:(e + 1) * t["N"]]).T
-        y = f64(g["Y"][m])
-        within("Y", f64(Y), y, 2 * 2.0 ** -8 * np.abs(y) + 2 * acc(t["K"]) * 2 * size)
-        within("sT", f64(sT)[:, :t["r"]], f64(g["sT"][m])[:, :t["r"]],
-               2 * 2.0 ** -8 * np.abs(f64(g["sT"][m])[:, :t["r"]]) + 1e-5)
+        # another batch may split the reduction another way, and round sT the
+        # other way: each result is off by half a bf16 step of its own, by the
+        # accumulation errors, and by sT's rounding, 2^-8 of |sT| |B|
+        A, B = f64(t["A"][e * t["r"]:(e + 1) * t["r"]]), f64(t["B"][e * t["N"]:(e + 1) * t["N"]])
+        X = f64(t["X"][m])
+        sT_, sTa = t["alpha"] / t["r"] * X @ A.T, t["alpha"] / t["r"] * np.abs(X) @ np.abs(A).T
+        size = np.abs(X) @ np.abs(What[e * t["N"]:(e + 1) * t["N"]]).T + sTa @ np.abs(B).T
+        y, s = f64(g["Y"][m]), f64(g["sT"][m])
+        within("Y", f64(Y), y, 2 * (2.0 ** -8 * np.abs(y) + 2.0 ** -8 * np.abs(sT_) @ np.abs(B).T + acc(t["K"]) * size))
+        r = t["r"]
+        within("sT", f64(sT)[:, :r] + f64(sT)[:, r:], s[:, :r] + s[:, r:],
+               2 * (2.0 ** -16 * np.abs(sT_) + acc(t["K"]) * sTa))
 
 
 def test_rows_of_nobody_and_of_other_experts_do_not_leak(q):
