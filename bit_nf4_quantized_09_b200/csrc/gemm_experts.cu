@@ -16,9 +16,9 @@
 //
 // Roles of a persistent CTA (one per SM, 20 warps):
 //   warps 0-15  dequantisers in four groups of four that take the reduction
-//               steps in turn, each with a weight stage of its own (two
-//               64-weight blocks per thread, the exact w_hat = bf16(level c')
-//               through the per-block byte tables); then the epilogue
+//               steps in turn (two 64-weight blocks per thread, the exact
+//               w_hat = bf16(level c') through the per-block byte tables); then
+//               the epilogue
 //   warp 16     TMA producer of the token tiles
 //   warp 17     TMA producer of the packed codes
 //   warp 18     TMEM owner, UMMA issuer
@@ -40,16 +40,17 @@ constexpr int kDeqWarps = 16;
 constexpr int kGroups = 4, kGroupWarps = 4;
 constexpr int kWarpX = 16, kWarpC = 17, kWarpMma = 18;
 constexpr int kThreads = (kWarpMma + 1) * 32;
-constexpr int kPW = kGroups;                 // weight stages: one per group
 constexpr uint32_t kWStage = 256 * 64 * 2;   // 32 KB
 constexpr uint32_t kCStage = 256 * 64 / 2;   // 8 KB of packed codes
 constexpr uint32_t kTmemCols = 512;
 
-// Shared memory by token capacity: 256 tokens leave room for two token and
-// three code stages; with at most 64 there are four of each.
+// Shared memory by token capacity: with 256 tokens three stages of each kind,
+// with at most 64 four. (Two token and four weight stages of 256 tokens: the
+// token copies, 1 us, were not always ahead of the UMMAs; 735 us on 8192 rows.)
 template <int CAP>
 struct Lay {
-    static constexpr int kPX = CAP == 256 ? 2 : 4;
+    static constexpr int kPX = CAP == 256 ? 3 : 4;  // token stages
+    static constexpr int kPW = CAP == 256 ? 3 : 4;  // weight stages
     static constexpr int kPC = CAP == 256 ? 3 : 4;
     static constexpr int kBoxRows = CAP == 256 ? 64 : 16;  // token rows per TMA box
     static constexpr uint32_t kXStage = CAP * 128;
@@ -89,8 +90,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* x_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
     uint64_t* x_empty = x_full + L::kPX;
     uint64_t* w_full = x_empty + L::kPX;
-    uint64_t* w_empty = w_full + kPW;
-    uint64_t* c_full = w_empty + kPW;
+    uint64_t* w_free = w_full + L::kPW;  // per group: the weight stage of its next step has been consumed
+    uint64_t* c_full = w_free + kGroups;
     uint64_t* c_empty = c_full + 2 * kGroups;
     uint64_t* acc = c_empty + L::kPC;
     uint64_t* tmem_free = acc + 1;
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     SharedTiles* pending = reinterpret_cast<SharedTiles*>(const_cast<int*>(abort_flag) + 1);
-    static_assert((2 * L::kPX + 2 * kPW + 2 * kGroups + L::kPC + 3) * 8 + 8 + sizeof(SharedTiles) <= 512, "barriers");
+    static_assert((2 * L::kPX + L::kPW + 3 * kGroups + L::kPC + 3) * 8 + 8 + sizeof(SharedTiles) <= 512, "barriers");
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int KT = static_cast<int>((a.red + 63) / 64);
@@ -110,10 +111,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(x_full + s, 1);
             mbar_init(x_empty + s, 1);
         }
-        for (int s = 0; s < kPW; ++s) {
-            mbar_init(w_full + s, kGroupWarps);
-            mbar_init(w_empty + s, 1);
-        }
+        for (int s = 0; s < L::kPW; ++s) mbar_init(w_full + s, kGroupWarps);
+        for (int s = 0; s < kGroups; ++s) mbar_init(w_free + s, 1);
         for (int s = 0; s < 2 * kGroups; ++s) mbar_init(c_full + s, 1);
         for (int s = 0; s < L::kPC; ++s) mbar_init(c_empty + s, kGroupWarps);
         mbar_init(acc, 1);
@@ -235,9 +234,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nk = uniform(tl.k_hi - tl.k_lo), steps = uniform(steps_of(tl));
             const uint32_t idesc = idesc_bf16(128, uniform((tl.rows + 15) & ~15), kTransW, false);
             for (int i = 0; i < steps; ++i, ++g) {
-                const int sx = g % L::kPX, sw = g % kPW;
+                const int sx = g % L::kPX, sw = g % L::kPW;
                 ok = wait_both(x_full + sx, static_cast<uint32_t>(g / L::kPX) & 1u, w_full + sw,
-                               static_cast<uint32_t>(g / kPW) & 1u, tmo, a.status);
+                               static_cast<uint32_t>(g / L::kPW) & 1u, tmo, a.status);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
@@ -257,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 umma_f16(tmem + h * 256, wd + h * (16384 / 16) + kk * kWk, xd + kk * 2, idesc, 1u);
                     }
                     umma_commit(x_empty + sx);
-                    umma_commit(w_empty + sw);
+                    umma_commit(w_free + ((g + L::kPW) & (kGroups - 1)));  // of step g + kPW, which takes this stage
                     if (i == steps - 1) umma_commit(acc);
                 }
                 __syncwarp();
@@ -275,7 +274,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = threadIdx.x & 127;    // the thread's two 64-weight blocks of a step: t and t + 128
         const bool leader = t == 0;
         const int q = warp & 3, h = (warp >> 2) & 1, part = warp >> 3;
-        uint8_t* wst = smem + L::kOffW + G * kWStage;
         // Block constants come from the stored form in global memory, loaded
         // one step of this group (four of the CTA) ahead as they stand: E4M3
         // code and second-level scale, or the fp32 constant. `pit`, `ptl` and
@@ -320,9 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = (G - g0) & (kGroups - 1); ok && i < steps; i += kGroups, ++jobs) {
                 // the weight stage is taken as late as possible: the codes
                 // are read before the wait
-                auto wait_stage = [&]() {
-                    return jobs == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(w_empty + G, static_cast<uint32_t>(jobs - 1) & 1u, tmo,
-                                                                          a.status));
+                const int sw = (g0 + i) % L::kPW;
+                uint8_t* wst = smem + L::kOffW + sw * kWStage;
+                auto wait_stage = [&]() {  // the first step to take each stage has nothing to wait for
+                    const int uses = jobs - (G < L::kPW ? 1 : 0);
+                    return uses < 0 || __all_sync(0xFFFFFFFFu, mbar_wait(w_free + G, static_cast<uint32_t>(uses) & 1u, tmo,
+                                                                         a.status));
                 };
                 if (i < nk) {
                     const int gk = gk0 + i, sc = gk % L::kPC;
@@ -376,22 +377,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_smem();  // -> visible to the tensor core
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(w_full + G);
+                    if (lane == 0) mbar_arrive(w_full + sw);
                 } else {
                     // rank-r step: B_e rows (forward) or A_e columns (dX) by TMA
                     pi += kGroups;
                     load_constants();
                     if (!(ok = wait_stage())) break;
                     if (leader) {
-                        mbar_arrive_expect_tx(w_full + G, kWStage);
+                        mbar_arrive_expect_tx(w_full + sw, kWStage);
                         if (!kTransW) {
-                            tma_load_3d(wst, &tm_lw, w_full + G, 0, tl.w0, tl.e);
+                            tma_load_3d(wst, &tm_lw, w_full + sw, 0, tl.w0, tl.e);
                         } else {
                             for (int b = 0; b < 4; ++b)
-                                tma_load_3d(wst + b * 8192, &tm_lw, w_full + G, tl.w0 + 64 * b, 0, tl.e);
+                                tma_load_3d(wst + b * 8192, &tm_lw, w_full + sw, tl.w0 + 64 * b, 0, tl.e);
                         }
                     } else if (lane == 0) {
-                        mbar_arrive(w_full + G);
+                        mbar_arrive(w_full + sw);
                     }
                     __syncwarp();
                 }
@@ -474,9 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) {
             *abort_flag = 1;
-            // a rank-r tile may still be landing in the weight stage
+            // a rank-r tile may still be landing in a weight stage
             if (leader)
-                for (int j = max(0, jobs - 1); j <= jobs; ++j) mbar_wait(w_full + G, static_cast<uint32_t>(j) & 1u, tmo, nullptr);
+                for (int j = max(0, g0 - 2 * L::kPW); j < g0 + L::kPW; ++j)
+                    if ((j & (kGroups - 1)) == G)
+                        mbar_wait(w_full + j % L::kPW, static_cast<uint32_t>(j / L::kPW) & 1u, tmo / 8, nullptr);
         }
         __syncwarp();
     }
