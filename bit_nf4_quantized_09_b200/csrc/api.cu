@@ -1685,12 +1685,13 @@ qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int
         return s;
     // dA and dB need only sU and sT: as dX's programmatic dependent their CTAs
     // start on the SMs that dX leaves idle
-    const int NR = rank_pad(r);
     CUtensorMap tx, tdy, tsu, tst;
     QLORA_MAP(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, K, M, K * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "X^T");
     QLORA_MAP(&tdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, N, M, N * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "dY^T");
-    if ((s = make_rank_map(&tsu, sU, M, kTermsU * r, kTermsU * r, NR, "sU")) != QLORA_OK) return s;
-    if ((s = make_rank_map(&tst, sT, M, kTermsT * r, kTermsT * r, NR, "sT")) != QLORA_OK) return s;
+    QLORA_MAP(&tsu, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sU, kTermsU * r, M, static_cast<uint64_t>(kTermsU) * r * 2, 64, 64,
+              CU_TENSOR_MAP_SWIZZLE_128B, "sU");
+    QLORA_MAP(&tst, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sT, kTermsT * r, M, static_cast<uint64_t>(kTermsT) * r * 2, 64, 64,
+              CU_TENSOR_MAP_SWIZZLE_128B, "sT");
     ExpertGradArgs g{};
     g.offsets = offsets;
     g.E = E;
@@ -1698,7 +1699,7 @@ qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int
     g.N = N;
     g.K = K;
     g.r = r;
-    g.NR = NR;
+    g.ctas = std::min(sms, kPlanSms);
     g.terms_u = kTermsU;
     g.terms_t = kTermsT;
     g.dA = dA;

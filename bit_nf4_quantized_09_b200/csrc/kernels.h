@@ -352,16 +352,17 @@ struct ExpertGradArgs {
     const int* offsets;
     int E;
     int64_t M, N, K;
-    int r, NR;
-    int terms_u, terms_t; // terms of sU and sT
+    int r;
+    int terms_u, terms_t; // terms of sU and sT, at most 192 columns each
+    int ctas;             // one per SM
     float* dA;            // [E r, K]
     float* dB;            // [E N, r]
     int stages;           // set by the launcher
     int* status;
     uint64_t timeout_ns;
 };
-// x {K, M}, dy {N, M} box {64, 64} SW128; su {terms_u r, M}, st {terms_t r, M}
-// box {NR, 64} with the NR * 2-byte swizzle.
+// x {K, M}, dy {N, M}, su {terms_u r, M}, st {terms_t r, M}: all box {64, 64}
+// SW128.
 cudaError_t launch_expert_grads(const CUtensorMap& x, const CUtensorMap& dy, const CUtensorMap& su,
                                 const CUtensorMap& st_, ExpertGradArgs a, bool pdl, cudaStream_t st);
 cudaError_t expert_rank_init_device();

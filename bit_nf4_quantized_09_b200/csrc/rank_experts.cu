@@ -324,43 +324,58 @@ __global__ void __launch_bounds__(kFewThreads)
 }
 
 // ------------------------------------------------------------------ grads --
-// One CTA per expert and 128 columns of X (dA) or dY (dB); the reduction runs
-// over the expert's rows, 64 at a time. The rows past its end in the last
-// step belong to other experts (or to nobody): both operands' copies of them
-// are zeroed in shared memory before the UMMA, so whatever they hold, NaN
-// included, adds nothing. An expert without rows gets zeros.
-__global__ void __launch_bounds__(kThreads, 2)
+// Tiles of 128 columns of X (dA) or dY (dB) for each expert, taken by
+// persistent CTAs, one per SM; the reduction runs over the expert's rows, 64 at
+// a time. The terms of sU (sT) stand side by side in memory, and side by side
+// they are the UMMA's N (3 r or 2 r columns): every X or dY tile is read once
+// from shared memory for all of them, and the epilogue adds the terms' columns.
+// The copies of the next tile run ahead of this one's epilogue.
+//
+// The rows past an expert's end in its last step belong to other experts (or to
+// nobody): both operands' copies of them are zeroed in shared memory before the
+// UMMA, so whatever they hold, NaN included, adds nothing. An expert without
+// rows gets zeros.
+constexpr uint32_t kBoxBytes = 64 * 64 * 2;  // 64 rows x 64 columns
+constexpr uint32_t kGradTmem = 512;          // two accumulators of up to 192 columns, 256 apart
+constexpr uint32_t kGradSmem = 208 * 1024;   // all stages
+
+__global__ void __launch_bounds__(kThreads, 1)
     expert_grads(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_dy,
                  const __grid_constant__ CUtensorMap tm_su, const __grid_constant__ CUtensorMap tm_st,
                  const ExpertGradArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
+    __shared__ int off[kMaxExperts + 1];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int tk = static_cast<int>((a.K + 127) / 128), tn = static_cast<int>((a.N + 127) / 128);
-    const int e = static_cast<int>(blockIdx.x) / (tk + tn), local = static_cast<int>(blockIdx.x) % (tk + tn);
-    const bool is_a = local < tk;
-    const int c0 = (is_a ? local : local - tk) * 128;  // first column of X or dY
-    const int NR = a.NR, r = a.r, T = is_a ? a.terms_u : a.terms_t;
-    const uint32_t b_bytes = static_cast<uint32_t>(NR) * 128u;
-    const uint32_t stage = kABytes + static_cast<uint32_t>(max(a.terms_u, a.terms_t)) * b_bytes;
+    const int tiles = a.E * (tk + tn), r = a.r;
+    const int boxes_u = (a.terms_u * r + 63) / 64, boxes_t = (a.terms_t * r + 63) / 64;
+    const uint32_t stage = kABytes + static_cast<uint32_t>(max(boxes_u, boxes_t)) * kBoxBytes;
     const int stages = a.stages;
     const uint64_t tmo = a.timeout_ns;
-    const CUtensorMap* ta = is_a ? &tm_x : &tm_dy;
-    const CUtensorMap* tb = is_a ? &tm_su : &tm_st;
+    // the safe offsets: clamped to [0, M] and to their running maximum
+    for (int i = threadIdx.x; i <= a.E; i += kThreads)
+        off[i] = min(max(__ldg(a.offsets + i), 0), static_cast<int>(a.M));
+    __syncthreads();
     if (warp == 0) {
-        int first, last;
-        expert_rows(a.offsets, e, static_cast<int>(a.M), &first, &last);
+        int top = 0;
+        for (int e0 = 0; e0 <= a.E; e0 += 32) {
+            const int v = max(warp_scan_max(e0 + lane <= a.E ? off[e0 + lane] : 0), top);
+            __syncwarp();
+            if (e0 + lane <= a.E) off[e0 + lane] = v;
+            top = __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
         if (lane == 0) {
-            bars.tile[0] = first;
-            bars.tile[1] = last - first;
             init_bars(&bars, stages);
-            tma_prefetch_desc(ta);
-            tma_prefetch_desc(tb);
+            tma_prefetch_desc(&tm_x);
+            tma_prefetch_desc(&tm_dy);
+            tma_prefetch_desc(&tm_su);
+            tma_prefetch_desc(&tm_st);
         }
     }
     if (warp == 1) {
-        tmem_alloc(&bars.tmem_slot, kTmemCols);
+        tmem_alloc(&bars.tmem_slot, kGradTmem);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -368,124 +383,179 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     const uint32_t tmem = bars.tmem_slot;
     volatile int* abort_flag = &bars.abort_flag;
-    const int row0 = bars.tile[0], m = bars.tile[1];
-    const int steps = (m + 63) / 64, chunks = (steps + kFlush - 1) / kFlush;
-    const int tail = m - (steps - 1) * 64;  // rows of the last step
+
+    struct GTile {
+        int e, c0, row0, m, steps, tail;
+        bool is_a;
+    };
+    auto tile_of = [&](int id) {
+        GTile g;
+        g.e = id / (tk + tn);
+        const int local = id - g.e * (tk + tn);
+        g.is_a = local < tk;
+        g.c0 = (g.is_a ? local : local - tk) * 128;
+        g.row0 = off[g.e];
+        g.m = off[g.e + 1] - g.row0;
+        g.steps = (g.m + 63) / 64;
+        g.tail = g.m - (g.steps - 1) * 64;  // rows of the last step
+        return g;
+    };
 
     if (warp == 0) {
         if (lane == 0) {
-            int i = 0;
-            for (; i < steps; ++i) {
-                const int s = i % stages;
-                if (i >= stages && !mbar_wait(bars.empty + s, static_cast<uint32_t>(i / stages - 1) & 1u, tmo, a.status)) {
-                    *abort_flag = 1;
-                    break;
+            int g = 0;
+            bool ok = true;
+            for (int id = static_cast<int>(blockIdx.x); ok && id < tiles; id += static_cast<int>(gridDim.x)) {
+                const GTile t = tile_of(id);
+                const int boxes = t.is_a ? boxes_u : boxes_t;
+                const CUtensorMap* ta = t.is_a ? &tm_x : &tm_dy;
+                const CUtensorMap* tb = t.is_a ? &tm_su : &tm_st;
+                for (int i = 0; i < t.steps; ++i, ++g) {
+                    const int s = g % stages;
+                    if (g >= stages && !mbar_wait(bars.empty + s, static_cast<uint32_t>(g / stages - 1) & 1u, tmo, a.status)) {
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                    if (*abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    const int row = t.row0 + i * 64;
+                    uint8_t* st = smem + s * stage;
+                    mbar_arrive_expect_tx(bars.full + s, kABytes + static_cast<uint32_t>(boxes) * kBoxBytes);
+                    tma_load_2d(st, ta, bars.full + s, t.c0, row);
+                    tma_load_2d(st + kBoxBytes, ta, bars.full + s, t.c0 + 64, row);
+                    for (int k = 0; k < boxes; ++k)
+                        tma_load_2d(st + kABytes + k * kBoxBytes, tb, bars.full + s, 64 * k, row);
                 }
-                if (*abort_flag) break;
-                const int row = row0 + i * 64;
-                uint8_t* st = smem + s * stage;
-                mbar_arrive_expect_tx(bars.full + s, kABytes + static_cast<uint32_t>(T) * b_bytes);
-                tma_load_2d(st, ta, bars.full + s, c0, row);
-                tma_load_2d(st + 8192, ta, bars.full + s, c0 + 64, row);
-                for (int k = 0; k < T; ++k) tma_load_2d(st + kABytes + k * b_bytes, tb, bars.full + s, k * r, row);
             }
-            for (int j = max(0, i - stages); j < i; ++j)
+            for (int j = max(0, g - stages); j < g; ++j)
                 mbar_wait(bars.full + j % stages, static_cast<uint32_t>(j / stages) & 1u, tmo, nullptr);
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_bf16(128, NR, true, true);
-            bool ok = true;
-            for (int i = 0; ok && i < steps; ++i) {
-                const int s = i % stages, chunk = i / kFlush, p = chunk & 1;
-                if (i % kFlush == 0 && chunk >= 2 &&
-                    !mbar_wait(bars.acc_free + p, static_cast<uint32_t>((chunk >> 1) - 1) & 1u, tmo, a.status))
-                    ok = false;
-                if (ok && !mbar_wait(bars.full + s, static_cast<uint32_t>(i / stages) & 1u, tmo, a.status)) ok = false;
+        const bool leader = elect_one();
+        const uint64_t d0 = sw128_desc(smem_u32(smem), kBoxBytes, 1024);
+        int g = 0, chunk = 0, masks = 0;
+        bool ok = true;
+        for (int id = static_cast<int>(blockIdx.x); ok && id < tiles; id += static_cast<int>(gridDim.x)) {
+            const GTile t = tile_of(id);
+            const int steps = uniform(t.steps), tail = uniform(t.tail);
+            const uint32_t idesc = idesc_bf16(128, uniform(((t.is_a ? a.terms_u : a.terms_t) * r + 15) & ~15), true, true);
+            for (int i = 0; ok && i < steps; ++i, ++g) {
+                const int s = g % stages, p = chunk & 1;
+                if (i % kFlush == 0 && chunk >= 2)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bars.acc_free + p, static_cast<uint32_t>((chunk >> 1) - 1) & 1u, tmo,
+                                                           a.status));
+                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bars.full + s, static_cast<uint32_t>(g / stages) & 1u, tmo, a.status));
                 if (ok && i == steps - 1 && tail < 64) {
-                    mbar_arrive(&bars.tail_in);  // the epilogue warps zero the rows past the end
-                    if (!mbar_wait(&bars.masked, 0u, tmo, a.status)) ok = false;
+                    if (leader) mbar_arrive(&bars.tail_in);  // the epilogue warps zero the rows past the end
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars.masked, static_cast<uint32_t>(masks) & 1u, tmo, a.status));
+                    ++masks;
                 }
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t at = smem_u32(smem + s * stage), bt = at + kABytes;
-                for (int kk = 0; kk < 4; ++kk)
-                    for (int k = 0; k < T; ++k)
-                        umma_f16(tmem + p * 64, sw128_desc(at + kk * 2048, 8192, 1024),
-                                 mn_b_desc(bt + k * b_bytes + kk * 16 * NR * 2, NR), idesc,
-                                 (i % kFlush > 0 || kk > 0 || k > 0) ? 1u : 0u);
-                umma_commit(bars.empty + s);
-                if (i % kFlush == kFlush - 1 || i == steps - 1) umma_commit(bars.acc_full + p);
+                const bool ends = i % kFlush == kFlush - 1 || i == steps - 1;
+                if (leader) {
+                    const uint64_t ad = d0 + static_cast<uint32_t>(s) * (stage / 16), bd = ad + kABytes / 16;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16(tmem + p * 256, ad + kk * (2048 / 16), bd + kk * (2048 / 16), idesc,
+                                 (i % kFlush > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit(bars.empty + s);
+                    if (ends) umma_commit(bars.acc_full + p);
+                }
+                __syncwarp();
+                if (ends) ++chunk;
             }
-            if (!ok) *abort_flag = 1;
-            umma_commit(&bars.drain);
-            mbar_wait(&bars.drain, 0u, tmo, nullptr);
         }
+        if (!ok) *abort_flag = 1;
+        if (leader) umma_commit(&bars.drain);
+        mbar_wait(&bars.drain, 0u, tmo, nullptr);
         __syncwarp();
     } else {
         const int q = warp & 3, t = q * 32 + lane;
-        float v[64];
-#pragma unroll
-        for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+        int g = 0, chunk = 0, masks = 0;
         bool ok = true;
-        for (int c = 0; ok && c < chunks; ++c) {
-            if (c == chunks - 1 && tail < 64) {
-                const int i = steps - 1, s = i % stages;
-                // the issuer has seen the last step land; its stage's barrier
-                // stays in that phase, so its parity is safe to read (these
-                // warps did not follow the phases before it)
-                ok = __all_sync(0xFFFFFFFFu,
-                                mbar_wait(&bars.tail_in, 0u, tmo, a.status) &&
-                                    mbar_wait(bars.full + s, static_cast<uint32_t>(i / stages) & 1u, tmo, a.status));
-                if (!ok) break;
-                const uint32_t st = smem_u32(smem + s * stage);
-                const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-                // A: rows of 128 bytes in two boxes; B: rows of 2 NR bytes per term
-                const int na = (64 - tail) * 8, nb = (64 - tail) * NR / 8;
-                for (int x = t; x < 2 * na; x += 128)
-                    sts128(st + (x / na) * 8192 + tail * 128 + (x % na) * 16, zero);
-                for (int x = t; x < T * nb; x += 128)
-                    sts128(st + kABytes + (x / nb) * b_bytes + tail * NR * 2 + (x % nb) * 16, zero);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.masked);
-            }
-            ok = flush_acc(&bars, tmem, q, lane, NR, c, v, tmo, a.status);
-        }
-        if (!ok) *abort_flag = 1;
-        if (ok && is_a) {
-            if (c0 + t < a.K) {
-                float* out = a.dA + static_cast<int64_t>(e) * r * a.K + c0 + t;
+        for (int id = static_cast<int>(blockIdx.x); ok && id < tiles; id += static_cast<int>(gridDim.x)) {
+            const GTile tl = tile_of(id);
+            const int T = tl.is_a ? a.terms_u : a.terms_t, boxes = tl.is_a ? boxes_u : boxes_t;
+            const int chunks = (tl.steps + kFlush - 1) / kFlush;
+            float v[64];
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    if (j < r) out[static_cast<int64_t>(j) * a.K] = v[j];
+            for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+            for (int c = 0; ok && c < chunks; ++c, ++chunk) {
+                if (c == chunks - 1 && tl.tail < 64) {
+                    // the issuer has seen the last step land; its stage's
+                    // barrier stays in that phase, so its parity is safe to
+                    // read (these warps did not follow the phases before it)
+                    const int gl = g + tl.steps - 1, s = gl % stages;
+                    ok = __all_sync(0xFFFFFFFFu,
+                                    mbar_wait(&bars.tail_in, static_cast<uint32_t>(masks) & 1u, tmo, a.status) &&
+                                        mbar_wait(bars.full + s, static_cast<uint32_t>(gl / stages) & 1u, tmo, a.status));
+                    if (!ok) break;
+                    ++masks;
+                    const uint32_t st = smem_u32(smem + s * stage) + static_cast<uint32_t>(tl.tail) * 128u;
+                    const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+                    const int n = (64 - tl.tail) * 8;  // 16-byte pieces of a box: rows of 128 bytes
+                    for (int b = 0; b < 2 + boxes; ++b)
+                        for (int x = t; x < n; x += 128) sts128(st + static_cast<uint32_t>(b) * kBoxBytes + x * 16, zero);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.masked);
+                }
+                const int p = chunk & 1;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bars.acc_full + p, static_cast<uint32_t>(chunk >> 1) & 1u, tmo, a.status));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + p * 256;
+                for (int k = 0; k < T; ++k) {
+#pragma unroll
+                    for (int c0 = 0; c0 < 64; c0 += 16) {
+                        if (c0 < r) {
+                            uint32_t x[16];
+                            tmem_ld16(acc + k * r + c0, x);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[c0 + i] += __uint_as_float(x[i]);  // of r = 8, the first eight are used
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.acc_free + p);
             }
-        } else if (ok) {
-            if (c0 + t < a.N) {
-                float4* out = reinterpret_cast<float4*>(a.dB + (static_cast<int64_t>(e) * a.N + c0 + t) * r);
+            if (!ok) break;
+            g += tl.steps;
+            if (tl.is_a) {
+                if (tl.c0 + t < a.K) {
+                    float* out = a.dA + static_cast<int64_t>(tl.e) * r * a.K + tl.c0 + t;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (j < r) out[static_cast<int64_t>(j) * a.K] = v[j];
+                }
+            } else if (tl.c0 + t < a.N) {
+                float4* out = reinterpret_cast<float4*>(a.dB + (static_cast<int64_t>(tl.e) * a.N + tl.c0 + t) * r);
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     if (4 * j < r) out[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             }
         }
+        if (!ok) *abort_flag = 1;
     }
 
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, kGradTmem);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 constexpr size_t kDownSmem(int NR, int stages) { return static_cast<size_t>(stages) * (kABytes + NR * 128) + 1024; }
-constexpr size_t kGradSmem(int NR, int terms, int stages) {
-    return static_cast<size_t>(stages) * (kABytes + terms * NR * 128) + 1024;
-}
 constexpr int kDownStages = 4;                 // 72-96 KB: two CTAs per SM
-constexpr size_t kGradBudget = 112 * 1024;     // per CTA, two per SM
 
 }  // namespace
 
@@ -496,7 +566,7 @@ cudaError_t expert_rank_init_device() {
         (e = cudaFuncSetAttribute(expert_down<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, down)) != cudaSuccess)
         return e;
     return cudaFuncSetAttribute(expert_grads, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(kGradBudget));
+                                static_cast<int>(kGradSmem + 1024));
 }
 
 cudaError_t launch_expert_down(bool b_mn, const CUtensorMap& act, const CUtensorMap& b, ExpertDownArgs a, int tiles,
@@ -529,15 +599,15 @@ cudaError_t launch_expert_down_few(const uint16_t* X, const uint16_t* A, const E
 
 cudaError_t launch_expert_grads(const CUtensorMap& x, const CUtensorMap& dy, const CUtensorMap& su, const CUtensorMap& st_,
                                 ExpertGradArgs a, bool pdl, cudaStream_t st) {
-    const int terms = std::max(a.terms_u, a.terms_t);
-    a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kGradBudget - 1024) / (kABytes + terms * a.NR * 128)));
-    if (a.stages < 2) return cudaErrorInvalidValue;
+    const int boxes = (std::max(a.terms_u, a.terms_t) * a.r + 63) / 64;
+    if (a.r < 8 || boxes < 1 || boxes > 3 || a.E < 1 || a.E > kMaxExperts || a.ctas < 1) return cudaErrorInvalidValue;
+    a.stages = static_cast<int>(std::min<size_t>(kMaxStages, kGradSmem / (kABytes + boxes * kBoxBytes)));
     const int64_t tiles = static_cast<int64_t>(a.E) * ((a.K + 127) / 128 + (a.N + 127) / 128);
-    if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, a.ctas)));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kGradSmem(a.NR, terms, a.stages);
+    cfg.dynamicSmemBytes = a.stages * (kABytes + boxes * kBoxBytes) + 1024;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -300,14 +300,4 @@ __device__ __forceinline__ bool find_row_tile(const int* offsets, int E, int M, 
     return false;
 }
 
-// The safe rows [first, last) of expert e (one warp).
-__device__ __forceinline__ void expert_rows(const int* offsets, int e, int M, int* first, int* last) {
-    const int lane = threadIdx.x & 31;
-    int top = 0;
-    for (int i = lane; i <= e; i += 32) top = max(top, min(max(__ldg(offsets + i), 0), M));
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    *first = top;
-    *last = max(top, min(max(__ldg(offsets + e + 1), 0), M));
-}
-
 }  // namespace qlora
