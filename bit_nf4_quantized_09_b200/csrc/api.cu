@@ -1385,6 +1385,9 @@ bool rows_ok(int64_t M, int E, int64_t cols) {
     return M <= (int64_t(1) << 30) && (M / 64 + E) * cdiv(cols, 256) < (int64_t(1) << 31);
 }
 
+// Block numbers of a stacked weight are 32 bits (137 GB of codes).
+bool blocks_ok(const qlora_nf4_weight* w) { return w->N <= (int64_t(1) << 32) / (w->K / kBlock); }
+
 // Checks the experts of a stacked weight: E N rows.
 qlora_status check_experts(int64_t rows, int E, int64_t M, const int32_t* offsets, int64_t* N) {
     if (E < 1 || E > kMaxExperts) return QLORA_ERR_INVALID_ARG;
@@ -1618,6 +1621,7 @@ qlora_status qlora_linear_fwd_experts(const uint16_t* X, int64_t M, const qlora_
     if (s != QLORA_OK) return s;
     int64_t N = 0;
     if ((s = check_experts(w->N, E, M, offsets, &N)) != QLORA_OK) return s;
+    if (!blocks_ok(w)) return QLORA_ERR_BAD_SHAPE;
     if (!rank_ok(r)) return QLORA_ERR_UNSUPPORTED_RANK;
     if (!std::isfinite(alpha)) return QLORA_ERR_INVALID_ARG;
     if (!rows_ok(M, E, std::max(N, w->K))) return QLORA_ERR_BAD_SHAPE;
@@ -1651,6 +1655,7 @@ qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int
     if (s != QLORA_OK) return s;
     int64_t N = 0;
     if ((s = check_experts(w->N, E, M, offsets, &N)) != QLORA_OK) return s;
+    if (!blocks_ok(w)) return QLORA_ERR_BAD_SHAPE;
     if (!rank_ok(r)) return QLORA_ERR_UNSUPPORTED_RANK;
     if (!std::isfinite(alpha)) return QLORA_ERR_INVALID_ARG;
     if (!rows_ok(M, E, std::max(N, w->K))) return QLORA_ERR_BAD_SHAPE;

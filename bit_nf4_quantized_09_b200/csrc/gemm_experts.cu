@@ -77,6 +77,23 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// lut_decode8_sx with every permute as the bare instruction: __byte_perm masks
+// its selector to three bits a nibble, which here are known to be clear but not
+// to the compiler. Integer instructions bound the decoding (22 per 8 weights).
+__device__ __forceinline__ void decode8(const Nf4BlockLut& t, uint32_t packed, uint32_t (&out)[4]) {
+    const uint32_t idx = packed & 0x77777777u, p4 = packed << 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t sel = h ? idx >> 16 : idx;
+        const uint32_t m = prmt_sx(p4, packed, h ? 0xFBEAu : 0xD9C8u);  // 0xFF where the code's top bit is set
+        const uint32_t la = prmt_sx(t.lo[0], t.lo[1], sel), lb = prmt_sx(t.lo[2], t.lo[3], sel);
+        const uint32_t ha = prmt_sx(t.hi[0], t.hi[1], sel), hb = prmt_sx(t.hi[2], t.hi[3], sel);
+        const uint32_t lo = (la & ~m) | (lb & m), hi = (ha & ~m) | (hb & m);
+        out[2 * h + 0] = prmt_sx(lo, hi, 0x4051u);
+        out[2 * h + 1] = prmt_sx(lo, hi, 0x6273u);
+    }
+}
+
 template <bool kTransW, bool kNoDq, int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_gemm(const __grid_constant__ CUtensorMap tm_act, const __grid_constant__ CUtensorMap tm_codes,
@@ -300,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // there meet zeros of dY or columns that are not written)
                 const int n = min(kTransW ? kt * 64 + (t & 63) : ptl.w0 + t + 128 * u, static_cast<int>(a.N) - 1);
                 const int kb = min(kTransW ? ptl.w0 / kBlock + (t >> 6) + 2 * u : kt, KB - 1);
-                const int64_t ib = (static_cast<int64_t>(ptl.e) * a.N + n) * KB + kb;
+                const uint32_t ib = (static_cast<uint32_t>(ptl.e) * static_cast<uint32_t>(a.N) + n) * KB + kb;  // < 2^32
                 if (kNoDq) {
                     raw_s[u] = __ldg(a.c.absmax + ib);
                 } else {
@@ -320,22 +337,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // are read before the wait
                 const int sw = (g0 + i) % L::kPW;
                 uint8_t* wst = smem + L::kOffW + sw * kWStage;
-                auto wait_stage = [&]() {  // the first step to take each stage has nothing to wait for
-                    const int uses = jobs - (G < L::kPW ? 1 : 0);
-                    return uses < 0 || __all_sync(0xFFFFFFFFu, mbar_wait(w_free + G, static_cast<uint32_t>(uses) & 1u, tmo,
-                                                                         a.status));
-                };
+                // the first step to take each weight stage has nothing to wait
+                // for: the phase before a barrier's first counts as complete
+                const int uses = jobs - (G < L::kPW ? 1 : 0);
                 if (i < nk) {
                     const int gk = gk0 + i, sc = gk % L::kPC;
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(c_full + 2 * G + (kjobs & 1), static_cast<uint32_t>(kjobs >> 1) & 1u, tmo,
-                                                           a.status));
+                    ok = wait_both(c_full + 2 * G + (kjobs & 1), static_cast<uint32_t>(kjobs >> 1) & 1u, w_free + G,
+                                   static_cast<uint32_t>(uses) & 1u, tmo, a.status);
                     if (!ok) break;
                     ++kjobs;
                     const uint32_t codes = smem_u32(smem + L::kOffC + sc * kCStage);
-                    const float cp[2] = {kNoDq ? raw_s[0] : __fmaf_rn(e4m3_to_f32(raw_q[0]), raw_s[0], mean),
-                                         kNoDq ? raw_s[1] : __fmaf_rn(e4m3_to_f32(raw_q[1]), raw_s[1], mean)};
-                    pi += kGroups;
-                    load_constants();
                     uint4 ca[2], cb[2];
                     uint32_t dst[2], swz;
                     if (!kTransW) {
@@ -347,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint32_t crow = codes + (t + 128 * u) * 32;
                             ca[u] = lds128(crow + ((0 ^ s32) << 4));
                             cb[u] = lds128(crow + ((1 ^ s32) << 4));
-                            dst[u] = smem_u32(wst) + (t + 128 * u) * 128;
+                            dst[u] = smem_u32(wst) + (t + 128 * u) * 128 + (swz << 4);
                         }
                     } else {
                         // reduction row nl, k-blocks b and b + 2 of the tile's four
@@ -358,12 +369,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int u = 0; u < 2; ++u) {
                             ca[u] = lds128(crow + (((2 * b + 4 * u) ^ swz) << 4));
                             cb[u] = lds128(crow + (((2 * b + 4 * u + 1) ^ swz) << 4));
-                            dst[u] = smem_u32(wst) + (b + 2 * u) * 8192 + (nl >> 3) * 1024 + (nl & 7) * 128;
+                            dst[u] = smem_u32(wst) + (b + 2 * u) * 8192 + (nl >> 3) * 1024 + (nl & 7) * 128 + (swz << 4);
                         }
                     }
+                    const float cp[2] = {kNoDq ? raw_s[0] : __fmaf_rn(e4m3_to_f32(raw_q[0]), raw_s[0], mean),
+                                         kNoDq ? raw_s[1] : __fmaf_rn(e4m3_to_f32(raw_q[1]), raw_s[1], mean)};
                     __syncwarp();
                     if (lane == 0) mbar_arrive(c_empty + sc);  // the codes have been read
-                    if (!(ok = wait_stage())) break;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const Nf4BlockLut lut = make_block_lut(tab.level, cp[u]);
@@ -371,8 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             uint32_t o[4];
-                            lut_decode8_sx(lut, words[j], o);
-                            sts128(dst[u] + ((static_cast<uint32_t>(j) ^ swz) << 4), o);
+                            decode8(lut, words[j], o);
+                            sts128(dst[u] ^ (static_cast<uint32_t>(j) << 4), o);  // rows are 128-byte aligned
+                        }
+                        if (u == 0) {  // the next step's constants, while this one's decoding goes on
+                            pi += kGroups;
+                            load_constants();
                         }
                     }
                     fence_proxy_async_smem();  // -> visible to the tensor core
@@ -382,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // rank-r step: B_e rows (forward) or A_e columns (dX) by TMA
                     pi += kGroups;
                     load_constants();
-                    if (!(ok = wait_stage())) break;
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(w_free + G, static_cast<uint32_t>(uses) & 1u, tmo, a.status));
+                    if (!ok) break;
                     if (leader) {
                         mbar_arrive_expect_tx(w_full + sw, kWStage);
                         if (!kTransW) {
