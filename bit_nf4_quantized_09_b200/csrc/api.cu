@@ -1424,7 +1424,7 @@ ExpertLayout expert_layout(int op, int64_t M, int64_t N, int64_t K, int r, int E
 // The rows' rank-r inputs: sT (b = A) or sU (b = B) as sums of bf16 terms.
 qlora_status expert_down(bool bwd, const uint16_t* act, int64_t M, int64_t red, const uint16_t* b, int E,
                          const int32_t* offsets, int r, float scale, int terms, uint16_t* out, int* status,
-                         cudaStream_t st) {
+                         size_t clear_bytes, cudaStream_t st) {
     ExpertDownArgs a{};
     a.offsets = offsets;
     a.E = E;
@@ -1436,6 +1436,8 @@ qlora_status expert_down(bool bwd, const uint16_t* act, int64_t M, int64_t red, 
     a.scale = scale;
     a.out = out;
     a.splits = skinny_splits(cdiv(M, 128) + std::min<int64_t>(E, M) - 1, red);
+    a.clear = status;  // the head of the workspace
+    a.clear_words = static_cast<int>(clear_bytes / 4);
     a.status = status;
     a.timeout_ns = timeout_ns();
     if (injected_failure()) return QLORA_ERR_CUDA;
@@ -1548,9 +1550,8 @@ qlora_status int8_impl(const uint16_t* X, int64_t M, const qlora_int8_weight* w,
     int8_t* xq = reinterpret_cast<int8_t*>(base + L.xq);
     float* xs = reinterpret_cast<float*>(base + L.xs);
     const int64_t K = w->K;
-    QLORA_TRY(cudaMemsetAsync(base, 0, L.header, st), "clear status and tickets");
-    if (injected_failure()) return QLORA_ERR_CUDA;
-    QLORA_LAUNCH(launch_quantize_rows(X, true, M, K, xq, xs, st), 1, "quantise tokens");
+    QLORA_LAUNCH(launch_quantize_rows(X, true, M, K, xq, xs, reinterpret_cast<int*>(base), static_cast<int>(L.header / 4), st),
+                 1, "quantise tokens");
     const GroupPlan& p = L.plan;
     CUtensorMap tx, tw;
     QLORA_MAP(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, p.cap == 256 ? 64 : 16, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1585,7 +1586,8 @@ qlora_status quantize_int8_any(const void* W, bool bf16, int64_t N, int64_t K, i
     if (injected_failure()) return QLORA_ERR_CUDA;
     const qlora_status s = device_ready(nullptr);
     if (s != QLORA_OK) return s;
-    QLORA_LAUNCH(launch_quantize_rows(W, bf16, N, K, codes, scale, static_cast<cudaStream_t>(stream)), 1, "quantise rows");
+    QLORA_LAUNCH(launch_quantize_rows(W, bf16, N, K, codes, scale, nullptr, 0, static_cast<cudaStream_t>(stream)), 1,
+                 "quantise rows");
     return QLORA_OK;
 }
 
@@ -1639,10 +1641,9 @@ qlora_status qlora_linear_fwd_experts(const uint16_t* X, int64_t M, const qlora_
     uint8_t* base = static_cast<uint8_t*>(ws);
     int* status = reinterpret_cast<int*>(base);
     uint16_t* sT = sT_save ? sT_save : reinterpret_cast<uint16_t*>(base + L.sT);
-    QLORA_TRY(cudaMemsetAsync(base, 0, L.header, st), "clear status and tickets");
-    if (injected_failure()) return QLORA_ERR_CUDA;
-    if ((s = expert_down(false, X, M, w->K, A, E, offsets, r, alpha / static_cast<float>(r), kTermsT, sT, status, st)) !=
-        QLORA_OK)
+    // the first launch of a call clears the status word and the tickets
+    if ((s = expert_down(false, X, M, w->K, A, E, offsets, r, alpha / static_cast<float>(r), kTermsT, sT, status, L.header,
+                         st)) != QLORA_OK)
         return s;
     return expert_matmul(false, X, M, w, N, E, offsets, sT, kTermsT, B, r, Y, base, L, sms, true, st);
 }
@@ -1680,12 +1681,11 @@ qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int
     uint16_t* sU = reinterpret_cast<uint16_t*>(base + L.sU);
     const uint16_t* sT = sT_in ? sT_in : reinterpret_cast<uint16_t*>(base + L.sT);
     const float scale = alpha / static_cast<float>(r);
-    QLORA_TRY(cudaMemsetAsync(base, 0, L.header, st), "clear status and tickets");
-    if (injected_failure()) return QLORA_ERR_CUDA;
     if (!sT_in && (s = expert_down(false, X, M, K, A, E, offsets, r, scale, kTermsT, reinterpret_cast<uint16_t*>(base + L.sT),
-                                   status, st)) != QLORA_OK)
+                                   status, L.header, st)) != QLORA_OK)
         return s;
-    if ((s = expert_down(true, dY, M, N, B, E, offsets, r, scale, kTermsU, sU, status, st)) != QLORA_OK) return s;
+    if ((s = expert_down(true, dY, M, N, B, E, offsets, r, scale, kTermsU, sU, status, sT_in ? L.header : 0, st)) != QLORA_OK)
+        return s;
     if ((s = expert_matmul(true, dY, M, w, N, E, offsets, sU, kTermsU, A, r, dX, base, L, sms, false, st)) != QLORA_OK)
         return s;
     // dA and dB need only sU and sT: as dX's programmatic dependent their CTAs

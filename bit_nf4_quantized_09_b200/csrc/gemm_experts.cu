@@ -471,7 +471,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // The tiles shared with other CTAs, once the loop (and the registers
         // it needs) is over: their last CTA to come here finishes them.
-        if (CAP == 64) {
+        if (CAP == 64 && pending->n > 0) {
+            // the launch before this one has cleared the tickets
+            asm volatile("griddepcontrol.wait;" ::: "memory");
             __threadfence();  // the parts are visible before the tickets
             ok = all_ok(ok, kDeqWarps * 32);
             if (threadIdx.x == 0) pending->take_tickets(ranges, a.tickets, ok);

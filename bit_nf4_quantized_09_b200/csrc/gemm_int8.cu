@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = all_ok(ok, kEpiWarps * 32);
         }
         // the tiles shared with other CTAs: their last CTA to come here finishes them
-        if (CAP == 64) {
+        if (CAP == 64 && pending->n > 0) {
             __threadfence();  // the parts are visible before the tickets
             ok = all_ok(ok, kEpiWarps * 32);
             if (threadIdx.x == 0) pending->take_tickets(ranges, a.tickets, ok);
@@ -395,8 +395,9 @@ constexpr int kCache = 4;
 
 template <bool kBf16, int TPR>
 __global__ void __launch_bounds__(TPR, kBf16 ? 1280 / TPR : 1024 / TPR)
-    quantize_rows(const void* X, int64_t K, int8_t* codes, float* scale) {
+    quantize_rows(const void* X, int64_t K, int8_t* codes, float* scale, int* clear, int clear_n) {
     asm volatile("griddepcontrol.launch_dependents;");
+    clear_words(clear, clear_n, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
     const int64_t row = blockIdx.x;
     const int t = threadIdx.x, nv = static_cast<int>(K / 8);
     __shared__ uint32_t part[TPR / 32];
@@ -460,8 +461,9 @@ __global__ void __launch_bounds__(TPR, kBf16 ? 1280 / TPR : 1024 / TPR)
 }
 
 template <bool kBf16, int TPR>
-cudaError_t launch_quantize(const void* X, int64_t rows, int64_t K, int8_t* codes, float* scale, cudaStream_t st) {
-    quantize_rows<kBf16, TPR><<<static_cast<unsigned>(rows), TPR, 0, st>>>(X, K, codes, scale);
+cudaError_t launch_quantize(const void* X, int64_t rows, int64_t K, int8_t* codes, float* scale, int* clear, int clear_n,
+                            cudaStream_t st) {
+    quantize_rows<kBf16, TPR><<<static_cast<unsigned>(rows), TPR, 0, st>>>(X, K, codes, scale, clear, clear_n);
     return cudaGetLastError();
 }
 
@@ -497,13 +499,13 @@ cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const I
 }
 
 cudaError_t launch_quantize_rows(const void* X, bool bf16, int64_t rows, int64_t K, int8_t* codes, float* scale,
-                                 cudaStream_t st) {
+                                 int* clear, int clear_n, cudaStream_t st) {
     if (rows < 1 || rows > 0x7FFFFFFF) return cudaErrorInvalidValue;
     if (K <= 4096)
-        return bf16 ? launch_quantize<true, 128>(X, rows, K, codes, scale, st)
-                    : launch_quantize<false, 128>(X, rows, K, codes, scale, st);
-    return bf16 ? launch_quantize<true, 256>(X, rows, K, codes, scale, st)
-                : launch_quantize<false, 256>(X, rows, K, codes, scale, st);
+        return bf16 ? launch_quantize<true, 128>(X, rows, K, codes, scale, clear, clear_n, st)
+                    : launch_quantize<false, 128>(X, rows, K, codes, scale, clear, clear_n, st);
+    return bf16 ? launch_quantize<true, 256>(X, rows, K, codes, scale, clear, clear_n, st)
+                : launch_quantize<false, 256>(X, rows, K, codes, scale, clear, clear_n, st);
 }
 
 }  // namespace qlora

@@ -333,6 +333,8 @@ struct ExpertDownArgs {
     uint16_t* out;        // bf16 [M, terms r]
     int splits;           // cluster size along the reduction: 1, 2, 4, 8 (at most the 64-deep steps)
     int stages;           // set by the launcher
+    int* clear;           // words that the launch zeroes (the call's status word and tickets)
+    int clear_words;
     int* status;
     uint64_t timeout_ns;
 };
@@ -390,8 +392,8 @@ struct Int8GemmArgs {
 cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, bool pdl,
                              cudaStream_t st);
 cudaError_t int8_init_device();
-// X: fp32 or bf16 [rows, K], K % 16 == 0.
+// X: fp32 or bf16 [rows, K], K % 16 == 0. clear: words that the launch zeroes.
 cudaError_t launch_quantize_rows(const void* X, bool bf16, int64_t rows, int64_t K, int8_t* codes, float* scale,
-                                 cudaStream_t st);
+                                 int* clear, int clear_words, cudaStream_t st);
 
 }  // namespace qlora

@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    clear_words(a.clear, a.clear_words, static_cast<int>(blockIdx.x * gridDim.y + blockIdx.y), static_cast<int>(gridDim.x * gridDim.y));
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int NR = a.NR, S = a.splits, y = static_cast<int>(blockIdx.y);
     const uint32_t b_bytes = static_cast<uint32_t>(NR) * 128u, stage = kABytes + b_bytes;
     const int stages = a.stages;
@@ -175,30 +176,33 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_bf16(128, NR, false, kBMn);
-            bool ok = true;
-            for (int i = 0; ok && i < steps; ++i) {
-                const int s = i % stages, chunk = i / kFlush, p = chunk & 1;
-                if (i % kFlush == 0 && chunk >= 2 &&
-                    !mbar_wait(bars.acc_free + p, static_cast<uint32_t>((chunk >> 1) - 1) & 1u, tmo, a.status))
-                    ok = false;
-                if (ok && !mbar_wait(bars.full + s, static_cast<uint32_t>(i / stages) & 1u, tmo, a.status)) ok = false;
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t at = smem_u32(smem + s * stage), bt = at + kABytes;
+        const bool leader = elect_one();
+        const uint32_t idesc = idesc_bf16(128, NR, false, kBMn);
+        const uint64_t ad0 = sw128_desc(smem_u32(smem), 16, 1024);
+        const uint64_t bd0 = kBMn ? mn_b_desc(smem_u32(smem) + kABytes, NR) : sw128_desc(smem_u32(smem) + kABytes, 16, 1024);
+        const uint32_t bk = static_cast<uint32_t>(kBMn ? 16 * NR * 2 : 32) / 16;
+        bool ok = true;
+        for (int i = 0; ok && i < steps; ++i) {
+            const int s = i % stages, chunk = i / kFlush, p = chunk & 1;
+            if (i % kFlush == 0 && chunk >= 2)
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bars.acc_free + p, static_cast<uint32_t>((chunk >> 1) - 1) & 1u, tmo,
+                                                       a.status));
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bars.full + s, static_cast<uint32_t>(i / stages) & 1u, tmo, a.status));
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+                const uint64_t ad = ad0 + static_cast<uint32_t>(s) * (stage / 16), bd = bd0 + static_cast<uint32_t>(s) * (stage / 16);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_f16(tmem + p * 64, sw128_desc(at + kk * 32, 16, 1024),
-                             kBMn ? mn_b_desc(bt + kk * 16 * NR * 2, NR) : sw128_desc(bt + kk * 32, 16, 1024), idesc,
-                             (i % kFlush > 0 || kk > 0) ? 1u : 0u);
+                    umma_f16(tmem + p * 64, ad + kk * 2, bd + kk * bk, idesc, (i % kFlush > 0 || kk > 0) ? 1u : 0u);
                 umma_commit(bars.empty + s);
                 if (i % kFlush == kFlush - 1 || i == steps - 1) umma_commit(bars.acc_full + p);
             }
-            if (!ok) *abort_flag = 1;
-            umma_commit(&bars.drain);
-            mbar_wait(&bars.drain, 0u, tmo, nullptr);
+            __syncwarp();
         }
+        if (!ok) *abort_flag = 1;
+        if (leader) umma_commit(&bars.drain);
+        mbar_wait(&bars.drain, 0u, tmo, nullptr);
         __syncwarp();
     } else {
         const int q = warp & 3, t = q * 32 + lane;
@@ -274,6 +278,7 @@ __global__ void __launch_bounds__(kFewThreads)
     expert_down_few(const uint16_t* __restrict__ X, const uint16_t* __restrict__ A, const ExpertDownArgs a) {
     asm volatile("griddepcontrol.launch_dependents;");
     __shared__ float part[kFewThreads / 32][8];
+    clear_words(a.clear, a.clear_words, static_cast<int>(blockIdx.x * gridDim.y + blockIdx.y), static_cast<int>(gridDim.x * gridDim.y));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row = static_cast<int>(blockIdx.x), j0 = static_cast<int>(blockIdx.y) * 8;
     int e = 0, row0 = 0, rows = 0;

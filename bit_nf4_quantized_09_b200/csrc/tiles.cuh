@@ -63,6 +63,14 @@ struct TileSched {          // in shared memory, one per CTA
     int base[kMaxExperts + 1];  // token tiles of the experts before e; base[E] = all
 };
 
+// CTA `cta` of `ctas` zeroes its share of `words` words: the first kernel of a
+// call clears the status word and the tickets for the kernels behind it.
+__device__ __forceinline__ void clear_words(int* p, int words, int cta, int ctas) {
+    for (int i = cta * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x); i < words;
+         i += ctas * static_cast<int>(blockDim.x))
+        p[i] = 0;
+}
+
 // Inclusive scans over a warp.
 __device__ __forceinline__ int warp_scan_max(int v) {
     const int lane = threadIdx.x & 31;
