@@ -480,8 +480,8 @@ def linear_bwd_group(dY: torch.Tensor, X: torch.Tensor, group: list, A: torch.Te
 # ------------------------------------------------------- layers of experts ---
 
 def _want(t: torch.Tensor | None, what: str, where: str, shape: tuple, dtype, device):
-    """Raises unless t is a contiguous CUDA tensor of this shape, type and device."""
-    if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    """Raises unless t is a contiguous tensor of this shape, type and device."""
+    if t is None or t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}" + (
             "" if t.is_contiguous() else ", not contiguous")
         raise QLoraError(-2 if t is not None and t.dtype == dtype and t.device == device else -1, where,
@@ -535,15 +535,19 @@ def expert_order(ids: torch.Tensor, E: int, order: torch.Tensor | None = None, o
     """(order int32 [M], offsets int32 [E + 1]) of a batch whose row m goes to
     expert ids[m] (int32): a stable sort by id, rows with an id outside [0, E)
     behind all others; expert e owns places [offsets[e], offsets[e + 1])."""
-    where, M = "qlora_expert_order", ids.numel()
-    _want(ids, "ids", where, (M,), torch.int32, ids.device)
+    where, M, dev = "qlora_expert_order", ids.numel(), ids.device
+    _want(ids, "ids", where, (M,), torch.int32, dev)
     if not 1 <= E <= 512:
         raise QLoraError(-1, where, f"E = {E}")
-    order = order if order is not None else torch.empty(M, dtype=torch.int32, device=ids.device)
-    offsets = offsets if offsets is not None else torch.empty(E + 1, dtype=torch.int32, device=ids.device)
-    _want(order, "order", where, (M,), torch.int32, ids.device)
-    _want(offsets, "offsets", where, (E + 1,), torch.int32, ids.device)
-    _check(_on(ids.device, lib().qlora_expert_order, _ptr(ids), M, E, _ptr(order), _ptr(offsets)), where)
+    if order is None:
+        order = torch.empty(M, dtype=torch.int32, device=dev)
+    else:
+        _want(order, "order", where, (M,), torch.int32, dev)
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    else:
+        _want(offsets, "offsets", where, (E + 1,), torch.int32, dev)
+    _check(_on(dev, lib().qlora_expert_order, _ptr(ids), M, E, _ptr(order), _ptr(offsets)), where)
     return order, offsets
 
 

@@ -15,6 +15,8 @@
 //
 // Bound by latency: 8 bytes per row move. 32768 ids over 64 experts: 53 us with
 // one CTA and match instructions, 8 us with the cluster and votes.
+#include <algorithm>
+
 #include "kernels.h"
 #include "tiles.cuh"
 
@@ -22,7 +24,7 @@ namespace qlora {
 
 namespace {
 
-constexpr int kWarps = 32;
+constexpr int kMaxWarps = 32;
 constexpr int kAhead = 8;  // ids of a lane in flight together
 constexpr int kClusterCtas = 8;
 
@@ -36,11 +38,12 @@ __device__ __forceinline__ unsigned same_key(int key, int bits) {
     return same;
 }
 
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kMaxWarps * 32)
     expert_order_kernel(const int* __restrict__ ids, int M, int E, int bits, int* __restrict__ order,
                         int* __restrict__ offsets) {
-    extern __shared__ int hist[];  // [kWarps][E + 1], then the CTA's totals [E + 1]
-    __shared__ int warp_sum[kWarps];
+    extern __shared__ int hist[];  // [warps][E + 1], then the CTA's totals [E + 1]
+    __shared__ int warp_sum[kMaxWarps];
+    const int kWarps = static_cast<int>(blockDim.x) >> 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = E + 1, tid = static_cast<int>(threadIdx.x);
     const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
     int* totals = hist + kWarps * H;
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
     if (warp == 0) {
-        const int s = warp_sum[lane];
+        const int s = lane < kWarps ? warp_sum[lane] : 0;
         warp_sum[lane] = warp_scan_add(s) - s;
     }
     __syncthreads();
@@ -127,28 +130,30 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
 }
 
-constexpr size_t smem_for(int E) { return static_cast<size_t>(kWarps + 1) * (E + 1) * 4; }
+constexpr size_t smem_for(int E, int warps) { return static_cast<size_t>(warps + 1) * (E + 1) * 4; }
 
 }  // namespace
 
 cudaError_t expert_order_init_device() {
     return cudaFuncSetAttribute(expert_order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(smem_for(kMaxExperts)));
+                                static_cast<int>(smem_for(kMaxExperts, kMaxWarps)));
 }
 
 cudaError_t launch_expert_order(const int* ids, int M, int E, int* order, int* offsets, cudaStream_t st) {
-    static_assert(kMaxExperts + 1 <= kWarps * 32, "one thread per id in the scan");
+    static_assert(kMaxExperts + 1 <= kMaxWarps * 32, "one thread per id in the scan");
     if (E < 1 || E > kMaxExperts || M < 0) return cudaErrorInvalidValue;
     // keys 0 .. E, and one more (all ones) for rows that do not exist
     int bits = 1;
     while ((1 << bits) - 1 <= E) ++bits;
     // a cluster once one CTA's lanes would have more than four ids each (the
     // barriers between CTAs cost about a microsecond)
-    const int ctas = M > 4 * kWarps * 32 ? kClusterCtas : 1;
+    const int ctas = M > 4 * kMaxWarps * 32 ? kClusterCtas : 1;
+    // no more warps than rows or ids to scan need
+    const int warps = ctas > 1 ? kMaxWarps : std::min(kMaxWarps, std::max(1, std::max((M + 31) / 32, (E + 32) / 32)));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = smem_for(E);
+    cfg.blockDim = dim3(static_cast<unsigned>(warps) * 32);
+    cfg.dynamicSmemBytes = smem_for(E, warps);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
