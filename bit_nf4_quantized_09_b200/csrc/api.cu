@@ -152,7 +152,7 @@ qlora_status device_ready(int* sms_out) {
             d.status = QLORA_ERR_UNSUPPORTED_DEVICE;
         } else if ((e = fused_init_device()) != cudaSuccess || (e = skinny_init_device()) != cudaSuccess ||
                    (e = gemv_mma_init_device()) != cudaSuccess || (e = merge_tc_init_device()) != cudaSuccess ||
-                   (e = expert_gemm_init_device()) != cudaSuccess ||
+                   (e = expert_gemm_init_device()) != cudaSuccess || (e = expert_gemv_init_device()) != cudaSuccess ||
                    (e = expert_rank_init_device()) != cudaSuccess || (e = expert_order_init_device()) != cudaSuccess ||
                    (e = int8_init_device()) != cudaSuccess) {
             d.status = cuda_fail(e, "cudaFuncSetAttribute");
@@ -1380,6 +1380,16 @@ GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps) {
     return p;
 }
 
+// The forward of few rows per expert: tiles of 8, 16 or 32 rows (gemv_experts.cu).
+void few_rows_plan(GroupPlan& p, int64_t M, int E, int64_t N) {
+    const int64_t act = std::max<int64_t>(1, std::min<int64_t>(E, M)), avg = std::max<int64_t>(1, cdiv(M, act));
+    if (avg > 16) return;
+    p.cap = avg <= 4 ? 8 : avg <= 8 ? 16 : 32;
+    p.tickets_bytes = up256(static_cast<size_t>((M / p.cap + act) * cdiv(N, 256)) * 4);
+    p.part_rows = p.cap;
+    p.part_bytes = up256(static_cast<size_t>(2 * kPlanSms) * p.part_rows * 256 * 4);
+}
+
 // M rows over E experts: 32-bit row numbers and tile numbers.
 bool rows_ok(int64_t M, int E, int64_t cols) {
     return M <= (int64_t(1) << 30) && (M / 64 + E) * cdiv(cols, 256) < (int64_t(1) << 31);
@@ -1409,6 +1419,7 @@ constexpr int kTermsT = 2, kTermsU = 3;
 ExpertLayout expert_layout(int op, int64_t M, int64_t N, int64_t K, int r, int E) {
     ExpertLayout L;
     L.plan = op == QLORA_OP_BWD ? group_plan(M, E, K, cdiv(N, 64)) : group_plan(M, E, N, K / kBlock);
+    if (op == QLORA_OP_FWD) few_rows_plan(L.plan, M, E, N);
     L.tickets = 256;
     L.header = L.tickets + L.plan.tickets_bytes;
     L.part = L.header;
@@ -1465,8 +1476,38 @@ qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_
                            uint16_t* out, uint8_t* base, const ExpertLayout& L, int sms, bool pdl, cudaStream_t st) {
     const int64_t K = w->K, red = dx ? N : K, cols = dx ? K : N;
     const GroupPlan& p = L.plan;
-    const uint32_t box = p.cap == 256 ? 64 : 16;
+    ExpertGemmArgs a{};
+    a.offsets = offsets;
+    a.E = E;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.out_cols = cols;
+    a.red = red;
+    a.rank_cols = r;
+    a.rank_x = rank_in;
+    a.rank_w = rank_w;
+    a.rank_ld = static_cast<int64_t>(terms) * r;
+    a.cap = p.cap;
+    a.ctas = std::min(sms, kPlanSms);
+    a.c = constants_of(w);
+    a.out = out;
+    a.part = reinterpret_cast<float*>(base + L.part);
+    a.part_rows = p.part_rows;
+    a.tickets = reinterpret_cast<int*>(base + L.tickets);
+    a.status = reinterpret_cast<int*>(base);
+    a.timeout_ns = timeout_ns();
     CUtensorMap t_act, t_codes, t_lact, t_lw;
+    if (p.cap <= 32) {
+        QLORA_MAP(&t_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, red, M, red * 2, 64, static_cast<uint32_t>(p.cap),
+                  CU_TENSOR_MAP_SWIZZLE_128B, "X");
+        QLORA_MAP(&t_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, N, K / 2, 128, 256, CU_TENSOR_MAP_SWIZZLE_128B,
+                  "codes", E);
+        if (injected_failure()) return QLORA_ERR_CUDA;
+        QLORA_LAUNCH(launch_expert_gemv(t_act, t_codes, a, tables(), st), 1, "expert forward, few rows");
+        return QLORA_OK;
+    }
+    const uint32_t box = p.cap == 256 ? 64 : 16;
     QLORA_MAP(&t_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, red, M, red * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B,
               dx ? "dY" : "X");
     // the first term of sT (sU): bf16 as the output is
@@ -1482,24 +1523,6 @@ qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_
         QLORA_MAP(&t_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_w, r, N, static_cast<uint64_t>(r) * 2, 64, 256,
                   CU_TENSOR_MAP_SWIZZLE_128B, "B", E);
     }
-    ExpertGemmArgs a{};
-    a.offsets = offsets;
-    a.E = E;
-    a.M = M;
-    a.N = N;
-    a.K = K;
-    a.out_cols = cols;
-    a.red = red;
-    a.rank_cols = r;
-    a.cap = p.cap;
-    a.ctas = std::min(sms, kPlanSms);
-    a.c = constants_of(w);
-    a.out = out;
-    a.part = reinterpret_cast<float*>(base + L.part);
-    a.part_rows = p.part_rows;
-    a.tickets = reinterpret_cast<int*>(base + L.tickets);
-    a.status = reinterpret_cast<int*>(base);
-    a.timeout_ns = timeout_ns();
     if (injected_failure()) return QLORA_ERR_CUDA;
     QLORA_LAUNCH(launch_expert_gemm(dx, t_act, t_codes, t_lact, t_lw, a, tables(), pdl, st), 1,
                  dx ? "expert dX" : "expert forward");

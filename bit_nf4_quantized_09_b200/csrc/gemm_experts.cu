@@ -69,14 +69,6 @@ static_assert(Lay<256>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "
 // most four stages the first has been consumed before the second is loaded.
 static_assert(Lay<256>::kPC <= 4 && Lay<64>::kPC <= 4, "code stages");
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-
 // lut_decode8_sx with every permute as the bare instruction: __byte_perm masks
 // its selector to three bits a nibble, which here are known to be clear but not
 // to the compiler. Integer instructions bound the decoding (22 per 8 weights).
@@ -155,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const Ranges ranges(sched.base[a.E] * tiles_w, KT, static_cast<int>(gridDim.x), CAP == 64);
-    SegIter it(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
+    SegIter<> it(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
     Tile tl;
     // steps of a segment: its reduction steps, and the rank-r step behind a tile's last
     auto steps_of = [&](const Tile& s) { return s.k_hi - s.k_lo + (s.k_hi == KT ? 1 : 0); };
@@ -297,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // `pi` walk that step's position.
         const int KB = static_cast<int>(a.K / kBlock);
         const float mean = kNoDq ? 0.0f : __ldg(a.c.mean);
-        SegIter pit(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
+        SegIter<> pit(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
         Tile ptl;
         int pi = G;
         bool plive = pit.next(ptl);

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const Ranges ranges(sched.base[a.E] * tiles_w, KT, static_cast<int>(gridDim.x), CAP == 64);
-    SegIter it(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
+    SegIter<> it(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
     Tile tl;
 
     if (warp == kWarpX || warp == kWarpW) {

@@ -1,0 +1,434 @@
+// The expert forward for few rows: Y[m] = X[m] . deq(W_e)^T + sT[m] . B_e^T for
+// experts of up to 32 rows.
+//
+// With a handful of rows per expert every weight is decoded for a few tokens
+// only, and the decoding (what bounds gemm_experts.cu there: 3.4 integer
+// instructions per weight, then a trip through shared memory to the UMMA) is
+// the whole cost. Here the weights never leave registers: mma.m16n8k16 takes
+// them as its A operand straight from the decoder, tokens are its N side (8,
+// 16 or 32).
+//
+// Decoding. w_hat = bf16(fp32(level[code] c')), exactly, from a table of level
+// pairs: a code byte holds two consecutive weights (the first in the high
+// nibble), and entry e of the table is the fp32 pair (level[e >> 4],
+// level[e & 15]). Two weights take a byte permute (the table offset), one
+// 64-bit shared-memory load, one packed multiplication by the block's constant
+// and one conversion to a bf16 pair: the operand register. The table has 16
+// copies, copy l of entry e at byte 256 e + 8 l, so that the 16 lanes of each
+// half of a 64-bit load meet 32 different banks, and the offset is the permute
+// of the code word and 8 l. The other 128 bytes of the 256-byte entries hold
+// the stages' block constants.
+//
+// A warp owns 32 rows of the 256-row weight tile as two 16-row MMA tiles that
+// share the token fragments. Lane (g, q) holds bytes 8q .. 8q + 7 of each
+// 64-weight block of its rows; MMA step s of a block pairs A slots 2q, 2q + 1,
+// 2q + 8, 2q + 9 with weights 16q + 4s .. + 3, the same order for the tokens'
+// columns (two 16-byte loads per block).
+//
+// A reduction step is four block columns: the codes of the 256 rows (one
+// 128-byte x 256-row TMA box), the tokens' columns, the rows' constants.
+// Producer warps, one per stage, load and decode the constants. Tiles are
+// dealt out as in tiles.cuh: shared tiles meet in global memory, in CTA order.
+#include "kernels.h"
+#include "tiles.cuh"
+
+namespace qlora {
+
+namespace {
+
+constexpr int kTilesW = 2;                 // 16-row MMA tiles per warp
+constexpr int kWarps = 8;                  // decoding warps: 256 weight rows
+constexpr int kStep = 4;                   // block columns per reduction step
+constexpr uint32_t kTable = 256 * 256;
+constexpr uint32_t kCodes = 256 * 32 * kStep;
+constexpr int kFew = 3, kFewMin = 1;       // fix-up and least range, in steps of 256 columns (tiles.cuh)
+
+template <int MT>
+struct Lay {
+    static constexpr int kCap = 8 * MT;                  // token rows of a tile
+    static constexpr int kStages = MT == 1 ? 4 : 3;
+    static constexpr int kThreads = (kWarps + kStages) * 32;
+    static constexpr uint32_t kXBox = kCap * 128;        // 64 columns of the tokens
+    static constexpr uint32_t kStage = kCodes + kStep * kXBox;
+    static constexpr uint32_t kOffStage = kTable;
+    static constexpr uint32_t kOffSched = kOffStage + kStages * kStage;
+    static constexpr uint32_t kOffBar = (kOffSched + sizeof(TileSched) + 63) / 64 * 64;
+    static constexpr uint32_t kBytes = kOffBar + 256 + 1024;
+};
+static_assert(Lay<1>::kBytes <= 227 * 1024 && Lay<2>::kBytes <= 227 * 1024 && Lay<4>::kBytes <= 227 * 1024, "shared memory");
+static_assert(2 * 4 * 8 + 4 + 4 + sizeof(SharedTiles) <= 256, "barriers");
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
+// The bf16 pair of code byte k of w times the constant (twice in cc). The
+// table does not change once it is built, so the load may be scheduled freely.
+__device__ __forceinline__ uint32_t decode2(uint32_t table, uint32_t lane8, uint32_t w, uint32_t k, uint64_t cc) {
+    const uint32_t off = prmt_sx(w, lane8, 0x7704u + (k << 4));
+    uint64_t lv, pr;
+    asm("ld.shared.b64 %0, [%1];" : "=l"(lv) : "r"(table + off));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(pr) : "l"(lv), "l"(cc));
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(pr));
+    return pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
+}
+
+__device__ __forceinline__ uint64_t twice(uint32_t c) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "r"(c));
+    return v;
+}
+
+// Where stage s holds the four constants of weight row r: in the free half of
+// table entry 32 s + r / 8.
+__device__ __forceinline__ uint32_t const_at(uint32_t table, int s, int r) {
+    return table + static_cast<uint32_t>(32 * s + (r >> 3)) * 256u + 128u + static_cast<uint32_t>(r & 7) * 16u;
+}
+
+// Row of its warp tile that fragment row g stands for (g + 8: this + 8): lanes
+// 0-15 read rows 0, 2, 4, 6 and lanes 16-31 rows 1, 3, 5, 7, whose 128-byte
+// swizzled chunks are disjoint.
+__device__ __forceinline__ int frag_row(int g) { return ((g & 3) << 1) | (g >> 2); }
+
+template <int MT, bool kNoDq>
+__global__ void __launch_bounds__(Lay<MT>::kThreads, 1)
+    expert_gemv(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_codes,
+                const ExpertGemmArgs a, const Nf4Tables tab) {
+    using L = Lay<MT>;
+    constexpr int S = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    TileSched& sched = *reinterpret_cast<TileSched*>(smem + L::kOffSched);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+    uint64_t* empty = full + 4;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + 4);
+    SharedTiles* pending = reinterpret_cast<SharedTiles*>(const_cast<int*>(abort_flag) + 1);
+    const uint32_t table = smem_u32(smem);
+    const int warp = warp_index(), lane = threadIdx.x & 31;
+    const int KB = static_cast<int>(a.K / kBlock), N = static_cast<int>(a.N);
+    const int steps = (KB + kStep - 1) / kStep;
+    const int tiles_w = static_cast<int>((a.N + 255) / 256);
+    const uint64_t tmo = a.timeout_ns;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full + s, 32);       // the lanes of the stage's producer warp
+            mbar_init(empty + s, kWarps);
+        }
+        *abort_flag = 0;
+        pending->n = 0;
+        fence_mbar_init();
+    }
+    build_sched(sched, a.offsets, a.E, static_cast<int>(a.M), L::kCap);
+    // the table: 8 pairs of copies of an entry
+    for (int i = threadIdx.x; i < 256 * 8; i += L::kThreads) {
+        const int e = i >> 3;
+        const uint32_t v[4] = {__float_as_uint(tab.level[e >> 4]), __float_as_uint(tab.level[e & 15]),
+                               __float_as_uint(tab.level[e >> 4]), __float_as_uint(tab.level[e & 15])};
+        sts128(table + static_cast<uint32_t>(e) * 256u + static_cast<uint32_t>(i & 7) * 16u, v);
+    }
+    __syncthreads();
+    const Ranges ranges(sched.base[a.E] * tiles_w, steps, static_cast<int>(gridDim.x), true, kFew, kFewMin);
+    SegIter<8> it(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
+    Tile tl;
+
+    if (warp >= kWarps) {
+        // ------------------------------------------------------ producers --
+        // (warp kWarps + s fills stage s)
+        const int s = warp - kWarps;
+        if (s == 0 && lane == 0) {
+            tma_prefetch_desc(&tm_codes);
+            tma_prefetch_desc(&tm_x);
+        }
+        const float mean = kNoDq ? 0.0f : __ldg(a.c.mean);
+        const bool vec = KB % kStep == 0;  // a row's four constants: one aligned word in one group of 256, or a float4
+        int k = 0, fills = 0;
+        bool ok = true;
+        while (ok && uniform(it.next(tl))) {
+            for (int kt = tl.k_lo; kt < tl.k_hi; ++kt, ++k) {
+                if (k % S != s) continue;
+                if (fills > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_sleep(empty + s, static_cast<uint32_t>(fills - 1) & 1u, tmo,
+                                                                          a.status))) {
+                    *abort_flag = 1;
+                    ok = false;
+                    break;
+                }
+                if (*abort_flag) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* st = smem + L::kOffStage + s * L::kStage;
+                const int b0 = kt * kStep;
+                if (lane == 0) {
+                    mbar_expect_tx(full + s, L::kStage);
+                    // columns past K and rows past the expert's N or past M read as zeros
+                    tma_load_3d(st, &tm_codes, full + s, b0 * 32, tl.w0, tl.e);
+#pragma unroll
+                    for (int b = 0; b < kStep; ++b)
+                        tma_load_2d(st + kCodes + b * L::kXBox, &tm_x, full + s, (b0 + b) * kBlock, tl.row0);
+                }
+                ++fills;
+                // constants of rows lane, lane + 32, ... (past the edges those of
+                // the nearest row and column, which reach no output)
+#pragma unroll 1
+                for (int j0 = 0; j0 < 8; j0 += 4) {
+                    float4 c[4];
+                    if (vec) {
+                        uint32_t qw[4];
+                        float sv[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int n = min(tl.w0 + lane + 32 * (j0 + j), N - 1);
+                            const uint32_t ib = (static_cast<uint32_t>(tl.e) * static_cast<uint32_t>(N) + n) * KB + b0;  // < 2^32
+                            if (kNoDq) {
+                                c[j] = __ldg(reinterpret_cast<const float4*>(a.c.absmax + ib));
+                            } else {
+                                qw[j] = __ldg(reinterpret_cast<const uint32_t*>(a.c.qabsmax + ib));
+                                sv[j] = __ldg(a.c.s2 + (ib >> 8));
+                            }
+                        }
+                        if (!kNoDq)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                c[j] = make_float4(__fmaf_rn(e4m3_to_f32(qw[j]), sv[j], mean),
+                                                   __fmaf_rn(e4m3_to_f32(qw[j] >> 8), sv[j], mean),
+                                                   __fmaf_rn(e4m3_to_f32(qw[j] >> 16), sv[j], mean),
+                                                   __fmaf_rn(e4m3_to_f32(qw[j] >> 24), sv[j], mean));
+                    } else {
+                        uint32_t qv[4][kStep];
+                        float sv[4][kStep];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int n = min(tl.w0 + lane + 32 * (j0 + j), N - 1);
+                            const uint32_t row = (static_cast<uint32_t>(tl.e) * static_cast<uint32_t>(N) + n) * KB;
+#pragma unroll
+                            for (int b = 0; b < kStep; ++b) {
+                                const uint32_t ib = row + min(b0 + b, KB - 1);
+                                if (kNoDq) {
+                                    sv[j][b] = __ldg(a.c.absmax + ib);
+                                } else {
+                                    qv[j][b] = __ldg(a.c.qabsmax + ib);
+                                    sv[j][b] = __ldg(a.c.s2 + (ib >> 8));
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float v[kStep];
+#pragma unroll
+                            for (int b = 0; b < kStep; ++b)
+                                v[b] = kNoDq ? sv[j][b] : __fmaf_rn(e4m3_to_f32(qv[j][b]), sv[j][b], mean);
+                            c[j] = make_float4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t v[4] = {__float_as_uint(c[j].x), __float_as_uint(c[j].y), __float_as_uint(c[j].z),
+                                               __float_as_uint(c[j].w)};
+                        sts128(const_at(table, s, lane + 32 * (j0 + j)), v);
+                    }
+                }
+                mbar_arrive(full + s);  // this lane's constants; the copies complete the phase
+            }
+        }
+        // the stage's last copies have landed (also after an abort)
+        if (lane == 0 && fills > 0) mbar_wait(full + s, static_cast<uint32_t>(fills - 1) & 1u, tmo, nullptr);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ decoding and MMA --
+        const int g = lane >> 2, q = lane & 3;
+        const uint32_t lane8 = 8u * static_cast<uint32_t>(lane & 15);
+        const int fr = frag_row(g);
+        const int wrow = warp * 16 * kTilesW + fr;  // tile row of fragment row g of MMA tile 0; tile h adds 16 h
+        const uint32_t coff = static_cast<uint32_t>(wrow) * 128u + 8u * (q & 1);
+        // token g + 8 t: chunks 2q and 2q + 1 of its 128-byte row, swizzled
+        uint32_t xoff[2];
+        xoff[0] = static_cast<uint32_t>(g) * 128u + (((2u * q) ^ static_cast<uint32_t>(g)) << 4);
+        xoff[1] = static_cast<uint32_t>(g) * 128u + (((2u * q + 1u) ^ static_cast<uint32_t>(g)) << 4);
+        bool ok = true;
+        int k = 0;
+        while (ok && uniform(it.next(tl))) {
+            float acc[kTilesW][MT][4];
+#pragma unroll
+            for (int h = 0; h < kTilesW; ++h)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[h][t][0] = acc[h][t][1] = acc[h][t][2] = acc[h][t][3] = 0.0f;
+            for (int kt = tl.k_lo; kt < tl.k_hi; ++kt, ++k) {
+                const int s = k % S;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + s, static_cast<uint32_t>(k / S) & 1u, tmo, a.status));
+                if (!ok) break;
+                const uint32_t st = table + L::kOffStage + static_cast<uint32_t>(s) * L::kStage;
+                uint4 cA[kTilesW], cB[kTilesW];  // constants of the four blocks, rows fr and fr + 8
+#pragma unroll
+                for (int h = 0; h < kTilesW; ++h) {
+                    cA[h] = lds128(const_at(table, s, wrow + 16 * h));
+                    cB[h] = lds128(const_at(table, s, wrow + 16 * h + 8));
+                }
+#pragma unroll
+                for (int b = 0; b < kStep; ++b) {
+                    if (kt * kStep + b >= KB) break;
+                    const uint32_t ch = ((2u * b + (q >> 1)) ^ static_cast<uint32_t>(fr & 7)) << 4;
+                    uint32_t xw[MT][8];
+                    const uint32_t xb = st + kCodes + b * L::kXBox;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        // lanes of tokens the tile does not have load nothing and feed zeros
+                        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+                        if (g + 8 * t < tl.rows) {
+                            x0 = lds128(xb + t * 1024u + xoff[0]);
+                            x1 = lds128(xb + t * 1024u + xoff[1]);
+                        }
+                        xw[t][0] = x0.x, xw[t][1] = x0.y, xw[t][2] = x0.z, xw[t][3] = x0.w;
+                        xw[t][4] = x1.x, xw[t][5] = x1.y, xw[t][6] = x1.z, xw[t][7] = x1.w;
+                    }
+#pragma unroll
+                    for (int h = 0; h < kTilesW; ++h) {
+                        const uint32_t ca = st + coff + static_cast<uint32_t>(h) * 2048u + ch;
+                        const uint2 wa = lds64(ca), wb = lds64(ca + 1024u);
+                        const uint64_t ka = twice(b == 0 ? cA[h].x : b == 1 ? cA[h].y : b == 2 ? cA[h].z : cA[h].w);
+                        const uint64_t kb = twice(b == 0 ? cB[h].x : b == 1 ? cB[h].y : b == 2 ? cB[h].z : cB[h].w);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t ra = i < 2 ? wa.x : wa.y, rb = i < 2 ? wb.x : wb.y, kk = (i & 1) * 2;
+                            const uint32_t af[4] = {decode2(table, lane8, ra, kk, ka), decode2(table, lane8, rb, kk, kb),
+                                                    decode2(table, lane8, ra, kk + 1, ka),
+                                                    decode2(table, lane8, rb, kk + 1, kb)};
+#pragma unroll
+                            for (int t = 0; t < MT; ++t) mma_bf16(acc[h][t], af, xw[t][2 * i], xw[t][2 * i + 1]);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + s);
+            }
+            if (!ok) break;
+            if (tl.k_hi == steps) {
+                // the rank-r term, by the CTA that has the tile's last step
+                asm volatile("griddepcontrol.wait;" ::: "memory");  // sT of the preceding launch
+                for (int k0 = 0; k0 < a.rank_cols; k0 += 16) {
+                    const int j0 = k0 + 2 * q, j1 = j0 + 8;
+                    const bool has1 = j1 < a.rank_cols;
+                    uint32_t x0[MT], x1[MT];
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        const bool tok = g + 8 * t < tl.rows;
+                        const uint16_t* x = a.rank_x + static_cast<int64_t>(tl.row0 + (tok ? g + 8 * t : 0)) * a.rank_ld;
+                        x0[t] = tok ? __ldcg(reinterpret_cast<const uint32_t*>(x + j0)) : 0u;
+                        x1[t] = tok && has1 ? __ldcg(reinterpret_cast<const uint32_t*>(x + j1)) : 0u;
+                    }
+#pragma unroll
+                    for (int h = 0; h < kTilesW; ++h) {
+                        const int64_t row = static_cast<int64_t>(tl.e) * N;
+                        const uint16_t* bA = a.rank_w + (row + min(tl.w0 + wrow + 16 * h, N - 1)) * a.rank_cols;
+                        const uint16_t* bB = a.rank_w + (row + min(tl.w0 + wrow + 16 * h + 8, N - 1)) * a.rank_cols;
+                        const uint32_t af[4] = {__ldg(reinterpret_cast<const uint32_t*>(bA + j0)),
+                                                __ldg(reinterpret_cast<const uint32_t*>(bB + j0)),
+                                                has1 ? __ldg(reinterpret_cast<const uint32_t*>(bA + j1)) : 0u,
+                                                has1 ? __ldg(reinterpret_cast<const uint32_t*>(bB + j1)) : 0u};
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) mma_bf16(acc[h][t], af, x0[t], x1[t]);
+                    }
+                }
+            }
+            // acc[h][t][0..1]: row wrow + 16 h, tokens 8t + 2q, + 1; [2..3]: that row + 8
+            const bool whole = tl.k_hi - tl.k_lo == steps;
+            float* part = a.part + (whole ? 0 : ranges.slot(static_cast<int>(blockIdx.x), tl.id) * a.part_rows * 256);
+#pragma unroll
+            for (int h = 0; h < kTilesW; ++h)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = 8 * t + 2 * q + (i & 1), n = wrow + 16 * h + 8 * (i >> 1);
+                        if (tok >= tl.rows) continue;
+                        if (!whole)
+                            part[tok * 256 + n] = acc[h][t][i];
+                        else if (tl.w0 + n < N)
+                            a.out[static_cast<int64_t>(tl.row0 + tok) * N + tl.w0 + n] =
+                                static_cast<uint16_t>(pack_bf16x2(acc[h][t][i], 0.0f));
+                    }
+            if (!whole && threadIdx.x == 0) pending->push(tl);
+        }
+        if (!ok) *abort_flag = 1;
+        // The tiles shared with other CTAs: their last CTA to come here
+        // finishes them. After a wait that ran out nobody does.
+        ok = all_ok(ok, kWarps * 32);
+        if (ok && pending->n > 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // the launch before has cleared the tickets
+            __threadfence();                                     // the parts are visible before the tickets
+            all_ok(true, kWarps * 32);
+            if (threadIdx.x == 0) pending->take_tickets(ranges, a.tickets, true);
+            all_ok(true, kWarps * 32);
+            __threadfence();
+            for (int j = 0; j < pending->n; ++j) {
+                if (!pending->last[j]) continue;
+                const Tile p = pending->tile[j];
+                uint16_t* out = a.out + static_cast<int64_t>(p.row0) * N + p.w0;
+                const int c0 = ranges.first_cta(p.id);
+                add_parts<float4>(a.part, a.part_rows * 256, ranges.slot(c0, p.id), c0, ranges.last_cta(p.id), p.rows,
+                                  N - p.w0, static_cast<int>(threadIdx.x), kWarps * 32,
+                                  [&](int tok, int nc, const float4& v) {
+                                      *reinterpret_cast<uint2*>(out + static_cast<int64_t>(tok) * N + nc) =
+                                          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                                  });
+            }
+        }
+        __syncwarp();
+    }
+    // launched as a programmatic dependent, the grid completes only after its primary
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <int MT, bool kNoDq>
+cudaError_t launch_one(const CUtensorMap& x, const CUtensorMap& codes, const ExpertGemmArgs& a, const Nf4Tables& tab,
+                       cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
+    cfg.blockDim = dim3(Lay<MT>::kThreads);
+    cfg.dynamicSmemBytes = Lay<MT>::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, expert_gemv<MT, kNoDq>, x, codes, a, tab);
+}
+
+template <int MT>
+cudaError_t launch_mt(const CUtensorMap& x, const CUtensorMap& codes, const ExpertGemmArgs& a, const Nf4Tables& tab,
+                      cudaStream_t st) {
+    return a.c.absmax ? launch_one<MT, true>(x, codes, a, tab, st) : launch_one<MT, false>(x, codes, a, tab, st);
+}
+
+template <int MT>
+cudaError_t opt_in() {
+    const cudaError_t e = cudaFuncSetAttribute(expert_gemv<MT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(Lay<MT>::kBytes));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(expert_gemv<MT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Lay<MT>::kBytes));
+}
+
+}  // namespace
+
+cudaError_t expert_gemv_init_device() {
+    cudaError_t e;
+    if ((e = opt_in<1>()) != cudaSuccess || (e = opt_in<2>()) != cudaSuccess) return e;
+    return opt_in<4>();
+}
+
+cudaError_t launch_expert_gemv(const CUtensorMap& x, const CUtensorMap& codes, const ExpertGemmArgs& a, const Nf4Tables& tab,
+                               cudaStream_t st) {
+    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 1 || a.rank_cols < 8 || a.rank_cols > 64 || a.out_cols != a.N)
+        return cudaErrorInvalidValue;
+    if (a.cap == 8) return launch_mt<1>(x, codes, a, tab, st);
+    if (a.cap == 16) return launch_mt<2>(x, codes, a, tab, st);
+    if (a.cap == 32) return launch_mt<4>(x, codes, a, tab, st);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace qlora

@@ -302,6 +302,9 @@ struct ExpertGemmArgs {
     int64_t out_cols;     // N (forward) or K (dX)
     int64_t red;          // K (forward) or N (dX)
     int rank_cols;        // r
+    const uint16_t* rank_x;  // few rows: sT, rows rank_ld apart, and B of every expert
+    const uint16_t* rank_w;
+    int64_t rank_ld;
     int cap, ctas;
     BlockConstants c;     // of the stacked weight, E N rows
     uint16_t* out;        // bf16 [M, out_cols]
@@ -320,6 +323,12 @@ cudaError_t launch_expert_gemm(bool trans_w, const CUtensorMap& act, const CUten
                                const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl,
                                cudaStream_t st);
 cudaError_t expert_gemm_init_device();
+// The forward in tiles of few rows (cap 8, 16 or 32): x box {64, cap} SW128,
+// codes {K/2, N, E} box {128, 256, 1} SW128. A programmatic dependent of the
+// launch that makes rank_x.
+cudaError_t launch_expert_gemv(const CUtensorMap& x, const CUtensorMap& codes, const ExpertGemmArgs& a, const Nf4Tables& tab,
+                               cudaStream_t st);
+cudaError_t expert_gemv_init_device();
 
 // out[m, k r + j] = term k of scale * (act[m] . B_e[:, j]) for the rows of
 // every expert: term 0 the bf16 rounding, term k that of what is left.

@@ -58,6 +58,15 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// A box of one plane of a 3-D tensor.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 struct TileSched {          // in shared memory, one per CTA
     int off[kMaxExperts + 1];   // safe row offsets
     int base[kMaxExperts + 1];  // token tiles of the experts before e; base[E] = all
@@ -142,15 +151,16 @@ struct Ranges {
     int tiles, steps, P, whole;
     uint32_t Q, units;  // 32 bits: at most P - 1 tiles, and tiles of 65536 steps or more are taken whole
     // share: whether tiles may be shared at all
-    __device__ Ranges(int tiles_, int steps_, int ctas, bool share) : tiles(tiles_), steps(steps_), P(ctas) {
+    __device__ Ranges(int tiles_, int steps_, int ctas, bool share, int fix_up = kFixUp, int min_steps = kMinSteps)
+        : tiles(tiles_), steps(steps_), P(ctas) {
         const int rest = tiles % P;
         whole = tiles;
         units = 0;
         Q = 0;
         if (share && rest > 0 && steps < 65536 && P <= 256) {
             const int u = rest * steps;
-            const int q = min(P, max(u / kMinSteps, rest));
-            if ((u + q - 1) / q + kFixUp < steps) {
+            const int q = min(P, max(u / min_steps, rest));
+            if ((u + q - 1) / q + fix_up < steps) {
                 whole = tiles - rest;
                 units = static_cast<uint32_t>(u);
                 Q = static_cast<uint32_t>(q);
@@ -168,7 +178,9 @@ struct Ranges {
 };
 static_assert(256ull * 255 * 65536 < (1ull << 32), "32-bit products");
 
-// Walks the segments of CTA c: its whole tiles, then its range.
+// Walks the segments of CTA c: its whole tiles, then its range. Token tiles
+// are multiples of kRound rows.
+template <int kRound = 16>
 struct SegIter {
     const TileSched& s;
     const Ranges& r;
@@ -199,7 +211,7 @@ struct SegIter {
         const int n = s.base[e + 1] - s.base[e];  // token tiles of this expert, at least 1
         const int local = out.id - s.base[e] * tiles_w;
         const int m = s.off[e + 1] - s.off[e];
-        const int per = ((m + n - 1) / n + 15) & ~15;
+        const int per = ((m + n - 1) / n + kRound - 1) & ~(kRound - 1);
         const int j = local % n;
         out.e = e;
         out.w0 = local / n * 256;
