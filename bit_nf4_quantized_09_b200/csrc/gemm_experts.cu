@@ -69,23 +69,6 @@ static_assert(Lay<256>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "
 // most four stages the first has been consumed before the second is loaded.
 static_assert(Lay<256>::kPC <= 4 && Lay<64>::kPC <= 4, "code stages");
 
-// lut_decode8_sx with every permute as the bare instruction: __byte_perm masks
-// its selector to three bits a nibble, which here are known to be clear but not
-// to the compiler. Integer instructions bound the decoding (22 per 8 weights).
-__device__ __forceinline__ void decode8(const Nf4BlockLut& t, uint32_t packed, uint32_t (&out)[4]) {
-    const uint32_t idx = packed & 0x77777777u, p4 = packed << 4;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t sel = h ? idx >> 16 : idx;
-        const uint32_t m = prmt_sx(p4, packed, h ? 0xFBEAu : 0xD9C8u);  // 0xFF where the code's top bit is set
-        const uint32_t la = prmt_sx(t.lo[0], t.lo[1], sel), lb = prmt_sx(t.lo[2], t.lo[3], sel);
-        const uint32_t ha = prmt_sx(t.hi[0], t.hi[1], sel), hb = prmt_sx(t.hi[2], t.hi[3], sel);
-        const uint32_t lo = (la & ~m) | (lb & m), hi = (ha & ~m) | (hb & m);
-        out[2 * h + 0] = prmt_sx(lo, hi, 0x4051u);
-        out[2 * h + 1] = prmt_sx(lo, hi, 0x6273u);
-    }
-}
-
 template <bool kTransW, bool kNoDq, int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_gemm(const __grid_constant__ CUtensorMap tm_act, const __grid_constant__ CUtensorMap tm_codes,

@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kTilesW = 2;                 // 16-row MMA tiles per warp
 constexpr int kWarps = 8;                  // decoding warps: 256 weight rows
+constexpr int kTablePairs = 2;             // of a block's four word pairs in the second MMA tile, by table
 constexpr int kStep = 4;                   // block columns per reduction step
 constexpr uint32_t kTable = 256 * 256;
 constexpr uint32_t kCodes = 256 * 32 * kStep;
@@ -76,9 +77,15 @@ __device__ __forceinline__ uint32_t decode2(uint32_t table, uint32_t lane8, uint
     return pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
 }
 
-__device__ __forceinline__ uint64_t twice(uint32_t c) {
+__device__ __forceinline__ uint64_t twice(float c) {
     uint64_t v;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "r"(c));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "f"(c));
+    return v;
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
 
@@ -96,7 +103,7 @@ __device__ __forceinline__ int frag_row(int g) { return ((g & 3) << 1) | (g >> 2
 template <int MT, bool kNoDq>
 __global__ void __launch_bounds__(Lay<MT>::kThreads, 1)
     expert_gemv(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_codes,
-                const ExpertGemmArgs a, const Nf4Tables tab) {
+                const __grid_constant__ ExpertGemmArgs a, const __grid_constant__ Nf4Tables tab) {
     using L = Lay<MT>;
     constexpr int S = L::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -123,13 +130,6 @@ __global__ void __launch_bounds__(Lay<MT>::kThreads, 1)
         fence_mbar_init();
     }
     build_sched(sched, a.offsets, a.E, static_cast<int>(a.M), L::kCap);
-    // the table: 8 pairs of copies of an entry
-    for (int i = threadIdx.x; i < 256 * 8; i += L::kThreads) {
-        const int e = i >> 3;
-        const uint32_t v[4] = {__float_as_uint(tab.level[e >> 4]), __float_as_uint(tab.level[e & 15]),
-                               __float_as_uint(tab.level[e >> 4]), __float_as_uint(tab.level[e & 15])};
-        sts128(table + static_cast<uint32_t>(e) * 256u + static_cast<uint32_t>(i & 7) * 16u, v);
-    }
     __syncthreads();
     const Ranges ranges(sched.base[a.E] * tiles_w, steps, static_cast<int>(gridDim.x), true, kFew, kFewMin);
     SegIter<8> it(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
@@ -243,12 +243,24 @@ __global__ void __launch_bounds__(Lay<MT>::kThreads, 1)
         const uint32_t lane8 = 8u * static_cast<uint32_t>(lane & 15);
         const int fr = frag_row(g);
         const int wrow = warp * 16 * kTilesW + fr;  // tile row of fragment row g of MMA tile 0; tile h adds 16 h
-        const uint32_t coff = static_cast<uint32_t>(wrow) * 128u + 8u * (q & 1);
-        // token g + 8 t: chunks 2q and 2q + 1 of its 128-byte row, swizzled
-        uint32_t xoff[2];
-        xoff[0] = static_cast<uint32_t>(g) * 128u + (((2u * q) ^ static_cast<uint32_t>(g)) << 4);
-        xoff[1] = static_cast<uint32_t>(g) * 128u + (((2u * q + 1u) ^ static_cast<uint32_t>(g)) << 4);
-        bool ok = true;
+        // The lane's words of a block, two by two: pair u = jj ^ q of the block's
+        // four at turn jj, an order in which no two lanes of a load meet a bank.
+        uint32_t coff[4], xoff[4];
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+            const uint32_t u = static_cast<uint32_t>(jj ^ q);
+            coff[jj] = static_cast<uint32_t>(wrow) * 128u + (((2u * q + (u >> 1)) ^ static_cast<uint32_t>(fr)) << 4) + ((u & 1u) << 3);
+            xoff[jj] = kCodes + static_cast<uint32_t>(q) * L::kXBox + static_cast<uint32_t>(g) * 128u +
+                       (((2u * u) ^ static_cast<uint32_t>(g)) << 4);
+        }
+        // the table, two copies of an entry at a time (while the first copies travel)
+        for (int i = threadIdx.x; i < 256 * 8; i += kWarps * 32) {
+            const int e = i >> 3;
+            const uint32_t v[4] = {__float_as_uint(tab.level[e >> 4]), __float_as_uint(tab.level[e & 15]),
+                                   __float_as_uint(tab.level[e >> 4]), __float_as_uint(tab.level[e & 15])};
+            sts128(table + static_cast<uint32_t>(e) * 256u + static_cast<uint32_t>(i & 7) * 16u, v);
+        }
+        bool ok = all_ok(true, kWarps * 32);
         int k = 0;
         while (ok && uniform(it.next(tl))) {
             float acc[kTilesW][MT][4];
@@ -261,43 +273,57 @@ __global__ void __launch_bounds__(Lay<MT>::kThreads, 1)
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + s, static_cast<uint32_t>(k / S) & 1u, tmo, a.status));
                 if (!ok) break;
                 const uint32_t st = table + L::kOffStage + static_cast<uint32_t>(s) * L::kStage;
-                uint4 cA[kTilesW], cB[kTilesW];  // constants of the four blocks, rows fr and fr + 8
+                // constants of the lane's block, rows fr and fr + 8 of both MMA
+                // tiles; a block past K counts as zeros
+                float cA[kTilesW], cB[kTilesW];
 #pragma unroll
                 for (int h = 0; h < kTilesW; ++h) {
-                    cA[h] = lds128(const_at(table, s, wrow + 16 * h));
-                    cB[h] = lds128(const_at(table, s, wrow + 16 * h + 8));
+                    const uint32_t at = const_at(table, s, wrow + 16 * h) + 4u * q;
+                    const bool in = kt * kStep + q < KB;
+                    cA[h] = in ? lds_f32(at) : 0.0f;
+                    cB[h] = in ? lds_f32(at + 256u) : 0.0f;
                 }
+                const uint64_t ka = twice(cA[0]), kb = twice(cB[0]), ka1 = twice(cA[1]), kb1 = twice(cB[1]);
+                const Nf4BlockLut la = make_block_lut(tab.level, cA[1]), lb = make_block_lut(tab.level, cB[1]);
 #pragma unroll
-                for (int b = 0; b < kStep; ++b) {
-                    if (kt * kStep + b >= KB) break;
-                    const uint32_t ch = ((2u * b + (q >> 1)) ^ static_cast<uint32_t>(fr & 7)) << 4;
-                    uint32_t xw[MT][8];
-                    const uint32_t xb = st + kCodes + b * L::kXBox;
+                for (int jj = 0; jj < 4; ++jj) {
+                    const uint2 wa = lds64(st + coff[jj]), wb = lds64(st + coff[jj] + 1024u);
+                    const uint2 va = lds64(st + coff[jj] + 2048u), vb = lds64(st + coff[jj] + 3072u);
 #pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        // lanes of tokens the tile does not have load nothing and feed zeros
-                        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
-                        if (g + 8 * t < tl.rows) {
-                            x0 = lds128(xb + t * 1024u + xoff[0]);
-                            x1 = lds128(xb + t * 1024u + xoff[1]);
+                    for (int w = 0; w < 2; ++w) {
+                        uint4 x[MT];
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            // lanes of tokens the tile does not have load nothing and feed zeros
+                            x[t] = make_uint4(0u, 0u, 0u, 0u);
+                            if (g + 8 * t < tl.rows) x[t] = lds128(((st + xoff[jj]) ^ (16u * w)) + t * 1024u);
                         }
-                        xw[t][0] = x0.x, xw[t][1] = x0.y, xw[t][2] = x0.z, xw[t][3] = x0.w;
-                        xw[t][4] = x1.x, xw[t][5] = x1.y, xw[t][6] = x1.z, xw[t][7] = x1.w;
-                    }
+                        const uint32_t ra = w ? wa.y : wa.x, rb = w ? wb.y : wb.x;
 #pragma unroll
-                    for (int h = 0; h < kTilesW; ++h) {
-                        const uint32_t ca = st + coff + static_cast<uint32_t>(h) * 2048u + ch;
-                        const uint2 wa = lds64(ca), wb = lds64(ca + 1024u);
-                        const uint64_t ka = twice(b == 0 ? cA[h].x : b == 1 ? cA[h].y : b == 2 ? cA[h].z : cA[h].w);
-                        const uint64_t kb = twice(b == 0 ? cB[h].x : b == 1 ? cB[h].y : b == 2 ? cB[h].z : cB[h].w);
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t af[4] = {decode2(table, lane8, ra, 2 * i, ka), decode2(table, lane8, rb, 2 * i, kb),
+                                                    decode2(table, lane8, ra, 2 * i + 1, ka),
+                                                    decode2(table, lane8, rb, 2 * i + 1, kb)};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t ra = i < 2 ? wa.x : wa.y, rb = i < 2 ? wb.x : wb.y, kk = (i & 1) * 2;
-                            const uint32_t af[4] = {decode2(table, lane8, ra, kk, ka), decode2(table, lane8, rb, kk, kb),
-                                                    decode2(table, lane8, ra, kk + 1, ka),
-                                                    decode2(table, lane8, rb, kk + 1, kb)};
+                            for (int t = 0; t < MT; ++t) mma_bf16(acc[0][t], af, i ? x[t].z : x[t].x, i ? x[t].w : x[t].y);
+                        }
+                        uint32_t oa[4], ob[4];
+                        const uint32_t qa = w ? va.y : va.x, qb = w ? vb.y : vb.x;
+                        if (jj < kTablePairs) {
 #pragma unroll
-                            for (int t = 0; t < MT; ++t) mma_bf16(acc[h][t], af, xw[t][2 * i], xw[t][2 * i + 1]);
+                            for (int i = 0; i < 4; ++i) {
+                                oa[i] = decode2(table, lane8, qa, i, ka1);
+                                ob[i] = decode2(table, lane8, qb, i, kb1);
+                            }
+                        } else {
+                            decode8(la, qa, oa);
+                            decode8(lb, qb, ob);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t af[4] = {oa[2 * i], ob[2 * i], oa[2 * i + 1], ob[2 * i + 1]};
+#pragma unroll
+                            for (int t = 0; t < MT; ++t) mma_bf16(acc[1][t], af, i ? x[t].z : x[t].x, i ? x[t].w : x[t].y);
                         }
                     }
                 }

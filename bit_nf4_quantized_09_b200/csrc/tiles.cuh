@@ -67,6 +67,23 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// lut_decode8_sx with every permute as the bare instruction: __byte_perm masks
+// its selector to three bits a nibble, which here are known to be clear but not
+// to the compiler. Integer instructions bound the decoding (22 per 8 weights).
+__device__ __forceinline__ void decode8(const Nf4BlockLut& t, uint32_t packed, uint32_t (&out)[4]) {
+    const uint32_t idx = packed & 0x77777777u, p4 = packed << 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t sel = h ? idx >> 16 : idx;
+        const uint32_t m = prmt_sx(p4, packed, h ? 0xFBEAu : 0xD9C8u);  // 0xFF where the code's top bit is set
+        const uint32_t la = prmt_sx(t.lo[0], t.lo[1], sel), lb = prmt_sx(t.lo[2], t.lo[3], sel);
+        const uint32_t ha = prmt_sx(t.hi[0], t.hi[1], sel), hb = prmt_sx(t.hi[2], t.hi[3], sel);
+        const uint32_t lo = (la & ~m) | (lb & m), hi = (ha & ~m) | (hb & m);
+        out[2 * h + 0] = prmt_sx(lo, hi, 0x4051u);
+        out[2 * h + 1] = prmt_sx(lo, hi, 0x6273u);
+    }
+}
+
 struct TileSched {          // in shared memory, one per CTA
     int off[kMaxExperts + 1];   // safe row offsets
     int base[kMaxExperts + 1];  // token tiles of the experts before e; base[E] = all
