@@ -1380,11 +1380,15 @@ GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps) {
     return p;
 }
 
-// The forward of few rows per expert: tiles of 8, 16 or 32 rows (gemv_experts.cu).
+// The forward of few rows per expert: tiles of 8 or 16 rows (gemv_experts.cu),
+// by the mean of the rows of an expert that has any. Measured on 8 experts of
+// 4096 x 4096, in tiles of 8, of 16, and of 64 by UMMA: 48 rows 41, 43 and 50
+// us, 64 rows 49, 43 and 51 us, 96 rows 59, 50 and 52 us, 128 rows 71, 57 and
+// 52 us (experts differ in rows, and one row too many decodes a tile twice).
 void few_rows_plan(GroupPlan& p, int64_t M, int E, int64_t N) {
     const int64_t act = std::max<int64_t>(1, std::min<int64_t>(E, M)), avg = std::max<int64_t>(1, cdiv(M, act));
-    if (avg > 16) return;
-    p.cap = avg <= 4 ? 8 : avg <= 8 ? 16 : 32;
+    if (avg > 12) return;
+    p.cap = avg <= 6 ? 8 : 16;
     p.tickets_bytes = up256(static_cast<size_t>((M / p.cap + act) * cdiv(N, 256)) * 4);
     p.part_rows = p.cap;
     p.part_bytes = up256(static_cast<size_t>(2 * kPlanSms) * p.part_rows * 256 * 4);
@@ -1498,7 +1502,7 @@ qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_
     a.status = reinterpret_cast<int*>(base);
     a.timeout_ns = timeout_ns();
     CUtensorMap t_act, t_codes, t_lact, t_lw;
-    if (p.cap <= 32) {
+    if (p.cap <= 16) {
         QLORA_MAP(&t_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, red, M, red * 2, 64, static_cast<uint32_t>(p.cap),
                   CU_TENSOR_MAP_SWIZZLE_128B, "X");
         QLORA_MAP(&t_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, N, K / 2, 128, 256, CU_TENSOR_MAP_SWIZZLE_128B,

@@ -1,34 +1,49 @@
-// The expert forward for few rows: Y[m] = X[m] . deq(W_e)^T + sT[m] . B_e^T for
-// experts of up to 32 rows.
+// The expert forward for few rows: Y[m] = X[m] . deq(W_e)^T + sT[m] . B_e^T in
+// tiles of up to 16 rows.
 //
 // With a handful of rows per expert every weight is decoded for a few tokens
 // only, and the decoding (what bounds gemm_experts.cu there: 3.4 integer
 // instructions per weight, then a trip through shared memory to the UMMA) is
 // the whole cost. Here the weights never leave registers: mma.m16n8k16 takes
-// them as its A operand straight from the decoder, tokens are its N side (8,
-// 16 or 32).
+// them as its A operand straight from the decoder, tokens are its N side (8 or
+// 16).
 //
-// Decoding. w_hat = bf16(fp32(level[code] c')), exactly, from a table of level
-// pairs: a code byte holds two consecutive weights (the first in the high
-// nibble), and entry e of the table is the fp32 pair (level[e >> 4],
-// level[e & 15]). Two weights take a byte permute (the table offset), one
-// 64-bit shared-memory load, one packed multiplication by the block's constant
-// and one conversion to a bf16 pair: the operand register. The table has 16
-// copies, copy l of entry e at byte 256 e + 8 l, so that the 16 lanes of each
-// half of a 64-bit load meet 32 different banks, and the offset is the permute
-// of the code word and 8 l. The other 128 bytes of the 256-byte entries hold
-// the stages' block constants.
+// Decoding, exactly w_hat = bf16(fp32(level[code] c')), in two ways side by
+// side, since one is bound by shared memory and the other by the integer pipe:
+//   - by a table of level pairs: a code byte holds two consecutive weights (the
+//     first in the high nibble), entry e is the fp32 pair (level[e >> 4],
+//     level[e & 15]). Two weights take a byte permute (the offset), a 64-bit
+//     load, one packed multiplication by the block's constant and one
+//     conversion to a bf16 pair, the operand register. The table has 16 copies,
+//     copy l of entry e at byte 256 e + 8 l: the 16 lanes of each half of a
+//     64-bit load meet 32 different banks, and the permute of the code word and
+//     8 l is the whole offset. The other 128 bytes of the 256-byte entries hold
+//     the stages' block constants.
+//   - by byte permutes of the block's 16 products (decode8), as in
+//     gemm_experts.cu.
+// All of it by table keeps the shared-memory pipe 85 % busy (64 rows over 8
+// experts of 4096 x 11008: 94 us), half and half the integer pipe 85 % (also 94
+// us); three quarters by table leaves neither the bound alone (91 us).
 //
 // A warp owns 32 rows of the 256-row weight tile as two 16-row MMA tiles that
-// share the token fragments. Lane (g, q) holds bytes 8q .. 8q + 7 of each
-// 64-weight block of its rows; MMA step s of a block pairs A slots 2q, 2q + 1,
-// 2q + 8, 2q + 9 with weights 16q + 4s .. + 3, the same order for the tokens'
-// columns (two 16-byte loads per block).
+// share the token fragments; the second decodes half of its words by permutes.
+// A reduction step is four block columns (the codes of 256 rows: one 128-byte x
+// 256-row TMA box), and lane (g, q) of a warp owns block q of its rows: the
+// products of a block are made once, by one lane. An MMA takes four weights of
+// each lane (A slots 2q, 2q + 1, 2q + 8, 2q + 9) and the same columns of the
+// tokens; which columns of the step an MMA covers does not matter to the sum.
 //
-// A reduction step is four block columns: the codes of the 256 rows (one
-// 128-byte x 256-row TMA box), the tokens' columns, the rows' constants.
-// Producer warps, one per stage, load and decode the constants. Tiles are
-// dealt out as in tiles.cuh: shared tiles meet in global memory, in CTA order.
+// Producer warps, one per stage, issue the copies and decode the constants.
+// Tiles are dealt out as in tiles.cuh: shared tiles meet in global memory, in
+// CTA order.
+//
+// Measured, with the down-projection: two experts of 11008 x 4096 with a row
+// each 33 us (47.5 MB, 1.4 TB/s; 42 us by UMMA), 64 rows over 8 experts of 4096
+// x 11008 91 us (191.9 MB, 2.1 TB/s; 121 us by UMMA). A step takes 1.4 to 1.7
+// us for 256 x 256 weights (2.9 cycles of the SM for 64 weights); launch and
+// first copies 7 us, the meeting of shared tiles 5 us. 16 decoding warps
+// instead of 8 (two groups, steps in turn) have 96 registers each and were
+// slower: 37 and 103 us.
 #include "kernels.h"
 #include "tiles.cuh"
 
@@ -42,7 +57,7 @@ constexpr int kTablePairs = 2;             // of a block's four word pairs in th
 constexpr int kStep = 4;                   // block columns per reduction step
 constexpr uint32_t kTable = 256 * 256;
 constexpr uint32_t kCodes = 256 * 32 * kStep;
-constexpr int kFew = 3, kFewMin = 1;       // fix-up and least range, in steps of 256 columns (tiles.cuh)
+constexpr int kFixUpSteps = 3, kMinRange = 1;  // as kFixUp and kMinSteps of tiles.cuh, in steps of 256 columns
 
 template <int MT>
 struct Lay {
@@ -56,7 +71,7 @@ struct Lay {
     static constexpr uint32_t kOffBar = (kOffSched + sizeof(TileSched) + 63) / 64 * 64;
     static constexpr uint32_t kBytes = kOffBar + 256 + 1024;
 };
-static_assert(Lay<1>::kBytes <= 227 * 1024 && Lay<2>::kBytes <= 227 * 1024 && Lay<4>::kBytes <= 227 * 1024, "shared memory");
+static_assert(Lay<1>::kBytes <= 227 * 1024 && Lay<2>::kBytes <= 227 * 1024, "shared memory");
 static_assert(2 * 4 * 8 + 4 + 4 + sizeof(SharedTiles) <= 256, "barriers");
 
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
@@ -131,7 +146,7 @@ __global__ void __launch_bounds__(Lay<MT>::kThreads, 1)
     }
     build_sched(sched, a.offsets, a.E, static_cast<int>(a.M), L::kCap);
     __syncthreads();
-    const Ranges ranges(sched.base[a.E] * tiles_w, steps, static_cast<int>(gridDim.x), true, kFew, kFewMin);
+    const Ranges ranges(sched.base[a.E] * tiles_w, steps, static_cast<int>(gridDim.x), true, kFixUpSteps, kMinRange);
     SegIter<8> it(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
     Tile tl;
 
@@ -442,9 +457,9 @@ cudaError_t opt_in() {
 }  // namespace
 
 cudaError_t expert_gemv_init_device() {
-    cudaError_t e;
-    if ((e = opt_in<1>()) != cudaSuccess || (e = opt_in<2>()) != cudaSuccess) return e;
-    return opt_in<4>();
+    const cudaError_t e = opt_in<1>();
+    if (e != cudaSuccess) return e;
+    return opt_in<2>();
 }
 
 cudaError_t launch_expert_gemv(const CUtensorMap& x, const CUtensorMap& codes, const ExpertGemmArgs& a, const Nf4Tables& tab,
@@ -453,7 +468,6 @@ cudaError_t launch_expert_gemv(const CUtensorMap& x, const CUtensorMap& codes, c
         return cudaErrorInvalidValue;
     if (a.cap == 8) return launch_mt<1>(x, codes, a, tab, st);
     if (a.cap == 16) return launch_mt<2>(x, codes, a, tab, st);
-    if (a.cap == 32) return launch_mt<4>(x, codes, a, tab, st);
     return cudaErrorInvalidValue;
 }
 

@@ -323,7 +323,7 @@ cudaError_t launch_expert_gemm(bool trans_w, const CUtensorMap& act, const CUten
                                const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl,
                                cudaStream_t st);
 cudaError_t expert_gemm_init_device();
-// The forward in tiles of few rows (cap 8, 16 or 32): x box {64, cap} SW128,
+// The forward in tiles of few rows (cap 8 or 16): x box {64, cap} SW128,
 // codes {K/2, N, E} box {128, 256, 1} SW128. A programmatic dependent of the
 // launch that makes rank_x.
 cudaError_t launch_expert_gemv(const CUtensorMap& x, const CUtensorMap& codes, const ExpertGemmArgs& a, const Nf4Tables& tab,

@@ -50,14 +50,6 @@ __device__ __forceinline__ uint64_t mn_b_desc(uint32_t addr, int NR) {
     return d;
 }
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_free[2], tail_in, masked, drain;

@@ -58,7 +58,7 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// A box of one plane of a 3-D tensor.
+// TMA copy of a box of one plane of a 3-D tensor.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(

@@ -146,6 +146,42 @@ def test_experts_against_fp64(q, name):
     compare(t, run(q, t))
 
 
+# forwards in tiles of 8 and 16 rows: constants in whole words and not, one
+# expert with far more rows than the mean, tiles shared among CTAs beside whole
+# ones, a reduction that ends inside a step
+FEW = {
+    "tiles_of_8": dict(counts=[1, 0, 2, 6], N=520, K=256, r=8, dq=False, lead=3, pad=2),
+    "tiles_of_16": dict(counts=[9, 16, 0, 7], N=264, K=320, r=16, dq=False),
+    "words_16": dict(counts=[2, 11, 4], N=72, K=4096, r=64, lead=3, pad=5),
+    "skewed": dict(counts=[0, 60, 0, 0, 0, 4, 0, 0], N=264, K=1088, r=32),
+    "whole_and_shared": dict(counts=[1 + i % 4 for i in range(80)], N=264, K=1600, r=8),
+}
+
+
+@pytest.mark.parametrize("name", FEW)
+def test_few_rows_against_fp64(q, name):
+    t = case(**FEW[name])
+    a = run(q, t)
+    compare(t, a)
+    b = run(q, t)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+
+
+@pytest.mark.parametrize("counts", [[3, 5, 1], [9, 14, 6]], ids=["8", "16"])
+def test_few_rows_do_not_leak(q, counts):
+    """As for many rows: NaN and infinities stay in their own rows."""
+    t = case(counts, N=264, K=320, r=16, lead=2, pad=4)
+    clean = run(q, t)["Y"].cpu()
+    dirty = dict(t, X=t["X"].clone())
+    dirty["X"][:2], dirty["X"][-4:], dirty["X"][t["off"][1] + 1] = float("nan"), float("inf"), float("nan")
+    got = run(q, dirty)["Y"].cpu()
+    mine = torch.zeros(t["M"], dtype=torch.bool)
+    mine[t["off"][1] + 1] = True
+    assert torch.equal(clean[~mine], got[~mine])
+    assert torch.isnan(got[mine].float()).all()
+
+
 def test_recomputed_rank_input_and_determinism(q):
     t = case([70, 200, 0, 33], N=264, K=448, r=32)
     a, b, c = run(q, t), run(q, t), run(q, t, sT_given=False)
