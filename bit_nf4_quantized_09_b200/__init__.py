@@ -540,11 +540,11 @@ def expert_order(ids: torch.Tensor, E: int, order: torch.Tensor | None = None, o
     if not 1 <= E <= 512:
         raise QLoraError(-1, where, f"E = {E}")
     if order is None:
-        order = torch.empty(M, dtype=torch.int32, device=dev)
+        order = torch.empty_like(ids)
     else:
         _want(order, "order", where, (M,), torch.int32, dev)
     if offsets is None:
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        offsets = ids.new_empty(E + 1)
     else:
         _want(offsets, "offsets", where, (E + 1,), torch.int32, dev)
     _check(_on(dev, lib().qlora_expert_order, _ptr(ids), M, E, _ptr(order), _ptr(offsets)), where)
