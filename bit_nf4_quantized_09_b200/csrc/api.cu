@@ -1363,16 +1363,18 @@ struct GroupPlan {
     int cap = 64, part_rows = 0;
     size_t tickets_bytes = 0, part_bytes = 0;
 };
-GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps) {
+GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps, int big) {
     GroupPlan p;
+    const bool pair = big == 512;
     const int64_t act = std::max<int64_t>(1, std::min<int64_t>(E, M));  // experts with rows, at most
     const int64_t avg = std::max<int64_t>(1, cdiv(M, act)), tiles_w = cdiv(cols, 256);
-    const int64_t t64 = tiles_w * act * cdiv(avg, 64), per256 = cdiv(avg, 256), t256 = tiles_w * act * per256;
-    const double step256 = std::max(1.0, static_cast<double>(avg) / per256 / 190.0);
+    const int64_t t64 = tiles_w * act * cdiv(avg, 64), per_big = cdiv(avg, big), t_big = tiles_w * act * per_big;
+    const double rows = static_cast<double>(avg) / per_big;
+    const double step_big = pair ? std::max(0.5, rows / 2 / 220.0) : std::max(1.0, rows / 190.0);
     const double whole64 = static_cast<double>(cdiv(t64, kPlanSms) * steps);
     const double cost64 = std::min(whole64, static_cast<double>(t64) * steps / kPlanSms + kFixUp);
-    const double cost256 = static_cast<double>(cdiv(t256, kPlanSms) * steps) * step256;
-    p.cap = avg > 64 && cost256 <= cost64 ? 256 : 64;
+    const double cost_big = static_cast<double>(cdiv(t_big, pair ? kPlanSms / 2 : kPlanSms) * steps) * step_big;
+    p.cap = avg > 64 && cost_big <= cost64 ? big : 64;
     // an expert adds at most one partly filled token tile
     p.tickets_bytes = p.cap == 64 ? up256(static_cast<size_t>((M / 64 + act) * tiles_w) * 4) : 0;
     p.part_rows = p.cap == 64 ? static_cast<int>(std::min<int64_t>(M, 64)) : 0;
@@ -1422,7 +1424,7 @@ struct ExpertLayout {
 constexpr int kTermsT = 2, kTermsU = 3;
 ExpertLayout expert_layout(int op, int64_t M, int64_t N, int64_t K, int r, int E) {
     ExpertLayout L;
-    L.plan = op == QLORA_OP_BWD ? group_plan(M, E, K, cdiv(N, 64)) : group_plan(M, E, N, K / kBlock);
+    L.plan = op == QLORA_OP_BWD ? group_plan(M, E, K, cdiv(N, 64), 512) : group_plan(M, E, N, K / kBlock, 512);
     if (op == QLORA_OP_FWD) few_rows_plan(L.plan, M, E, N);
     L.tickets = 256;
     L.header = L.tickets + L.plan.tickets_bytes;
@@ -1511,20 +1513,21 @@ qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_
         QLORA_LAUNCH(launch_expert_gemv(t_act, t_codes, a, tables(), st), 1, "expert forward, few rows");
         return QLORA_OK;
     }
-    const uint32_t box = p.cap == 256 ? 64 : 16;
+    const bool pair = p.cap == 512;
+    const uint32_t box = pair ? 64 : 16, wrows = pair ? 128 : 256;
     QLORA_MAP(&t_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, red, M, red * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B,
               dx ? "dY" : "X");
     // the first term of sT (sU): bf16 as the output is
     QLORA_MAP(&t_lact, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_in, r, M, static_cast<uint64_t>(terms) * r * 2, 64, box,
               CU_TENSOR_MAP_SWIZZLE_128B, dx ? "sU" : "sT");
     if (dx) {
-        QLORA_MAP(&t_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, N, K / 2, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B,
-                  "codes", E);
+        QLORA_MAP(&t_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, N, K / 2, wrows / 2, 64,
+                  pair ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, "codes", E);
         QLORA_MAP(&t_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_w, K, r, K * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "A", E);
     } else {
-        QLORA_MAP(&t_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, N, K / 2, 32, 256, CU_TENSOR_MAP_SWIZZLE_32B,
+        QLORA_MAP(&t_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, N, K / 2, 32, wrows, CU_TENSOR_MAP_SWIZZLE_32B,
                   "codes", E);
-        QLORA_MAP(&t_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_w, r, N, static_cast<uint64_t>(r) * 2, 64, 256,
+        QLORA_MAP(&t_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_w, r, N, static_cast<uint64_t>(r) * 2, 64, wrows,
                   CU_TENSOR_MAP_SWIZZLE_128B, "B", E);
     }
     if (injected_failure()) return QLORA_ERR_CUDA;
@@ -1550,7 +1553,7 @@ struct Int8Layout {
 };
 Int8Layout int8_layout(int64_t M, int64_t N, int64_t K, int E) {
     Int8Layout L;
-    L.plan = group_plan(M, E, N, cdiv(K, 128));
+    L.plan = group_plan(M, E, N, cdiv(K, 128), 256);
     L.tickets = 256;
     L.header = L.tickets + L.plan.tickets_bytes;
     L.part = L.header;

@@ -40,34 +40,107 @@ constexpr int kDeqWarps = 16;
 constexpr int kGroups = 4, kGroupWarps = 4;
 constexpr int kWarpX = 16, kWarpC = 17, kWarpMma = 18;
 constexpr int kThreads = (kWarpMma + 1) * 32;
-constexpr uint32_t kWStage = 256 * 64 * 2;   // 32 KB
-constexpr uint32_t kCStage = 256 * 64 / 2;   // 8 KB of packed codes
 constexpr uint32_t kTmemCols = 512;
 
-// Shared memory by token capacity: with 256 tokens three stages of each kind,
-// with at most 64 four. (Two token and four weight stages of 256 tokens: the
-// token copies, 1 us, were not always ahead of the UMMAs; 735 us on 8192 rows.)
+// Tiles of up to 64 tokens run on single CTAs. Tiles of up to 512 tokens run on
+// pairs of CTAs (a cluster of two on neighbouring SMs, cta_group::2): each CTA
+// decodes 128 of the tile's 256 weight rows and holds half of its tokens, and
+// one UMMA of M = 256 reads both CTAs' shared memory, so a weight is decoded
+// for 512 tokens. The tokens are one UMMA's N, or two of up to 256 each.
 template <int CAP>
 struct Lay {
-    static constexpr int kPX = CAP == 256 ? 3 : 4;  // token stages
-    static constexpr int kPW = CAP == 256 ? 3 : 4;  // weight stages
-    static constexpr int kPC = CAP == 256 ? 3 : 4;
-    static constexpr int kBoxRows = CAP == 256 ? 64 : 16;  // token rows per TMA box
-    static constexpr uint32_t kXStage = CAP * 128;
+    static constexpr bool kPair = CAP == 512;
+    static constexpr int kRows = kPair ? 128 : 256;        // weight rows of a CTA
+    static constexpr int kPX = kPair ? 3 : 4, kPW = kPair ? 6 : 4, kPC = 4;  // token, weight and code stages
+    static constexpr int kBoxRows = kPair ? 64 : 16;       // token rows per TMA box
+    static constexpr uint32_t kXHalf = 128 * 128;          // a pair's CTA: 128 tokens of each UMMA
+    static constexpr uint32_t kXStage = kPair ? 2 * kXHalf : CAP * 128;
+    static constexpr uint32_t kWStage = kRows * 64 * 2;
+    static constexpr uint32_t kCStage = kRows * 64 / 2;    // packed codes
     static constexpr uint32_t kOffW = kPX * kXStage;
     static constexpr uint32_t kOffC = kOffW + kPW * kWStage;
     static constexpr uint32_t kOffSched = kOffC + kPC * kCStage;
     static constexpr uint32_t kOffBar = (kOffSched + sizeof(TileSched) + 63) / 64 * 64;
     static constexpr uint32_t kBytes = kOffBar + 512 + 1024;
 };
-static_assert(Lay<256>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "shared memory of one CTA");
+static_assert(Lay<512>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "shared memory of one CTA");
 // Code stages are a ring over all reduction steps, but each group waits on
 // barriers of its own (two, by the parity of its steps): it has not seen the
 // ring's other steps, and a phase parity is only safe to one who has seen the
 // phase before. Two steps of one barrier lie at least four reduction steps
 // apart (at the least when every second step is a rank-r step), so with at
 // most four stages the first has been consumed before the second is loaded.
-static_assert(Lay<256>::kPC <= 4 && Lay<64>::kPC <= 4, "code stages");
+// Weight stages need no such thing: before a group takes stage s for step g it
+// has waited for UMMA g - 4 - kPW, so with kPW >= 4 the phase before is over.
+static_assert(Lay<512>::kPC <= 4 && Lay<64>::kPC <= 4, "code stages");
+static_assert(Lay<512>::kPW >= kGroups && Lay<64>::kPW >= kGroups, "weight stages");
+
+// The tcgen05 forms of a CTA pair. The pair's UMMA takes the first 128 rows of
+// A and the first half of B's rows from the leader's (even) CTA, the others
+// from its partner's, at the same shared-memory addresses; each CTA's TMEM gets
+// its own 128 rows of D.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {  // a warp of each CTA
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(0x3))
+        : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if (kPair)
+        umma_commit_pair(bar);
+    else
+        umma_commit(bar);
+}
+
+// TMA copies into this CTA's shared memory that complete on a barrier of the
+// pair's leader (a mapa address).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// Arrives on a barrier of the pair's leader. What it releases stays in this
+// CTA's shared memory and TMEM, where this SM's tensor core meets it, so CTA
+// scope is enough; a release at cluster scope waits for the constants' loads in
+// flight as well, 1500 to 1900 cycles a step.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0)) : "memory");
+}
+
+// N of UMMA h of a pair's tile: its tokens 256 h on, in multiples of 32.
+__device__ __forceinline__ int pair_n(int rows, int h) { return min((max(rows - 256 * h, 0) + 31) & ~31, 256); }
 
 template <bool kTransW, bool kNoDq, int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -82,8 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* x_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
     uint64_t* x_empty = x_full + L::kPX;
     uint64_t* w_full = x_empty + L::kPX;
-    uint64_t* w_free = w_full + L::kPW;  // per group: the weight stage of its next step has been consumed
-    uint64_t* c_full = w_free + kGroups;
+    uint64_t* w_empty = w_full + L::kPW;
+    uint64_t* c_full = w_empty + L::kPW;
     uint64_t* c_empty = c_full + 2 * kGroups;
     uint64_t* acc = c_empty + L::kPC;
     uint64_t* tmem_free = acc + 1;
@@ -91,10 +164,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     SharedTiles* pending = reinterpret_cast<SharedTiles*>(const_cast<int*>(abort_flag) + 1);
-    static_assert((2 * L::kPX + L::kPW + 3 * kGroups + L::kPC + 3) * 8 + 8 + sizeof(SharedTiles) <= 512, "barriers");
+    static_assert((2 * L::kPX + 2 * L::kPW + 2 * kGroups + L::kPC + 3) * 8 + 8 + sizeof(SharedTiles) <= 512, "barriers");
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int KT = static_cast<int>((a.red + 63) / 64);
+    const int crank = L::kPair ? static_cast<int>(cluster_ctarank()) : 0;
+    const int unit = static_cast<int>(blockIdx.x) / (L::kPair ? 2 : 1), units = static_cast<int>(gridDim.x) / (L::kPair ? 2 : 1);
     const int tiles_w = static_cast<int>((a.out_cols + 255) / 256);
     const uint64_t tmo = a.timeout_ns;
 
@@ -103,20 +178,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(x_full + s, 1);
             mbar_init(x_empty + s, 1);
         }
-        for (int s = 0; s < L::kPW; ++s) mbar_init(w_full + s, kGroupWarps);
-        for (int s = 0; s < kGroups; ++s) mbar_init(w_free + s, 1);
+        for (int s = 0; s < L::kPW; ++s) {
+            mbar_init(w_full + s, kGroupWarps * (L::kPair ? 2 : 1));
+            mbar_init(w_empty + s, 1);
+        }
         for (int s = 0; s < 2 * kGroups; ++s) mbar_init(c_full + s, 1);
         for (int s = 0; s < L::kPC; ++s) mbar_init(c_empty + s, kGroupWarps);
         mbar_init(acc, 1);
-        mbar_init(tmem_free, kDeqWarps);
+        mbar_init(tmem_free, kDeqWarps * (L::kPair ? 2 : 1));
         mbar_init(drain, 1);
         *abort_flag = 0;
         pending->n = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
-        tmem_alloc(tmem_slot, kTmemCols);
-        tmem_relinquish();
+        if (L::kPair) {
+            tmem_alloc_pair(tmem_slot, kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, kTmemCols);
+            tmem_relinquish();
+        }
     }
     if (warp == kWarpX && lane == 0) {
         tma_prefetch_desc(&tm_act);
@@ -128,9 +210,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (L::kPair) cluster_sync();  // the partner's barriers are initialised before any remote arrival
     const uint32_t tmem = *tmem_slot;
-    const Ranges ranges(sched.base[a.E] * tiles_w, KT, static_cast<int>(gridDim.x), CAP == 64);
-    SegIter<> it(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
+    const Ranges ranges(sched.base[a.E] * tiles_w, KT, units, !L::kPair);
+    SegIter<> it(sched, ranges, unit, tiles_w);
     Tile tl;
     // steps of a segment: its reduction steps, and the rank-r step behind a tile's last
     auto steps_of = [&](const Tile& s) { return s.k_hi - s.k_lo + (s.k_hi == KT ? 1 : 0); };
@@ -141,7 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int g = 0;
             bool waited = false, ok = true;
             while (ok && it.next(tl)) {
-                const int boxes = (tl.rows + L::kBoxRows - 1) / L::kBoxRows, nk = tl.k_hi - tl.k_lo, steps = steps_of(tl);
+                // of a pair: this CTA's half of each UMMA's tokens
+                const int mine[2] = {L::kPair ? pair_n(tl.rows, 0) / 2 : tl.rows, L::kPair ? pair_n(tl.rows, 1) / 2 : 0};
+                const int boxes[2] = {(mine[0] + L::kBoxRows - 1) / L::kBoxRows, (mine[1] + L::kBoxRows - 1) / L::kBoxRows};
+                const int nk = tl.k_hi - tl.k_lo, steps = steps_of(tl);
                 for (int i = 0; i < steps; ++i, ++g) {
                     const int s = g % L::kPX;
                     if (g >= L::kPX && !mbar_wait(x_empty + s, static_cast<uint32_t>(g / L::kPX - 1) & 1u, tmo, a.status)) {
@@ -161,14 +247,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                         waited = true;
                     }
                     uint8_t* st = smem + s * L::kXStage;
-                    mbar_arrive_expect_tx(x_full + s, static_cast<uint32_t>(boxes) * L::kBoxRows * 128u);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(st + b * L::kBoxRows * 128, rank ? &tm_lact : &tm_act, x_full + s,
-                                    rank ? 0 : (tl.k_lo + i) * 64, tl.row0 + b * L::kBoxRows);
+                    // the leader expects the bytes of both CTAs of a pair
+                    if (crank == 0)
+                        mbar_arrive_expect_tx(x_full + s, static_cast<uint32_t>(boxes[0] + boxes[1]) * L::kBoxRows * 128u *
+                                                              (L::kPair ? 2u : 1u));
+                    const CUtensorMap* map = rank ? &tm_lact : &tm_act;
+                    const int x = rank ? 0 : (tl.k_lo + i) * 64;
+                    for (int h = 0; h < (L::kPair ? 2 : 1); ++h)
+                        for (int b = 0; b < boxes[h]; ++b) {
+                            uint8_t* dst = st + h * L::kXHalf + b * L::kBoxRows * 128;
+                            const int row = tl.row0 + 256 * h + crank * mine[h] + b * L::kBoxRows;
+                            if (L::kPair)
+                                tma_load_2d_pair(dst, map, mapa_shared(smem_u32(x_full + s), 0), x, row);
+                            else
+                                tma_load_2d(dst, map, x_full + s, x, row);
+                        }
                 }
             }
-            for (int j = max(0, g - L::kPX); j < g; ++j)
-                mbar_wait(x_full + j % L::kPX, static_cast<uint32_t>(j / L::kPX) & 1u, tmo, nullptr);
+            // no copy still landing when the CTA ends; a partner's complete on the
+            // leader's barriers: they have been consumed or, after an abort, land
+            // while it waits for what no one signals
+            if (crank == 0) {
+                for (int j = max(0, g - L::kPX); j < g; ++j)
+                    mbar_wait(x_full + j % L::kPX, static_cast<uint32_t>(j / L::kPX) & 1u, tmo, nullptr);
+            } else if (!ok) {
+                mbar_wait(x_full, 0u, 1000000u, nullptr);  // 1 ms
+            }
         }
         __syncwarp();
     } else if (warp == kWarpC) {
@@ -193,12 +297,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int kt = tl.k_lo + i;
                     par ^= 1u << G;
-                    mbar_arrive_expect_tx(bar, kCStage);
+                    mbar_arrive_expect_tx(bar, L::kCStage);
                     // rows past the expert's N and columns past K read as zeros
                     if (!kTransW)
-                        tma_load_3d(smem + L::kOffC + s * kCStage, &tm_codes, bar, kt * 32, tl.w0, tl.e);
+                        tma_load_3d(smem + L::kOffC + s * L::kCStage, &tm_codes, bar, kt * 32, tl.w0 + crank * L::kRows, tl.e);
                     else
-                        tma_load_3d(smem + L::kOffC + s * kCStage, &tm_codes, bar, tl.w0 / 2, kt * 64, tl.e);
+                        tma_load_3d(smem + L::kOffC + s * L::kCStage, &tm_codes, bar, (tl.w0 + crank * L::kRows) / 2, kt * 64, tl.e);
                 }
             }
             // after an abort copies may still be landing: every stage's last
@@ -212,11 +316,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kWarpMma) {
         // ----------------------------------------------------------- MMA --
         const bool leader = elect_one();
+        if (L::kPair && crank == 1) {
+            it.stop();  // the leader issues for both CTAs
+        }
         // descriptors of stage 0; later stages and steps add their byte offset / 16
         const uint64_t xd0 = sw128_desc(smem_u32(smem), 16, 1024);
         const uint64_t wd0 = kTransW ? sw128_desc(smem_u32(smem + L::kOffW), 8192, 1024)
                                      : sw128_desc(smem_u32(smem + L::kOffW), 16, 1024);
         constexpr uint32_t kWk = (kTransW ? 2048 : 32) / 16;
+        auto mma = [](uint32_t d, uint64_t wd, uint64_t xd, uint32_t idesc, uint32_t acc_) {
+            if (L::kPair)
+                umma_f16_pair(d, wd, xd, idesc, acc_);
+            else
+                umma_f16(d, wd, xd, idesc, acc_);
+        };
         int g = 0, n = 0;
         bool ok = true;
         while (ok && uniform(it.next(tl))) {
@@ -224,32 +337,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             tc_fence_after();
             const int nk = uniform(tl.k_hi - tl.k_lo), steps = uniform(steps_of(tl));
-            const uint32_t idesc = idesc_bf16(128, uniform((tl.rows + 15) & ~15), kTransW, false);
+            // two UMMAs at a time: halves of the weight rows, or of a pair's tokens
+            const int rows = uniform(tl.rows);
+            const bool two = !L::kPair || rows > 256;
+            const uint32_t idesc[2] = {idesc_bf16(L::kPair ? 256 : 128, L::kPair ? pair_n(rows, 0) : (rows + 15) & ~15, kTransW, false),
+                                       idesc_bf16(L::kPair ? 256 : 128, L::kPair ? pair_n(rows, 1) : (rows + 15) & ~15, kTransW, false)};
+            // the second UMMA's operands, behind the first's
+            constexpr uint32_t kW2 = L::kPair ? 0 : 16384 / 16, kX2 = L::kPair ? L::kXHalf / 16 : 0;
             for (int i = 0; i < steps; ++i, ++g) {
                 const int sx = g % L::kPX, sw = g % L::kPW;
-                ok = wait_both(x_full + sx, static_cast<uint32_t>(g / L::kPX) & 1u, w_full + sw,
-                               static_cast<uint32_t>(g / L::kPW) & 1u, tmo, a.status);
+                const uint32_t x_par = static_cast<uint32_t>(g / L::kPX) & 1u, w_par = static_cast<uint32_t>(g / L::kPW) & 1u;
+                ok = wait_both(x_full + sx, x_par, w_full + sw, w_par, tmo, a.status);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
                     const uint64_t xd = xd0 + static_cast<uint32_t>(sx) * (L::kXStage / 16);
-                    const uint64_t wd = wd0 + static_cast<uint32_t>(sw) * (kWStage / 16);
+                    const uint64_t wd = wd0 + static_cast<uint32_t>(sw) * (L::kWStage / 16);
                     if (i < nk) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                umma_f16(tmem + h * 256, wd + h * (16384 / 16) + kk * kWk, xd + kk * 2, idesc,
-                                         (i > 0 || kk > 0) ? 1u : 0u);
+                                if (h == 0 || two)
+                                    mma(tmem + h * 256, wd + h * kW2 + kk * kWk, xd + h * kX2 + kk * 2, idesc[h],
+                                        (i > 0 || kk > 0) ? 1u : 0u);
                     } else {
                         for (int kk = 0; kk < (a.rank_cols + 15) / 16; ++kk)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                umma_f16(tmem + h * 256, wd + h * (16384 / 16) + kk * kWk, xd + kk * 2, idesc, 1u);
+                                if (h == 0 || two) mma(tmem + h * 256, wd + h * kW2 + kk * kWk, xd + h * kX2 + kk * 2, idesc[h], 1u);
                     }
-                    umma_commit(x_empty + sx);
-                    umma_commit(w_free + ((g + L::kPW) & (kGroups - 1)));  // of step g + kPW, which takes this stage
-                    if (i == steps - 1) umma_commit(acc);
+                    commit<L::kPair>(x_empty + sx);
+                    commit<L::kPair>(w_empty + sw);
+                    if (i == steps - 1) commit<L::kPair>(acc);
                 }
                 __syncwarp();
             }
@@ -257,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) *abort_flag = 1;
         // no UMMA in flight when the TMEM is freed
-        if (leader) umma_commit(drain);
+        if (leader && crank == 0) commit<L::kPair>(drain);
         mbar_wait(drain, 0u, tmo, nullptr);
         __syncwarp();
     } else {
@@ -272,12 +392,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // `pi` walk that step's position.
         const int KB = static_cast<int>(a.K / kBlock);
         const float mean = kNoDq ? 0.0f : __ldg(a.c.mean);
-        SegIter<> pit(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
+        SegIter<> pit(sched, ranges, unit, tiles_w);
+        constexpr int kU = L::kRows / 128;  // blocks of a thread
+        const int w_off = crank * L::kRows;
         Tile ptl;
         int pi = G;
         bool plive = pit.next(ptl);
-        uint32_t raw_q[2] = {0u, 0u};
-        float raw_s[2] = {0.0f, 0.0f};
+        uint32_t raw_q[kU] = {};
+        float raw_s[kU] = {};
         auto load_constants = [&]() {
             while (plive && pi >= steps_of(ptl)) {
                 pi -= steps_of(ptl);
@@ -286,12 +408,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!plive || pi >= ptl.k_hi - ptl.k_lo) return;  // nothing left, or the rank-r step
             const int kt = ptl.k_lo + pi;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < kU; ++u) {
                 // weight row n and k-block of block u; past the edges of the
                 // expert's weight the nearest one inside (not used: codes 0
                 // there meet zeros of dY or columns that are not written)
-                const int n = min(kTransW ? kt * 64 + (t & 63) : ptl.w0 + t + 128 * u, static_cast<int>(a.N) - 1);
-                const int kb = min(kTransW ? ptl.w0 / kBlock + (t >> 6) + 2 * u : kt, KB - 1);
+                const int n = min(kTransW ? kt * 64 + (t & 63) : ptl.w0 + w_off + t + 128 * u, static_cast<int>(a.N) - 1);
+                const int kb = min(kTransW ? (ptl.w0 + w_off) / kBlock + (t >> 6) + 2 * u : kt, KB - 1);
                 const uint32_t ib = (static_cast<uint32_t>(ptl.e) * static_cast<uint32_t>(a.N) + n) * KB + kb;  // < 2^32
                 if (kNoDq) {
                     raw_s[u] = __ldg(a.c.absmax + ib);
@@ -302,34 +424,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         load_constants();
+        // this warp's share of a weight stage is there (a pair's: the leader knows)
+        auto arrive_w = [&](int s) {
+            if (L::kPair)
+                arrive_leader(w_full + s);
+            else
+                mbar_arrive(w_full + s);
+        };
         bool ok = true;
         int g0 = 0, gk0 = 0, n = 0;  // steps and reduction steps before this tile
-        int jobs = 0, kjobs = 0;     // steps and reduction steps of this group
+        int kjobs = 0;               // reduction steps of this group
         while (ok && it.next(tl)) {
             const int nk = tl.k_hi - tl.k_lo, steps = steps_of(tl);
-            for (int i = (G - g0) & (kGroups - 1); ok && i < steps; i += kGroups, ++jobs) {
+            for (int i = (G - g0) & (kGroups - 1); ok && i < steps; i += kGroups) {
                 // the weight stage is taken as late as possible: the codes
                 // are read before the wait
                 const int sw = (g0 + i) % L::kPW;
-                uint8_t* wst = smem + L::kOffW + sw * kWStage;
-                // the first step to take each weight stage has nothing to wait
-                // for: the phase before a barrier's first counts as complete
-                const int uses = jobs - (G < L::kPW ? 1 : 0);
+                uint8_t* wst = smem + L::kOffW + sw * L::kWStage;
+                // the stage's step before has been consumed; a stage's first step
+                // has nothing to wait for (the phase before a barrier's first
+                // counts as complete)
+                const uint32_t w_par = static_cast<uint32_t>((g0 + i) / L::kPW - 1) & 1u;
                 if (i < nk) {
                     const int gk = gk0 + i, sc = gk % L::kPC;
-                    ok = wait_both(c_full + 2 * G + (kjobs & 1), static_cast<uint32_t>(kjobs >> 1) & 1u, w_free + G,
-                                   static_cast<uint32_t>(uses) & 1u, tmo, a.status);
+                    ok = wait_both(c_full + 2 * G + (kjobs & 1), static_cast<uint32_t>(kjobs >> 1) & 1u, w_empty + sw,
+                                   w_par, tmo, a.status);
                     if (!ok) break;
                     ++kjobs;
-                    const uint32_t codes = smem_u32(smem + L::kOffC + sc * kCStage);
-                    uint4 ca[2], cb[2];
-                    uint32_t dst[2], swz;
+                    const uint32_t codes = smem_u32(smem + L::kOffC + sc * L::kCStage);
+                    uint4 ca[kU], cb[kU];
+                    uint32_t dst[kU], swz;
                     if (!kTransW) {
                         // rows t and t + 128 of the weight tile: 32 code bytes, 32-byte swizzle
                         const uint32_t s32 = (t >> 2) & 1;
                         swz = t & 7;
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
+                        for (int u = 0; u < kU; ++u) {
                             const uint32_t crow = codes + (t + 128 * u) * 32;
                             ca[u] = lds128(crow + ((0 ^ s32) << 4));
                             cb[u] = lds128(crow + ((1 ^ s32) << 4));
@@ -338,21 +468,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         // reduction row nl, k-blocks b and b + 2 of the tile's four
                         const uint32_t nl = t & 63, b = t >> 6;
-                        const uint32_t crow = codes + nl * 128;
+                        const uint32_t crow = codes + nl * (L::kPair ? 64 : 128);
+                        const uint32_t csw = L::kPair ? (nl >> 1) & 3 : nl & 7;  // 64- or 128-byte swizzle
                         swz = nl & 7;
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            ca[u] = lds128(crow + (((2 * b + 4 * u) ^ swz) << 4));
-                            cb[u] = lds128(crow + (((2 * b + 4 * u + 1) ^ swz) << 4));
+                        for (int u = 0; u < kU; ++u) {
+                            ca[u] = lds128(crow + (((2 * b + 4 * u) ^ csw) << 4));
+                            cb[u] = lds128(crow + (((2 * b + 4 * u + 1) ^ csw) << 4));
                             dst[u] = smem_u32(wst) + (b + 2 * u) * 8192 + (nl >> 3) * 1024 + (nl & 7) * 128 + (swz << 4);
                         }
                     }
-                    const float cp[2] = {kNoDq ? raw_s[0] : __fmaf_rn(e4m3_to_f32(raw_q[0]), raw_s[0], mean),
-                                         kNoDq ? raw_s[1] : __fmaf_rn(e4m3_to_f32(raw_q[1]), raw_s[1], mean)};
+                    float cp[kU];
+#pragma unroll
+                    for (int u = 0; u < kU; ++u)
+                        cp[u] = kNoDq ? raw_s[u] : __fmaf_rn(e4m3_to_f32(raw_q[u]), raw_s[u], mean);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(c_empty + sc);  // the codes have been read
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
+                    for (int u = 0; u < kU; ++u) {
                         const Nf4BlockLut lut = make_block_lut(tab.level, cp[u]);
                         const uint32_t words[8] = {ca[u].x, ca[u].y, ca[u].z, ca[u].w, cb[u].x, cb[u].y, cb[u].z, cb[u].w};
 #pragma unroll
@@ -368,23 +501,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_smem();  // -> visible to the tensor core
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(w_full + sw);
+                    if (lane == 0) arrive_w(sw);
                 } else {
                     // rank-r step: B_e rows (forward) or A_e columns (dX) by TMA
                     pi += kGroups;
                     load_constants();
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(w_free + G, static_cast<uint32_t>(uses) & 1u, tmo, a.status));
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(w_empty + sw, w_par, tmo, a.status));
                     if (!ok) break;
                     if (leader) {
-                        mbar_arrive_expect_tx(w_full + sw, kWStage);
-                        if (!kTransW) {
-                            tma_load_3d(wst, &tm_lw, w_full + sw, 0, tl.w0, tl.e);
-                        } else {
-                            for (int b = 0; b < 4; ++b)
-                                tma_load_3d(wst + b * 8192, &tm_lw, w_full + sw, tl.w0 + 64 * b, 0, tl.e);
+                        if (crank == 0)
+                            mbar_arrive_expect_tx(w_full + sw, L::kWStage * (L::kPair ? 2u : 1u));
+                        else
+                            arrive_w(sw);
+                        for (int b = 0; b < (kTransW ? 2 * kU : 1); ++b) {
+                            const int x = kTransW ? tl.w0 + w_off + 64 * b : 0, y = kTransW ? 0 : tl.w0 + w_off;
+                            if (L::kPair)
+                                tma_load_3d_pair(wst + b * 8192, &tm_lw, mapa_shared(smem_u32(w_full + sw), 0), x, y, tl.e);
+                            else
+                                tma_load_3d(wst + b * 8192, &tm_lw, w_full + sw, x, y, tl.e);
                         }
                     } else if (lane == 0) {
-                        mbar_arrive(w_full + sw);
+                        arrive_w(sw);
                     }
                     __syncwarp();
                 }
@@ -398,7 +535,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc, static_cast<uint32_t>(n) & 1u, tmo, a.status)) && ok;
             tc_fence_after();
             const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * 256;
-            const int nl = h * 128 + q * 32 + lane;  // tile row (output column) of this lane
+            // output column of this lane in the tile, and the first of this warp's
+            // tokens: h is a half of a CTA's weight rows, or of a pair's tokens
+            const int nl = L::kPair ? w_off + q * 32 + lane : h * 128 + q * 32 + lane;
+            const int tok0 = L::kPair ? 256 * h : 0;
+            const int toks = L::kPair ? min(tl.rows - tok0, 256) : tl.rows;
             if (CAP != 64 || nk == KT) {
                 // lane = output column, register = token: two neighbouring
                 // lanes swap halves of a token pair, so each lane stores two
@@ -406,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // covers two 64-byte row segments
                 const int col = tl.w0 + (nl & ~1);
                 const bool write = ok && col < a.out_cols;
-                for (int c = part * 32; c < tl.rows; c += 64) {
+                for (int c = part * 32; c < toks; c += 64) {
                     uint32_t r[32];
                     tmem_ld32(trow + c, r);
                     tmem_ld_wait();
@@ -416,14 +557,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
                         const uint32_t lo = (lane & 1) ? got : r[i], hi = (lane & 1) ? r[i + 1] : got;
                         const int tok = c + i + (lane & 1);
-                        if (write && tok < tl.rows)
-                            *reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(tl.row0 + tok) * a.out_cols + col) =
+                        if (write && tok < toks)
+                            *reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(tl.row0 + tok0 + tok) * a.out_cols + col) =
                                 pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(tmem_free);
+                if (lane == 0) {
+                    if (L::kPair)
+                        arrive_leader(tmem_free);
+                    else
+                        mbar_arrive(tmem_free);
+                }
             } else if (CAP == 64) {
                 // partial sums [token][256 columns] to this CTA's slot
                 const int slot_floats = a.part_rows * 256;
@@ -480,9 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
+    if (L::kPair) cluster_sync();  // the leader's UMMAs read and write both CTAs
     if (warp == kWarpMma) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        if (L::kPair)
+            tmem_dealloc_pair(tmem, kTmemCols);
+        else
+            tmem_dealloc(tmem, kTmemCols);
     }
     // launched as a programmatic dependent, the grid completes only after its primary
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -496,11 +646,16 @@ cudaError_t launch_one(const CUtensorMap& act, const CUtensorMap& codes, const C
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Lay<CAP>::kBytes;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = Lay<CAP>::kPair ? 2 : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = pdl ? 2 : 1;
+    if (Lay<CAP>::kPair) cfg.gridDim.x &= ~1u;
     return cudaLaunchKernelEx(&cfg, expert_gemm<kTransW, kNoDq, CAP>, act, codes, lact, lw, a, tab);
 }
 
@@ -508,16 +663,16 @@ template <bool kTransW>
 cudaError_t launch_dir(const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact, const CUtensorMap& lw,
                        const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl, cudaStream_t st) {
     if (a.c.absmax)
-        return a.cap == 256 ? launch_one<kTransW, true, 256>(act, codes, lact, lw, a, tab, pdl, st)
+        return a.cap == 512 ? launch_one<kTransW, true, 512>(act, codes, lact, lw, a, tab, pdl, st)
                             : launch_one<kTransW, true, 64>(act, codes, lact, lw, a, tab, pdl, st);
-    return a.cap == 256 ? launch_one<kTransW, false, 256>(act, codes, lact, lw, a, tab, pdl, st)
+    return a.cap == 512 ? launch_one<kTransW, false, 512>(act, codes, lact, lw, a, tab, pdl, st)
                         : launch_one<kTransW, false, 64>(act, codes, lact, lw, a, tab, pdl, st);
 }
 
 template <bool kTransW, bool kNoDq>
 cudaError_t opt_in() {
-    cudaError_t e = cudaFuncSetAttribute(expert_gemm<kTransW, kNoDq, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Lay<256>::kBytes));
+    cudaError_t e = cudaFuncSetAttribute(expert_gemm<kTransW, kNoDq, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Lay<512>::kBytes));
     if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(expert_gemm<kTransW, kNoDq, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(Lay<64>::kBytes));
@@ -536,7 +691,7 @@ cudaError_t expert_gemm_init_device() {
 cudaError_t launch_expert_gemm(bool trans_w, const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact,
                                const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl,
                                cudaStream_t st) {
-    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 1 || (a.cap != 64 && a.cap != 256) || a.rank_cols < 1 || a.rank_cols > 64)
+    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 2 || (a.cap != 64 && a.cap != 512) || a.rank_cols < 1 || a.rank_cols > 64)
         return cudaErrorInvalidValue;
     return trans_w ? launch_dir<true>(act, codes, lact, lw, a, tab, pdl, st)
                    : launch_dir<false>(act, codes, lact, lw, a, tab, pdl, st);

@@ -209,6 +209,10 @@ struct SegIter {
             u1 = r.begin(c + 1);
         }
     }
+    __device__ void stop() {
+        tile = r.whole;
+        u = u1;
+    }
     __device__ bool next(Tile& out) {
         if (tile < r.whole) {
             out.id = tile;
