@@ -51,14 +51,14 @@ template <int CAP>
 struct Lay {
     static constexpr bool kPair = CAP == 512;
     static constexpr int kRows = kPair ? 128 : 256;        // weight rows of a CTA
-    static constexpr int kPX = kPair ? 3 : 4, kPW = kPair ? 6 : 4, kPC = 4;  // token, weight and code stages
+    static constexpr int kP = 4, kPC = 4;                  // operand (token and weight) and code stages
     static constexpr int kBoxRows = kPair ? 64 : 16;       // token rows per TMA box
     static constexpr uint32_t kXHalf = 128 * 128;          // a pair's CTA: 128 tokens of each UMMA
     static constexpr uint32_t kXStage = kPair ? 2 * kXHalf : CAP * 128;
     static constexpr uint32_t kWStage = kRows * 64 * 2;
     static constexpr uint32_t kCStage = kRows * 64 / 2;    // packed codes
-    static constexpr uint32_t kOffW = kPX * kXStage;
-    static constexpr uint32_t kOffC = kOffW + kPW * kWStage;
+    static constexpr uint32_t kOffW = kP * kXStage;
+    static constexpr uint32_t kOffC = kOffW + kP * kWStage;
     static constexpr uint32_t kOffSched = kOffC + kPC * kCStage;
     static constexpr uint32_t kOffBar = (kOffSched + sizeof(TileSched) + 63) / 64 * 64;
     static constexpr uint32_t kBytes = kOffBar + 512 + 1024;
@@ -70,10 +70,11 @@ static_assert(Lay<512>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "
 // phase before. Two steps of one barrier lie at least four reduction steps
 // apart (at the least when every second step is a rank-r step), so with at
 // most four stages the first has been consumed before the second is loaded.
-// Weight stages need no such thing: before a group takes stage s for step g it
-// has waited for UMMA g - 4 - kPW, so with kPW >= 4 the phase before is over.
+// Operand stages need no such thing: before a group takes stage s for step g it
+// has waited for the UMMAs of step g - 4 - kP, so with kP >= 4 the phase before
+// is over.
 static_assert(Lay<512>::kPC <= 4 && Lay<64>::kPC <= 4, "code stages");
-static_assert(Lay<512>::kPW >= kGroups && Lay<64>::kPW >= kGroups, "weight stages");
+static_assert(Lay<512>::kP >= kGroups && Lay<64>::kP >= kGroups, "operand stages");
 
 // The tcgen05 forms of a CTA pair. The pair's UMMA takes the first 128 rows of
 // A and the first half of B's rows from the leader's (even) CTA, the others
@@ -152,11 +153,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     TileSched& sched = *reinterpret_cast<TileSched*>(smem + L::kOffSched);
-    uint64_t* x_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
-    uint64_t* x_empty = x_full + L::kPX;
-    uint64_t* w_full = x_empty + L::kPX;
-    uint64_t* w_empty = w_full + L::kPW;
-    uint64_t* c_full = w_empty + L::kPW;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);  // tokens and weights of a step
+    uint64_t* empty = full + L::kP;
+    uint64_t* c_full = empty + L::kP;
     uint64_t* c_empty = c_full + 2 * kGroups;
     uint64_t* acc = c_empty + L::kPC;
     uint64_t* tmem_free = acc + 1;
@@ -164,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     SharedTiles* pending = reinterpret_cast<SharedTiles*>(const_cast<int*>(abort_flag) + 1);
-    static_assert((2 * L::kPX + 2 * L::kPW + 2 * kGroups + L::kPC + 3) * 8 + 8 + sizeof(SharedTiles) <= 512, "barriers");
+    static_assert((2 * L::kP + 2 * kGroups + L::kPC + 3) * 8 + 8 + sizeof(SharedTiles) <= 512, "barriers");
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int KT = static_cast<int>((a.red + 63) / 64);
@@ -174,13 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t tmo = a.timeout_ns;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < L::kPX; ++s) {
-            mbar_init(x_full + s, 1);
-            mbar_init(x_empty + s, 1);
-        }
-        for (int s = 0; s < L::kPW; ++s) {
-            mbar_init(w_full + s, kGroupWarps * (L::kPair ? 2 : 1));
-            mbar_init(w_empty + s, 1);
+        for (int s = 0; s < L::kP; ++s) {
+            mbar_init(full + s, 1 + kGroupWarps * (L::kPair ? 2 : 1));  // the token producer and the decoders
+            mbar_init(empty + s, 1);
         }
         for (int s = 0; s < 2 * kGroups; ++s) mbar_init(c_full + s, 1);
         for (int s = 0; s < L::kPC; ++s) mbar_init(c_empty + s, kGroupWarps);
@@ -220,59 +215,60 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kWarpX) {
         // ------------------------------------------- token-tile producer --
-        if (lane == 0) {
-            int g = 0;
-            bool waited = false, ok = true;
-            while (ok && it.next(tl)) {
-                // of a pair: this CTA's half of each UMMA's tokens
-                const int mine[2] = {L::kPair ? pair_n(tl.rows, 0) / 2 : tl.rows, L::kPair ? pair_n(tl.rows, 1) / 2 : 0};
-                const int boxes[2] = {(mine[0] + L::kBoxRows - 1) / L::kBoxRows, (mine[1] + L::kBoxRows - 1) / L::kBoxRows};
-                const int nk = tl.k_hi - tl.k_lo, steps = steps_of(tl);
-                for (int i = 0; i < steps; ++i, ++g) {
-                    const int s = g % L::kPX;
-                    if (g >= L::kPX && !mbar_wait(x_empty + s, static_cast<uint32_t>(g / L::kPX - 1) & 1u, tmo, a.status)) {
-                        *abort_flag = 1;
-                        ok = false;
-                        break;
+        const bool leader = elect_one();
+        const int cr = uniform(crank);
+        int g = 0;
+        bool waited = false, ok = true;
+        while (ok && uniform(it.next(tl))) {
+            // of a pair: this CTA's half of each UMMA's tokens
+            const int rows = uniform(tl.rows), row0 = uniform(tl.row0), k_lo = uniform(tl.k_lo);
+            const int nk = uniform(tl.k_hi) - k_lo, steps = uniform(steps_of(tl));
+            const int mine[2] = {L::kPair ? pair_n(rows, 0) / 2 : rows, L::kPair ? pair_n(rows, 1) / 2 : 0};
+            const int boxes[2] = {(mine[0] + L::kBoxRows - 1) / L::kBoxRows, (mine[1] + L::kBoxRows - 1) / L::kBoxRows};
+            // the leader expects the bytes of both CTAs of a pair
+            const uint32_t bytes = static_cast<uint32_t>(boxes[0] + boxes[1]) * L::kBoxRows * 128u * (L::kPair ? 2u : 1u);
+            auto load = [&](const CUtensorMap* map, int s, int x) {
+                if (!leader) return;
+                if (cr == 0) mbar_arrive_expect_tx(full + s, bytes);
+#pragma unroll
+                for (int h = 0; h < (L::kPair ? 2 : 1); ++h)
+                    for (int b = 0; b < boxes[h]; ++b) {
+                        uint8_t* dst = smem + s * L::kXStage + h * L::kXHalf + b * L::kBoxRows * 128;
+                        const int row = row0 + 256 * h + cr * mine[h] + b * L::kBoxRows;
+                        if (L::kPair)
+                            tma_load_2d_pair(dst, map, mapa_shared(smem_u32(full + s), 0), x, row);
+                        else
+                            tma_load_2d(dst, map, full + s, x, row);
                     }
-                    if (*abort_flag) {
-                        ok = false;
-                        break;
-                    }
-                    const bool rank = i >= nk;
-                    if (rank && !waited) {
-                        // sT or sU of the preceding launch, of which this one
-                        // may be a programmatic dependent
-                        asm volatile("griddepcontrol.wait;" ::: "memory");
-                        waited = true;
-                    }
-                    uint8_t* st = smem + s * L::kXStage;
-                    // the leader expects the bytes of both CTAs of a pair
-                    if (crank == 0)
-                        mbar_arrive_expect_tx(x_full + s, static_cast<uint32_t>(boxes[0] + boxes[1]) * L::kBoxRows * 128u *
-                                                              (L::kPair ? 2u : 1u));
-                    const CUtensorMap* map = rank ? &tm_lact : &tm_act;
-                    const int x = rank ? 0 : (tl.k_lo + i) * 64;
-                    for (int h = 0; h < (L::kPair ? 2 : 1); ++h)
-                        for (int b = 0; b < boxes[h]; ++b) {
-                            uint8_t* dst = st + h * L::kXHalf + b * L::kBoxRows * 128;
-                            const int row = tl.row0 + 256 * h + crank * mine[h] + b * L::kBoxRows;
-                            if (L::kPair)
-                                tma_load_2d_pair(dst, map, mapa_shared(smem_u32(x_full + s), 0), x, row);
-                            else
-                                tma_load_2d(dst, map, x_full + s, x, row);
-                        }
+            };
+            for (int i = 0; i < steps; ++i, ++g) {
+                const int s = g % L::kP;
+                if (g >= L::kP) ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(g / L::kP - 1) & 1u, tmo,
+                                                                       a.status));
+                if (!ok) *abort_flag = 1;
+                if (*abort_flag) ok = false;
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (i < nk) {
+                    load(&tm_act, s, (k_lo + i) * 64);
+                } else {
+                    // sT or sU of the preceding launch, of which this one may
+                    // be a programmatic dependent
+                    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+                    waited = true;
+                    load(&tm_lact, s, 0);
                 }
+                __syncwarp();
             }
-            // no copy still landing when the CTA ends; a partner's complete on the
-            // leader's barriers: they have been consumed or, after an abort, land
-            // while it waits for what no one signals
-            if (crank == 0) {
-                for (int j = max(0, g - L::kPX); j < g; ++j)
-                    mbar_wait(x_full + j % L::kPX, static_cast<uint32_t>(j / L::kPX) & 1u, tmo, nullptr);
-            } else if (!ok) {
-                mbar_wait(x_full, 0u, 1000000u, nullptr);  // 1 ms
-            }
+        }
+        // no copy still landing when the CTA ends; a partner's complete on the
+        // leader's barriers: they have been consumed or, after an abort, land
+        // while it waits for what no one signals
+        if (cr == 0) {
+            for (int j = max(0, g - L::kP); j < g; ++j)
+                mbar_wait(full + j % L::kP, static_cast<uint32_t>(j / L::kP) & 1u, tmo, nullptr);
+        } else if (!ok) {
+            mbar_wait(full, 0u, 1000000u, nullptr);  // 1 ms
         }
         __syncwarp();
     } else if (warp == kWarpC) {
@@ -345,14 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the second UMMA's operands, behind the first's
             constexpr uint32_t kW2 = L::kPair ? 0 : 16384 / 16, kX2 = L::kPair ? L::kXHalf / 16 : 0;
             for (int i = 0; i < steps; ++i, ++g) {
-                const int sx = g % L::kPX, sw = g % L::kPW;
-                const uint32_t x_par = static_cast<uint32_t>(g / L::kPX) & 1u, w_par = static_cast<uint32_t>(g / L::kPW) & 1u;
-                ok = wait_both(x_full + sx, x_par, w_full + sw, w_par, tmo, a.status);
+                const int s = g % L::kP;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + s, static_cast<uint32_t>(g / L::kP) & 1u, tmo, a.status));
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
-                    const uint64_t xd = xd0 + static_cast<uint32_t>(sx) * (L::kXStage / 16);
-                    const uint64_t wd = wd0 + static_cast<uint32_t>(sw) * (L::kWStage / 16);
+                    const uint64_t xd = xd0 + static_cast<uint32_t>(s) * (L::kXStage / 16);
+                    const uint64_t wd = wd0 + static_cast<uint32_t>(s) * (L::kWStage / 16);
                     if (i < nk) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -367,8 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int h = 0; h < 2; ++h)
                                 if (h == 0 || two) mma(tmem + h * 256, wd + h * kW2 + kk * kWk, xd + h * kX2 + kk * 2, idesc[h], 1u);
                     }
-                    commit<L::kPair>(x_empty + sx);
-                    commit<L::kPair>(w_empty + sw);
+                    commit<L::kPair>(empty + s);
                     if (i == steps - 1) commit<L::kPair>(acc);
                 }
                 __syncwarp();
@@ -427,9 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this warp's share of a weight stage is there (a pair's: the leader knows)
         auto arrive_w = [&](int s) {
             if (L::kPair)
-                arrive_leader(w_full + s);
+                arrive_leader(full + s);
             else
-                mbar_arrive(w_full + s);
+                mbar_arrive(full + s);
         };
         bool ok = true;
         int g0 = 0, gk0 = 0, n = 0;  // steps and reduction steps before this tile
@@ -439,15 +433,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = (G - g0) & (kGroups - 1); ok && i < steps; i += kGroups) {
                 // the weight stage is taken as late as possible: the codes
                 // are read before the wait
-                const int sw = (g0 + i) % L::kPW;
+                const int sw = (g0 + i) % L::kP;
                 uint8_t* wst = smem + L::kOffW + sw * L::kWStage;
                 // the stage's step before has been consumed; a stage's first step
                 // has nothing to wait for (the phase before a barrier's first
                 // counts as complete)
-                const uint32_t w_par = static_cast<uint32_t>((g0 + i) / L::kPW - 1) & 1u;
+                const uint32_t w_par = static_cast<uint32_t>((g0 + i) / L::kP - 1) & 1u;
                 if (i < nk) {
                     const int gk = gk0 + i, sc = gk % L::kPC;
-                    ok = wait_both(c_full + 2 * G + (kjobs & 1), static_cast<uint32_t>(kjobs >> 1) & 1u, w_empty + sw,
+                    ok = wait_both(c_full + 2 * G + (kjobs & 1), static_cast<uint32_t>(kjobs >> 1) & 1u, empty + sw,
                                    w_par, tmo, a.status);
                     if (!ok) break;
                     ++kjobs;
@@ -506,19 +500,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // rank-r step: B_e rows (forward) or A_e columns (dX) by TMA
                     pi += kGroups;
                     load_constants();
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(w_empty + sw, w_par, tmo, a.status));
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + sw, w_par, tmo, a.status));
                     if (!ok) break;
                     if (leader) {
                         if (crank == 0)
-                            mbar_arrive_expect_tx(w_full + sw, L::kWStage * (L::kPair ? 2u : 1u));
+                            mbar_arrive_expect_tx(full + sw, L::kWStage * (L::kPair ? 2u : 1u));
                         else
                             arrive_w(sw);
                         for (int b = 0; b < (kTransW ? 2 * kU : 1); ++b) {
                             const int x = kTransW ? tl.w0 + w_off + 64 * b : 0, y = kTransW ? 0 : tl.w0 + w_off;
                             if (L::kPair)
-                                tma_load_3d_pair(wst + b * 8192, &tm_lw, mapa_shared(smem_u32(w_full + sw), 0), x, y, tl.e);
+                                tma_load_3d_pair(wst + b * 8192, &tm_lw, mapa_shared(smem_u32(full + sw), 0), x, y, tl.e);
                             else
-                                tma_load_3d(wst + b * 8192, &tm_lw, w_full + sw, x, y, tl.e);
+                                tma_load_3d(wst + b * 8192, &tm_lw, full + sw, x, y, tl.e);
                         }
                     } else if (lane == 0) {
                         arrive_w(sw);
@@ -617,9 +611,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort_flag = 1;
             // a rank-r tile may still be landing in a weight stage
             if (leader)
-                for (int j = max(0, g0 - 2 * L::kPW); j < g0 + L::kPW; ++j)
+                for (int j = max(0, g0 - 2 * L::kP); j < g0 + L::kP; ++j)
                     if ((j & (kGroups - 1)) == G)
-                        mbar_wait(w_full + j % L::kPW, static_cast<uint32_t>(j / L::kPW) & 1u, tmo / 8, nullptr);
+                        mbar_wait(full + j % L::kP, static_cast<uint32_t>(j / L::kP) & 1u, tmo / 8, nullptr);
         }
         __syncwarp();
     }
