@@ -273,41 +273,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kWarpC) {
         // ------------------------------------------------- code producer --
-        if (lane == 0) {
-            int g = 0, g0 = 0;
-            uint32_t par = 0;  // per group, parity of its reduction steps so far
-            bool ok = true;
-            for (; ok && it.next(tl); g0 += steps_of(tl)) {
-                const int nk = tl.k_hi - tl.k_lo;
-                for (int i = 0; i < nk; ++i, ++g) {
-                    const int s = g % L::kPC, G = (g0 + i) & (kGroups - 1);
-                    uint64_t* bar = c_full + 2 * G + ((par >> G) & 1u);
-                    if (g >= L::kPC && !mbar_wait(c_empty + s, static_cast<uint32_t>(g / L::kPC - 1) & 1u, tmo, a.status)) {
-                        *abort_flag = 1;
-                        ok = false;
-                        break;
-                    }
-                    if (*abort_flag) {
-                        ok = false;
-                        break;
-                    }
-                    const int kt = tl.k_lo + i;
-                    par ^= 1u << G;
+        const bool leader = elect_one();
+        int g = 0, g0 = 0;
+        uint32_t par = 0;  // per group, parity of its reduction steps so far
+        bool ok = true;
+        while (ok && uniform(it.next(tl))) {
+            const int k_lo = uniform(tl.k_lo), nk = uniform(tl.k_hi) - k_lo, e = uniform(tl.e);
+            const int w0 = uniform(tl.w0 + crank * L::kRows);
+            for (int i = 0; i < nk; ++i, ++g) {
+                const int s = g % L::kPC, G = (g0 + i) & (kGroups - 1);
+                uint64_t* bar = c_full + 2 * G + ((par >> G) & 1u);
+                if (g >= L::kPC) ok = __all_sync(0xFFFFFFFFu, mbar_wait(c_empty + s, static_cast<uint32_t>(g / L::kPC - 1) & 1u, tmo,
+                                                                        a.status));
+                if (!ok) *abort_flag = 1;
+                if (*abort_flag) ok = false;
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const int kt = k_lo + i;
+                par ^= 1u << G;
+                if (leader) {
                     mbar_arrive_expect_tx(bar, L::kCStage);
                     // rows past the expert's N and columns past K read as zeros
                     if (!kTransW)
-                        tma_load_3d(smem + L::kOffC + s * L::kCStage, &tm_codes, bar, kt * 32, tl.w0 + crank * L::kRows, tl.e);
+                        tma_load_3d(smem + L::kOffC + s * L::kCStage, &tm_codes, bar, kt * 32, w0, e);
                     else
-                        tma_load_3d(smem + L::kOffC + s * L::kCStage, &tm_codes, bar, (tl.w0 + crank * L::kRows) / 2, kt * 64, tl.e);
+                        tma_load_3d(smem + L::kOffC + s * L::kCStage, &tm_codes, bar, w0 / 2, kt * 64, e);
                 }
+                __syncwarp();
             }
-            // after an abort copies may still be landing: every stage's last
-            // copy is over once its barrier has been consumed, or (bounded)
-            // once the time limit has passed
-            if (!ok)
-                for (int j = max(0, g - L::kPC); j < g; ++j)
-                    mbar_wait(c_empty + j % L::kPC, static_cast<uint32_t>(j / L::kPC) & 1u, tmo, nullptr);
+            g0 += uniform(steps_of(tl));
         }
+        // after an abort copies may still be landing: every stage's last copy is
+        // over once its barrier has been consumed, or (bounded) once the time
+        // limit has passed
+        if (!ok)
+            for (int j = max(0, g - L::kPC); j < g; ++j)
+                mbar_wait(c_empty + j % L::kPC, static_cast<uint32_t>(j / L::kPC) & 1u, tmo, nullptr);
         __syncwarp();
     } else if (warp == kWarpMma) {
         // ----------------------------------------------------------- MMA --
