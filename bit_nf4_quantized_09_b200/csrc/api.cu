@@ -1350,31 +1350,43 @@ extern "C" qlora_status qlora_quantize_nf4_noalloc(const float* W, int64_t N, in
 // ================================================== layers of experts, int8 ==
 namespace {
 
-// How a grouped matmul cuts its rows: tiles of up to 256 tokens read (and
-// decode) each weight tile least often, but are taken whole, one round of the
-// SMs after another; tiles of 64 can share out their last round (tiles.cuh).
-// Taken is what should end first, by the tiles that evenly filled experts would
-// have: a step costs what decoding its weight tile costs (C, 0.7 us) or, with
-// more than about 190 tokens, its UMMAs. Measured, of the matmul alone: 8192
-// rows over 8 experts 722 us in tiles of 256, 1543 rows over 13 experts 70 us
-// (100 us in tiles of 64), 777 rows over 7 narrow experts 54 us (28 us in tiles
-// of 64).
+// How a grouped matmul cuts its rows: large tiles read (and decode) each weight
+// tile least often, but are taken whole, one round of the SMs after another;
+// tiles of 64 can share out their last round (tiles.cuh). Taken is what should
+// end first, in units of a 64-deep step of a 64-token tile (0.67 us): by the
+// tiles of evenly filled experts (of 64 rows: of experts half above the
+// mean, since those decode twice). On pairs of CTAs (NF4) a step takes the
+// decoding of half a weight tile, 0.35 us, or what its tokens' UMMAs take.
+// Measured, NF4 forward, 8 experts of 4096 x 4096, tiles of 64, 256 and 512
+// rows: 320 rows 54, 60 and 61 us; 600 rows 81, 61 and 62; 1024 rows 116, 63
+// and 67; 2048 rows 180, 88 and 86; 4096 rows 318, 153 and 130. On single CTAs
+// (8-bit integers) a step of 256 rows is bound by its UMMAs from 190 rows on.
 struct GroupPlan {
     int cap = 64, part_rows = 0;
     size_t tickets_bytes = 0, part_bytes = 0;
 };
-GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps, int big) {
+GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps, bool pairs) {
     GroupPlan p;
-    const bool pair = big == 512;
     const int64_t act = std::max<int64_t>(1, std::min<int64_t>(E, M));  // experts with rows, at most
     const int64_t avg = std::max<int64_t>(1, cdiv(M, act)), tiles_w = cdiv(cols, 256);
-    const int64_t t64 = tiles_w * act * cdiv(avg, 64), per_big = cdiv(avg, big), t_big = tiles_w * act * per_big;
-    const double rows = static_cast<double>(avg) / per_big;
-    const double step_big = pair ? std::max(0.5, rows / 2 / 220.0) : std::max(1.0, rows / 190.0);
+    const int64_t t64 = tiles_w * act * cdiv(pairs ? avg * 3 / 2 : avg, 64);
     const double whole64 = static_cast<double>(cdiv(t64, kPlanSms) * steps);
-    const double cost64 = std::min(whole64, static_cast<double>(t64) * steps / kPlanSms + kFixUp);
-    const double cost_big = static_cast<double>(cdiv(t_big, pair ? kPlanSms / 2 : kPlanSms) * steps) * step_big;
-    p.cap = avg > 64 && cost_big <= cost64 ? big : 64;
+    double best = std::min(whole64, static_cast<double>(t64) * steps / kPlanSms + kFixUp);
+    auto consider = [&](int cap, int units, double least, double rows_per_step) {
+        const int64_t per = cdiv(avg, cap);
+        const double step = std::max(least, static_cast<double>(avg) / per / rows_per_step);
+        const double cost = static_cast<double>(cdiv(tiles_w * act * per, units) * steps) * step;
+        if (cost < best) {
+            best = cost;
+            p.cap = cap;
+        }
+    };
+    if (pairs) {
+        consider(256, kPlanSms / 2, 0.52, 300.0);
+        consider(512, kPlanSms / 2, 0.52, 400.0);
+    } else if (avg > 64) {
+        consider(256, kPlanSms, 1.0, 190.0);
+    }
     // an expert adds at most one partly filled token tile
     p.tickets_bytes = p.cap == 64 ? up256(static_cast<size_t>((M / 64 + act) * tiles_w) * 4) : 0;
     p.part_rows = p.cap == 64 ? static_cast<int>(std::min<int64_t>(M, 64)) : 0;
@@ -1424,7 +1436,7 @@ struct ExpertLayout {
 constexpr int kTermsT = 2, kTermsU = 3;
 ExpertLayout expert_layout(int op, int64_t M, int64_t N, int64_t K, int r, int E) {
     ExpertLayout L;
-    L.plan = op == QLORA_OP_BWD ? group_plan(M, E, K, cdiv(N, 64), 512) : group_plan(M, E, N, K / kBlock, 512);
+    L.plan = op == QLORA_OP_BWD ? group_plan(M, E, K, cdiv(N, 64), true) : group_plan(M, E, N, K / kBlock, true);
     if (op == QLORA_OP_FWD) few_rows_plan(L.plan, M, E, N);
     L.tickets = 256;
     L.header = L.tickets + L.plan.tickets_bytes;
@@ -1513,7 +1525,7 @@ qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_
         QLORA_LAUNCH(launch_expert_gemv(t_act, t_codes, a, tables(), st), 1, "expert forward, few rows");
         return QLORA_OK;
     }
-    const bool pair = p.cap == 512;
+    const bool pair = p.cap >= 256;
     const uint32_t box = pair ? 64 : 16, wrows = pair ? 128 : 256;
     QLORA_MAP(&t_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, red, M, red * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B,
               dx ? "dY" : "X");
@@ -1553,7 +1565,7 @@ struct Int8Layout {
 };
 Int8Layout int8_layout(int64_t M, int64_t N, int64_t K, int E) {
     Int8Layout L;
-    L.plan = group_plan(M, E, N, cdiv(K, 128), 256);
+    L.plan = group_plan(M, E, N, cdiv(K, 128), false);
     L.tickets = 256;
     L.header = L.tickets + L.plan.tickets_bytes;
     L.part = L.header;

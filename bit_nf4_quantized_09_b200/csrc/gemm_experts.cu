@@ -49,12 +49,13 @@ constexpr uint32_t kTmemCols = 512;
 // for 512 tokens. The tokens are one UMMA's N, or two of up to 256 each.
 template <int CAP>
 struct Lay {
-    static constexpr bool kPair = CAP == 512;
+    static constexpr bool kPair = CAP >= 256;
     static constexpr int kRows = kPair ? 128 : 256;        // weight rows of a CTA
-    static constexpr int kP = 4, kPC = 4;                  // operand (token and weight) and code stages
+    static constexpr int kP = CAP == 256 ? 6 : 4;          // operand (token and weight) stages
+    static constexpr int kPC = 4;                          // code stages
     static constexpr int kBoxRows = kPair ? 64 : 16;       // token rows per TMA box
     static constexpr uint32_t kXHalf = 128 * 128;          // a pair's CTA: 128 tokens of each UMMA
-    static constexpr uint32_t kXStage = kPair ? 2 * kXHalf : CAP * 128;
+    static constexpr uint32_t kXStage = kPair ? CAP / 256 * kXHalf : CAP * 128;
     static constexpr uint32_t kWStage = kRows * 64 * 2;
     static constexpr uint32_t kCStage = kRows * 64 / 2;    // packed codes
     static constexpr uint32_t kOffW = kP * kXStage;
@@ -63,7 +64,7 @@ struct Lay {
     static constexpr uint32_t kOffBar = (kOffSched + sizeof(TileSched) + 63) / 64 * 64;
     static constexpr uint32_t kBytes = kOffBar + 512 + 1024;
 };
-static_assert(Lay<512>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "shared memory of one CTA");
+static_assert(Lay<512>::kBytes <= 227 * 1024 && Lay<256>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "shared memory of one CTA");
 // Code stages are a ring over all reduction steps, but each group waits on
 // barriers of its own (two, by the parity of its steps): it has not seen the
 // ring's other steps, and a phase parity is only safe to one who has seen the
@@ -73,8 +74,8 @@ static_assert(Lay<512>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "
 // Operand stages need no such thing: before a group takes stage s for step g it
 // has waited for the UMMAs of step g - 4 - kP, so with kP >= 4 the phase before
 // is over.
-static_assert(Lay<512>::kPC <= 4 && Lay<64>::kPC <= 4, "code stages");
-static_assert(Lay<512>::kP >= kGroups && Lay<64>::kP >= kGroups, "operand stages");
+static_assert(Lay<512>::kPC <= 4 && Lay<256>::kPC <= 4 && Lay<64>::kPC <= 4, "code stages");
+static_assert(Lay<512>::kP >= kGroups && Lay<256>::kP >= kGroups && Lay<64>::kP >= kGroups, "operand stages");
 
 // The tcgen05 forms of a CTA pair. The pair's UMMA takes the first 128 rows of
 // A and the first half of B's rows from the leader's (even) CTA, the others
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // of a pair: this CTA's half of each UMMA's tokens
             const int rows = uniform(tl.rows), row0 = uniform(tl.row0), k_lo = uniform(tl.k_lo);
             const int nk = uniform(tl.k_hi) - k_lo, steps = uniform(steps_of(tl));
-            const int mine[2] = {L::kPair ? pair_n(rows, 0) / 2 : rows, L::kPair ? pair_n(rows, 1) / 2 : 0};
+            const int mine[2] = {L::kPair ? pair_n(rows, 0) / 2 : rows, CAP == 512 ? pair_n(rows, 1) / 2 : 0};
             const int boxes[2] = {(mine[0] + L::kBoxRows - 1) / L::kBoxRows, (mine[1] + L::kBoxRows - 1) / L::kBoxRows};
             // the leader expects the bytes of both CTAs of a pair
             const uint32_t bytes = static_cast<uint32_t>(boxes[0] + boxes[1]) * L::kBoxRows * 128u * (L::kPair ? 2u : 1u);
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!leader) return;
                 if (cr == 0) mbar_arrive_expect_tx(full + s, bytes);
 #pragma unroll
-                for (int h = 0; h < (L::kPair ? 2 : 1); ++h)
+                for (int h = 0; h < (CAP == 512 ? 2 : 1); ++h)
                     for (int b = 0; b < boxes[h]; ++b) {
                         uint8_t* dst = smem + s * L::kXStage + h * L::kXHalf + b * L::kBoxRows * 128;
                         const int row = row0 + 256 * h + cr * mine[h] + b * L::kBoxRows;
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nk = uniform(tl.k_hi - tl.k_lo), steps = uniform(steps_of(tl));
             // two UMMAs at a time: halves of the weight rows, or of a pair's tokens
             const int rows = uniform(tl.rows);
-            const bool two = !L::kPair || rows > 256;
+            const bool two = CAP == 64 || (CAP == 512 && rows > 256);
             const uint32_t idesc[2] = {idesc_bf16(L::kPair ? 256 : 128, L::kPair ? pair_n(rows, 0) : (rows + 15) & ~15, kTransW, false),
                                        idesc_bf16(L::kPair ? 256 : 128, L::kPair ? pair_n(rows, 1) : (rows + 15) & ~15, kTransW, false)};
             // the second UMMA's operands, behind the first's
@@ -529,12 +530,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // at the barriers; they leave together)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc, static_cast<uint32_t>(n) & 1u, tmo, a.status)) && ok;
             tc_fence_after();
-            const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * 256;
+            const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + (CAP == 256 ? 0 : h * 256);
             // output column of this lane in the tile, and the first of this warp's
-            // tokens: h is a half of a CTA's weight rows, or of a pair's tokens
+            // tokens: h is a half of a CTA's weight rows, the second UMMA of a
+            // pair's 512 tokens, or every other 32 of a pair's 256
             const int nl = L::kPair ? w_off + q * 32 + lane : h * 128 + q * 32 + lane;
-            const int tok0 = L::kPair ? 256 * h : 0;
-            const int toks = L::kPair ? min(tl.rows - tok0, 256) : tl.rows;
+            const int tok0 = CAP == 512 ? 256 * h : 0;
+            const int toks = CAP == 512 ? min(tl.rows - tok0, 256) : tl.rows;
             if (CAP != 64 || nk == KT) {
                 // lane = output column, register = token: two neighbouring
                 // lanes swap halves of a token pair, so each lane stores two
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // covers two 64-byte row segments
                 const int col = tl.w0 + (nl & ~1);
                 const bool write = ok && col < a.out_cols;
-                for (int c = part * 32; c < toks; c += 64) {
+                for (int c = CAP == 256 ? (2 * part + h) * 32 : part * 32; c < toks; c += CAP == 256 ? 128 : 64) {
                     uint32_t r[32];
                     tmem_ld32(trow + c, r);
                     tmem_ld_wait();
@@ -654,39 +656,48 @@ cudaError_t launch_one(const CUtensorMap& act, const CUtensorMap& codes, const C
     return cudaLaunchKernelEx(&cfg, expert_gemm<kTransW, kNoDq, CAP>, act, codes, lact, lw, a, tab);
 }
 
+template <bool kTransW, int CAP>
+cudaError_t launch_cap(const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact, const CUtensorMap& lw,
+                       const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl, cudaStream_t st) {
+    return a.c.absmax ? launch_one<kTransW, true, CAP>(act, codes, lact, lw, a, tab, pdl, st)
+                      : launch_one<kTransW, false, CAP>(act, codes, lact, lw, a, tab, pdl, st);
+}
+
 template <bool kTransW>
 cudaError_t launch_dir(const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact, const CUtensorMap& lw,
                        const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl, cudaStream_t st) {
-    if (a.c.absmax)
-        return a.cap == 512 ? launch_one<kTransW, true, 512>(act, codes, lact, lw, a, tab, pdl, st)
-                            : launch_one<kTransW, true, 64>(act, codes, lact, lw, a, tab, pdl, st);
-    return a.cap == 512 ? launch_one<kTransW, false, 512>(act, codes, lact, lw, a, tab, pdl, st)
-                        : launch_one<kTransW, false, 64>(act, codes, lact, lw, a, tab, pdl, st);
+    if (a.cap == 64) return launch_cap<kTransW, 64>(act, codes, lact, lw, a, tab, pdl, st);
+    if (a.cap == 256) return launch_cap<kTransW, 256>(act, codes, lact, lw, a, tab, pdl, st);
+    return launch_cap<kTransW, 512>(act, codes, lact, lw, a, tab, pdl, st);
 }
 
-template <bool kTransW, bool kNoDq>
+template <bool kTransW, bool kNoDq, int CAP>
 cudaError_t opt_in() {
-    cudaError_t e = cudaFuncSetAttribute(expert_gemm<kTransW, kNoDq, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Lay<512>::kBytes));
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(expert_gemm<kTransW, kNoDq, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(Lay<64>::kBytes));
+    return cudaFuncSetAttribute(expert_gemm<kTransW, kNoDq, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Lay<CAP>::kBytes));
+}
+
+template <int CAP>
+cudaError_t opt_in_cap() {
+    cudaError_t e;
+    if ((e = opt_in<false, false, CAP>()) != cudaSuccess || (e = opt_in<false, true, CAP>()) != cudaSuccess ||
+        (e = opt_in<true, false, CAP>()) != cudaSuccess)
+        return e;
+    return opt_in<true, true, CAP>();
 }
 
 }  // namespace
 
 cudaError_t expert_gemm_init_device() {
     cudaError_t e;
-    if ((e = opt_in<false, false>()) != cudaSuccess || (e = opt_in<false, true>()) != cudaSuccess ||
-        (e = opt_in<true, false>()) != cudaSuccess)
-        return e;
-    return opt_in<true, true>();
+    if ((e = opt_in_cap<64>()) != cudaSuccess || (e = opt_in_cap<256>()) != cudaSuccess) return e;
+    return opt_in_cap<512>();
 }
 
 cudaError_t launch_expert_gemm(bool trans_w, const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact,
                                const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl,
                                cudaStream_t st) {
-    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 2 || (a.cap != 64 && a.cap != 512) || a.rank_cols < 1 || a.rank_cols > 64)
+    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 2 || (a.cap != 64 && a.cap != 256 && a.cap != 512) || a.rank_cols < 1 || a.rank_cols > 64)
         return cudaErrorInvalidValue;
     return trans_w ? launch_dir<true>(act, codes, lact, lw, a, tab, pdl, st)
                    : launch_dir<false>(act, codes, lact, lw, a, tab, pdl, st);
