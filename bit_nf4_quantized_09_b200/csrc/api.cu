@@ -1353,14 +1353,17 @@ namespace {
 // How a grouped matmul cuts its rows: large tiles read (and decode) each weight
 // tile least often, but are taken whole, one round of the SMs after another;
 // tiles of 64 can share out their last round (tiles.cuh). Taken is what should
-// end first, in units of a 64-deep step of a 64-token tile (0.67 us): by the
-// tiles of evenly filled experts (of 64 rows: of experts half above the
-// mean, since those decode twice). On pairs of CTAs (NF4) a step takes the
-// decoding of half a weight tile, 0.35 us, or what its tokens' UMMAs take.
-// Measured, NF4 forward, 8 experts of 4096 x 4096, tiles of 64, 256 and 512
-// rows: 320 rows 54, 60 and 61 us; 600 rows 81, 61 and 62; 1024 rows 116, 63
-// and 67; 2048 rows 180, 88 and 86; 4096 rows 318, 153 and 130. On single CTAs
-// (8-bit integers) a step of 256 rows is bound by its UMMAs from 190 rows on.
+// end first, in units of a reduction step of a 64-token tile (NF4 0.67 us, 8-bit
+// 0.44 us), by the tiles of experts somewhat above the mean.
+// NF4: tiles of 256 and 512 run on pairs of CTAs (`pairs`), where a step takes
+// the decoding of half a weight tile, 0.35 us, or its tokens' UMMAs. Measured,
+// forward, 8 experts of 4096 x 4096, tiles of 64, 256 and 512 rows: 320 rows 54,
+// 60 and 61 us; 600 rows 81, 61 and 62; 1024 rows 116, 63 and 67; 2048 rows 180,
+// 88 and 86; 4096 rows 318, 153 and 130.
+// 8-bit: tiles of 512 run on pairs, of 256 on single CTAs. Measured, 64, 256 and
+// 512 rows: 600 rows of 8 experts of 4096 x 4096 48, 39 and 43 us; 3000 rows 84,
+// 65 and 68; 8192 rows of 16 experts (143 and 135); one weight of 11008 x 4096,
+// 200 rows 41, 34 and 29, 4096 rows (139 and 135).
 struct GroupPlan {
     int cap = 64, part_rows = 0;
     size_t tickets_bytes = 0, part_bytes = 0;
@@ -1373,7 +1376,7 @@ GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps, bool pairs) 
     const double whole64 = static_cast<double>(cdiv(t64, kPlanSms) * steps);
     double best = std::min(whole64, static_cast<double>(t64) * steps / kPlanSms + kFixUp);
     auto consider = [&](int cap, int units, double least, double rows_per_step) {
-        const int64_t per = cdiv(avg, cap);
+        const int64_t per = cdiv(E > 1 && !pairs ? avg * 5 / 4 : avg, cap);
         const double step = std::max(least, static_cast<double>(avg) / per / rows_per_step);
         const double cost = static_cast<double>(cdiv(tiles_w * act * per, units) * steps) * step;
         if (cost < best) {
@@ -1385,7 +1388,8 @@ GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps, bool pairs) 
         consider(256, kPlanSms / 2, 0.52, 300.0);
         consider(512, kPlanSms / 2, 0.52, 400.0);
     } else if (avg > 64) {
-        consider(256, kPlanSms, 1.0, 190.0);
+        consider(256, kPlanSms, 1.5, 142.0);
+        consider(512, kPlanSms / 2, 1.2, 300.0);
     }
     // an expert adds at most one partly filled token tile
     p.tickets_bytes = p.cap == 64 ? up256(static_cast<size_t>((M / 64 + act) * tiles_w) * 4) : 0;
@@ -1596,9 +1600,10 @@ qlora_status int8_impl(const uint16_t* X, int64_t M, const qlora_int8_weight* w,
                  1, "quantise tokens");
     const GroupPlan& p = L.plan;
     CUtensorMap tx, tw;
-    QLORA_MAP(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, p.cap == 256 ? 64 : 16, CU_TENSOR_MAP_SWIZZLE_128B,
+    QLORA_MAP(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, K, 128, p.cap == 64 ? 16 : 64, CU_TENSOR_MAP_SWIZZLE_128B,
               "token codes");
-    QLORA_MAP(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K, N, K, 128, 256, CU_TENSOR_MAP_SWIZZLE_128B, "codes", E);
+    QLORA_MAP(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K, N, K, 128, p.cap == 512 ? 128 : 256,
+              CU_TENSOR_MAP_SWIZZLE_128B, "codes", E);
     Int8GemmArgs a{};
     a.offsets = offsets;
     a.E = E;

@@ -34,21 +34,24 @@ namespace {
 constexpr int kEpiWarps = 16;
 constexpr int kWarpX = 16, kWarpW = 17, kWarpMma = 18;
 constexpr int kThreads = (kWarpMma + 1) * 32;
-constexpr uint32_t kWStage = 256 * 128;  // 32 KB: 256 channels x 128 codes
 constexpr uint32_t kTmemCols = 512;
 
 template <int CAP>
 struct Lay {
-    static constexpr int kStages = CAP == 256 ? 3 : 5;
-    static constexpr int kBoxRows = CAP == 256 ? 64 : 16;
-    static constexpr uint32_t kXStage = CAP * 128;
+    static constexpr bool kPair = CAP == 512;
+    static constexpr int kStages = CAP == 512 ? 4 : CAP == 256 ? 3 : 5;
+    static constexpr int kBoxRows = CAP == 64 ? 16 : 64;
+    static constexpr uint32_t kXHalf = 128 * 128;        // a pair's CTA: 128 tokens of each UMMA
+    static constexpr uint32_t kXStage = kPair ? 2 * kXHalf : CAP * 128;
+    static constexpr int kRows = kPair ? 128 : 256;      // channels of a CTA
+    static constexpr uint32_t kWStage = kRows * 128;
     static constexpr uint32_t kOffW = kStages * kXStage;
     static constexpr uint32_t kOffXs = kOffW + kStages * kWStage;
-    static constexpr uint32_t kOffSched = kOffXs + 1024;
+    static constexpr uint32_t kOffSched = kOffXs + 2048;
     static constexpr uint32_t kOffBar = (kOffSched + sizeof(TileSched) + 63) / 64 * 64;
     static constexpr uint32_t kBytes = kOffBar + 256 + 1024;
 };
-static_assert(Lay<256>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "shared memory of one CTA");
+static_assert(Lay<512>::kBytes <= 227 * 1024 && Lay<256>::kBytes <= 227 * 1024 && Lay<64>::kBytes <= 227 * 1024, "shared memory of one CTA");
 
 __device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                         uint32_t accumulate) {
@@ -56,6 +59,16 @@ __device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t a_desc, uint64
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
@@ -87,6 +100,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int KT = static_cast<int>((a.K + 127) / 128);
     const int tiles_w = static_cast<int>((a.N + 255) / 256);
+    const int crank = L::kPair ? static_cast<int>(cluster_ctarank()) : 0, w_off = crank * L::kRows;
+    const int unit = static_cast<int>(blockIdx.x) / (L::kPair ? 2 : 1), units = static_cast<int>(gridDim.x) / (L::kPair ? 2 : 1);
     const uint64_t tmo = a.timeout_ns;
 
     if (threadIdx.x == 0) {
@@ -95,15 +110,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(empty + s, 1);
         }
         mbar_init(acc, 1);
-        mbar_init(tmem_free, kEpiWarps);
+        mbar_init(tmem_free, kEpiWarps * (L::kPair ? 2 : 1));
         mbar_init(drain, 1);
         *abort_flag = 0;
         pending->n = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
-        tmem_alloc(tmem_slot, kTmemCols);
-        tmem_relinquish();
+        if (L::kPair) {
+            tmem_alloc_pair(tmem_slot, kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, kTmemCols);
+            tmem_relinquish();
+        }
     }
     if (warp == kWarpX && lane == 0) {
         tma_prefetch_desc(&tm_x);
@@ -113,48 +133,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (L::kPair) cluster_sync();  // the partner's barriers are initialised before any remote arrival
     const uint32_t tmem = *tmem_slot;
-    const Ranges ranges(sched.base[a.E] * tiles_w, KT, static_cast<int>(gridDim.x), CAP == 64);
-    SegIter<> it(sched, ranges, static_cast<int>(blockIdx.x), tiles_w);
+    const Ranges ranges(sched.base[a.E] * tiles_w, KT, units, CAP == 64);
+    SegIter<> it(sched, ranges, unit, tiles_w);
     Tile tl;
 
     if (warp == kWarpX || warp == kWarpW) {
-        if (lane == 0) {
-            const bool is_x = warp == kWarpX;
-            if (is_x) asm volatile("griddepcontrol.wait;" ::: "memory");  // the quantised tokens
-            int g = 0;
-            bool ok = true;
-            while (ok && it.next(tl)) {
-                const int boxes = (tl.rows + L::kBoxRows - 1) / L::kBoxRows;
-                for (int k = tl.k_lo; k < tl.k_hi; ++k, ++g) {
-                    const int s = g % L::kStages;
-                    if (g >= L::kStages &&
-                        !mbar_wait(empty + s, static_cast<uint32_t>(g / L::kStages - 1) & 1u, tmo, a.status)) {
-                        *abort_flag = 1;
-                        ok = false;
-                        break;
-                    }
-                    if (*abort_flag) {
-                        ok = false;
-                        break;
-                    }
+        const bool is_x = warp == kWarpX, leader = elect_one();
+        const int cr = uniform(crank);
+        if (is_x) asm volatile("griddepcontrol.wait;" ::: "memory");  // the quantised tokens
+        int g = 0;
+        bool ok = true;
+        while (ok && uniform(it.next(tl))) {
+            const int rows = uniform(tl.rows), row0 = uniform(tl.row0), w0 = uniform(tl.w0 + w_off), e = uniform(tl.e);
+            const int k_lo = uniform(tl.k_lo), k_hi = uniform(tl.k_hi);
+            // tokens of each UMMA; of a pair: this CTA's half of them
+            const int mine[2] = {L::kPair ? pair_n(rows, 0) / 2 : rows, L::kPair ? pair_n(rows, 1) / 2 : 0};
+            const int boxes[2] = {(mine[0] + L::kBoxRows - 1) / L::kBoxRows, (mine[1] + L::kBoxRows - 1) / L::kBoxRows};
+            // a pair's leader expects the bytes of both CTAs
+            const uint32_t bytes = (is_x ? static_cast<uint32_t>(boxes[0] + boxes[1]) * L::kBoxRows * 128u : L::kWStage) *
+                                   (L::kPair ? 2u : 1u);
+            for (int k = k_lo; k < k_hi; ++k, ++g) {
+                const int s = g % L::kStages;
+                if (g >= L::kStages)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + s, static_cast<uint32_t>(g / L::kStages - 1) & 1u, tmo, a.status));
+                if (!ok) *abort_flag = 1;
+                if (*abort_flag) ok = false;
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (leader) {
+                    if (cr == 0) mbar_arrive_expect_tx(full + s, bytes);
+                    const uint32_t bar = L::kPair ? mapa_shared(smem_u32(full + s), 0) : 0u;
                     if (is_x) {
-                        mbar_arrive_expect_tx(full + s, static_cast<uint32_t>(boxes) * L::kBoxRows * 128u);
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(smem + s * L::kXStage + b * L::kBoxRows * 128, &tm_x, full + s, k * 128,
-                                        tl.row0 + b * L::kBoxRows);
+#pragma unroll
+                        for (int h = 0; h < (L::kPair ? 2 : 1); ++h)
+                            for (int b = 0; b < boxes[h]; ++b) {
+                                uint8_t* dst = smem + s * L::kXStage + h * L::kXHalf + b * L::kBoxRows * 128;
+                                const int row = row0 + 256 * h + cr * mine[h] + b * L::kBoxRows;
+                                if (L::kPair)
+                                    tma_load_2d_pair(dst, &tm_x, bar, k * 128, row);
+                                else
+                                    tma_load_2d(dst, &tm_x, full + s, k * 128, row);
+                            }
+                    } else if (L::kPair) {
+                        tma_load_3d_pair(smem + L::kOffW + s * L::kWStage, &tm_w, bar, k * 128, w0, e);
                     } else {
-                        mbar_arrive_expect_tx(full + s, kWStage);
-                        tma_load_3d(smem + L::kOffW + s * kWStage, &tm_w, full + s, k * 128, tl.w0, tl.e);
+                        tma_load_3d(smem + L::kOffW + s * L::kWStage, &tm_w, full + s, k * 128, w0, e);
                     }
                 }
+                __syncwarp();
             }
+        }
+        // no copy still landing when the CTA ends; a partner's complete on the
+        // leader's barriers: they have been consumed or, after an abort, land
+        // while it waits for what no one signals
+        if (cr == 0) {
             for (int j = max(0, g - L::kStages); j < g; ++j)
                 mbar_wait(full + j % L::kStages, static_cast<uint32_t>(j / L::kStages) & 1u, tmo, nullptr);
+        } else if (!ok) {
+            mbar_wait(full, 0u, 1000000u, nullptr);  // 1 ms
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
         const bool leader = elect_one();
+        if (L::kPair && crank == 1) it.stop();  // the leader issues for both CTAs
         const uint64_t xd0 = sw128_desc(smem_u32(smem), 16, 1024), wd0 = sw128_desc(smem_u32(smem + L::kOffW), 16, 1024);
         int g = 0, n = 0;
         bool ok = true;
@@ -163,7 +206,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             tc_fence_after();
             const int steps = uniform(tl.k_hi - tl.k_lo);
-            const uint32_t idesc = idesc_i8(128, uniform((tl.rows + 15) & ~15));
+            // two UMMAs at a time: halves of the channels, or of a pair's tokens
+            const int rows = uniform(tl.rows);
+            const bool two = !L::kPair || rows > 256;
+            const uint32_t idesc[2] = {idesc_i8(L::kPair ? 256 : 128, L::kPair ? pair_n(rows, 0) : (rows + 15) & ~15),
+                                       idesc_i8(L::kPair ? 256 : 128, L::kPair ? pair_n(rows, 1) : (rows + 15) & ~15)};
+            constexpr uint32_t kW2 = L::kPair ? 0 : 16384 / 16, kX2 = L::kPair ? L::kXHalf / 16 : 0;
             for (int i = 0; i < steps; ++i, ++g) {
                 const int s = g % L::kStages;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + s, static_cast<uint32_t>(g / L::kStages) & 1u, tmo, a.status));
@@ -171,29 +219,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 if (leader) {
                     const uint64_t xd = xd0 + static_cast<uint32_t>(s) * (L::kXStage / 16);
-                    const uint64_t wd = wd0 + static_cast<uint32_t>(s) * (kWStage / 16);
+                    const uint64_t wd = wd0 + static_cast<uint32_t>(s) * (L::kWStage / 16);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            umma_i8(tmem + h * 256, wd + h * (16384 / 16) + kk * 2, xd + kk * 2, idesc,
-                                    (i > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit(empty + s);
-                    if (i == steps - 1) umma_commit(acc);
+                            if (L::kPair) {
+                                if (h == 0 || two)
+                                    umma_i8_pair(tmem + h * 256, wd + kk * 2, xd + h * kX2 + kk * 2, idesc[h],
+                                                 (i > 0 || kk > 0) ? 1u : 0u);
+                            } else {
+                                umma_i8(tmem + h * 256, wd + h * kW2 + kk * 2, xd + kk * 2, idesc[0],
+                                        (i > 0 || kk > 0) ? 1u : 0u);
+                            }
+                    commit<L::kPair>(empty + s);
+                    if (i == steps - 1) commit<L::kPair>(acc);
                 }
                 __syncwarp();
             }
             ++n;
         }
         if (!ok) *abort_flag = 1;
-        if (leader) umma_commit(drain);
+        if (leader && crank == 0) commit<L::kPair>(drain);
         mbar_wait(drain, 0u, tmo, nullptr);
         __syncwarp();
     } else {
         // ------------------------------------------------------ epilogue --
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the token scales
         const int q = warp & 3, h = (warp >> 2) & 1, part = warp >> 3;
-        const int nl = h * 128 + q * 32 + lane;
+        // channel in the tile; h: a half of a CTA's channels, or of a pair's tokens
+        const int nl = L::kPair ? w_off + q * 32 + lane : h * 128 + q * 32 + lane;
         bool ok = true;
         int n = 0;
         while (ok && it.next(tl)) {
@@ -208,19 +263,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // tokens in chunks of 32, every second one this warp's. Two
                 // neighbouring lanes swap halves of a token pair: word i of a
                 // chunk holds channels nl & ~1, + 1 of token 2 i + (lane & 1).
-                constexpr int kChunks = CAP / 64;
+                constexpr int kChunks = CAP == 64 ? 1 : 4;
+                const int tok0 = L::kPair ? 256 * h : 0, toks = min(tl.rows - tok0, 256);
                 uint32_t y[kChunks][16];
 #pragma unroll
                 for (int k = 0; k < kChunks; ++k) {
                     const int c = part * 32 + 64 * k;
-                    if (c < tl.rows) {
+                    if (c < toks) {
                         uint32_t r[32];
                         tmem_ld32(trow + c, r);
                         tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            const float y0 = __int2float_rn(static_cast<int>(r[i])) * (xs_s[c + i] * ws);
-                            const float y1 = __int2float_rn(static_cast<int>(r[i + 1])) * (xs_s[c + i + 1] * ws);
+                            const float y0 = __int2float_rn(static_cast<int>(r[i])) * (xs_s[tok0 + c + i] * ws);
+                            const float y1 = __int2float_rn(static_cast<int>(r[i + 1])) * (xs_s[tok0 + c + i + 1] * ws);
                             const float got = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? y0 : y1, 1);
                             y[k][i / 2] = (lane & 1) ? pack_bf16x2(got, y1) : pack_bf16x2(y0, got);
                         }
@@ -228,16 +284,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(tmem_free);
+                if (lane == 0) {
+                    if (L::kPair)
+                        arrive_leader(tmem_free);
+                    else
+                        mbar_arrive(tmem_free);
+                }
                 const int col = tl.w0 + (nl & ~1);
                 if (ok && col < a.N) {
-                    uint16_t* out = a.Y + static_cast<int64_t>(tl.row0) * a.N + col;
+                    uint16_t* out = a.Y + static_cast<int64_t>(tl.row0 + tok0) * a.N + col;
 #pragma unroll
                     for (int k = 0; k < kChunks; ++k)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const int tok = part * 32 + 64 * k + 2 * i + (lane & 1);
-                            if (tok < tl.rows) *reinterpret_cast<uint32_t*>(out + tok * a.N) = y[k][i];
+                            if (tok < toks) *reinterpret_cast<uint32_t*>(out + tok * a.N) = y[k][i];
                         }
                 }
             } else if (CAP == 64) {
@@ -292,9 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
+    if (L::kPair) cluster_sync();  // the leader's UMMAs read and write both CTAs
     if (warp == kWarpMma) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        if (L::kPair)
+            tmem_dealloc_pair(tmem, kTmemCols);
+        else
+            tmem_dealloc(tmem, kTmemCols);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -485,11 +550,16 @@ cudaError_t launch_one(const CUtensorMap& x, const CUtensorMap& w, const Int8Gem
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Lay<CAP>::kBytes;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = Lay<CAP>::kPair ? 2 : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = pdl ? 2 : 1;
+    if (Lay<CAP>::kPair) cfg.gridDim.x &= ~1u;
     return cudaLaunchKernelEx(&cfg, int8_gemm<CAP>, x, w, a);
 }
 
@@ -498,6 +568,9 @@ cudaError_t launch_one(const CUtensorMap& x, const CUtensorMap& w, const Int8Gem
 cudaError_t int8_init_device() {
     cudaError_t e = cudaFuncSetAttribute(int8_gemm<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(Lay<256>::kBytes));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(int8_gemm<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(Lay<512>::kBytes));
     if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(int8_gemm<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(Lay<64>::kBytes));
@@ -505,7 +578,9 @@ cudaError_t int8_init_device() {
 
 cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, bool pdl,
                              cudaStream_t st) {
-    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 1 || (a.cap != 64 && a.cap != 256)) return cudaErrorInvalidValue;
+    if (a.E < 1 || a.E > kMaxExperts || a.ctas < 2 || (a.cap != 64 && a.cap != 256 && a.cap != 512))
+        return cudaErrorInvalidValue;
+    if (a.cap == 512) return launch_one<512>(x, w, a, pdl, st);
     return a.cap == 256 ? launch_one<256>(x, w, a, pdl, st) : launch_one<64>(x, w, a, pdl, st);
 }
 

@@ -67,6 +67,64 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// The tcgen05 forms of a CTA pair. The pair's UMMA takes the first 128 rows of
+// A and the first half of B's rows from the leader's (even) CTA, the others
+// from its partner's, at the same shared-memory addresses; each CTA's TMEM gets
+// its own 128 rows of D.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {  // a warp of each CTA
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(0x3))
+        : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if (kPair)
+        umma_commit_pair(bar);
+    else
+        umma_commit(bar);
+}
+
+// TMA copies into this CTA's shared memory that complete on a barrier of the
+// pair's leader (a mapa address).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// Arrives on a barrier of the pair's leader. What it releases stays in this
+// CTA's shared memory and TMEM, where this SM's tensor core meets it, so CTA
+// scope is enough; a release at cluster scope waits for the constants' loads in
+// flight as well, 1500 to 1900 cycles a step.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0)) : "memory");
+}
+
+// N of UMMA h of a pair's tile: its tokens 256 h on, in multiples of 32.
+__device__ __forceinline__ int pair_n(int rows, int h) { return min((max(rows - 256 * h, 0) + 31) & ~31, 256); }
+
 // lut_decode8_sx with every permute as the bare instruction: __byte_perm masks
 // its selector to three bits a nibble, which here are known to be clear but not
 // to the compiler. Integer instructions bound the decoding (22 per 8 weights).
