@@ -168,6 +168,26 @@ def test_few_rows_against_fp64(q, name):
         assert torch.equal(a[k], b[k]), k
 
 
+# tiles of 256 and 512 tokens on pairs of CTAs: token counts around the tiles'
+# sizes and the 32-row granularity, weight tiles of which one CTA has no row
+PAIRS = {
+    "edges_512": dict(counts=[512, 513, 31, 1, 257, 289], N=2440, K=448, r=16),
+    "edges_256": dict(counts=[33, 200, 64, 128, 97], N=264, K=1088, r=8, dq=False, lead=1),
+    "one_half": dict(counts=[130, 70], N=2056, K=2112, r=64, pad=3),
+    "many_rounds": dict(counts=[100] * 40, N=904, K=64, r=32),
+}
+
+
+@pytest.mark.parametrize("name", PAIRS)
+def test_pairs_against_fp64(q, name):
+    t = case(**PAIRS[name])
+    a = run(q, t)
+    compare(t, a)
+    b = run(q, t)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+
+
 @pytest.mark.parametrize("counts", [[3, 5, 1], [9, 14, 6]], ids=["8", "16"])
 def test_few_rows_do_not_leak(q, counts):
     """As for many rows: NaN and infinities stay in their own rows."""
