@@ -14,7 +14,8 @@
 // the ids again (L2) and writes each row to its place.
 //
 // Bound by latency: 8 bytes per row move. 32768 ids over 64 experts: 53 us with
-// one CTA and match instructions, 8 us with the cluster and votes.
+// one CTA and match instructions, 12 us with the cluster and votes; 16 ids over
+// 8 experts 4.8 us, about what a launch takes.
 #include <algorithm>
 
 #include "kernels.h"

@@ -8,26 +8,45 @@
 // token ("ta-paperlens QLoRA explainer", 勾配は実際どこへ行くのか: every matmul
 // restores the 4-bit blocks it needs to BF16 on the spot).
 //
-// Operands. The weight is the UMMA's M side (two M = 128 halves: 256 output
-// columns) and the tokens its N side (16 to 256, a multiple of 16), so a tile
-// costs what its expert's rows cost and not a padded 256: an expert with 40
-// rows runs N = 48. The 64-column rank-r term (sT . B_e^T, sU . A_e) is one
-// more reduction step of the same accumulators, its operands loaded by TMA.
+// Operands. The weight is the UMMA's M side (256 output columns a tile) and the
+// tokens its N side (a multiple of 16, of 32 on pairs), so a tile costs what its
+// expert's rows cost: an expert with 40 rows runs N = 48. The 64-column rank-r
+// term (sT . B_e^T, sU . A_e) is one more reduction step of the same
+// accumulators, its operands loaded by TMA.
 //
-// Roles of a persistent CTA (one per SM, 20 warps):
+// Tiles of up to 64 tokens run on single CTAs, two UMMAs of M = 128 at a time.
+// Tiles of up to 256 or 512 tokens run on pairs of CTAs (a cluster of two on
+// neighbouring SMs, cta_group::2): each CTA decodes 128 of the 256 weight rows
+// and holds half of the tokens, and one UMMA of M = 256 reads both CTAs' shared
+// memory, so a weight is decoded once for all tokens of the tile. The leader
+// issues for both; copies and decoders of both CTAs arrive on its barriers.
+//
+// Roles of a persistent CTA (one per SM, 19 warps):
 //   warps 0-15  dequantisers in four groups of four that take the reduction
-//               steps in turn (two 64-weight blocks per thread, the exact
-//               w_hat = bf16(level c') through the per-block byte tables); then
-//               the epilogue
+//               steps in turn (64-weight blocks, the exact w_hat =
+//               bf16(level c') through the per-block byte tables); then the
+//               epilogue
 //   warp 16     TMA producer of the token tiles
 //   warp 17     TMA producer of the packed codes
 //   warp 18     TMEM owner, UMMA issuer
+// The producers and the issuer run on warp-uniform values and issue under
+// elect_one(): from one lane of a divergent branch a step of copies cost 570
+// cycles (8192 rows 663 us, 635 us without).
 // Block constants are read from the stored form by the threads that use them;
 // no transposed copy of an expert stack's constants is written, most of which
 // few tokens would not use.
 //
-// The work is dealt out in equal ranges of reduction steps (tiles.cuh); parts
-// of a tile meet in global memory, in a fixed order: results are bitwise
+// Bounds, with the down-projection. 8192 rows over 8 experts of 11008 x 4096
+// (r = 64): 632 us, 1194 TFLOP/s, the tensor pipe 81 % busy at the 1.55 GHz that
+// full load leaves; on single CTAs, which decode each weight twice as often, 715
+// us (ALU pipe 66 % busy, tensor pipe 68 %). dX of 4096 x 11008: 550 us of 718
+// for the backward. 1543 rows over 13 experts of 2056 x 4096: 65 us, bound by
+// decoding (a step of 128 x 64 weights per CTA every 0.35 us, the ALU pipe 61 %
+// busy). 160 rows over 8 experts of 4096 x 4096 (tiles of 64): 54 us, a step of
+// 256 x 64 weights every 0.67 us.
+//
+// The work is dealt out in whole tiles and ranges of reduction steps (tiles.cuh);
+// parts of a tile meet in global memory, in a fixed order: results are bitwise
 // reproducible.
 #include "kernels.h"
 #include "tiles.cuh"
@@ -42,11 +61,7 @@ constexpr int kWarpX = 16, kWarpC = 17, kWarpMma = 18;
 constexpr int kThreads = (kWarpMma + 1) * 32;
 constexpr uint32_t kTmemCols = 512;
 
-// Tiles of up to 64 tokens run on single CTAs. Tiles of up to 512 tokens run on
-// pairs of CTAs (a cluster of two on neighbouring SMs, cta_group::2): each CTA
-// decodes 128 of the tile's 256 weight rows and holds half of its tokens, and
-// one UMMA of M = 256 reads both CTAs' shared memory, so a weight is decoded
-// for 512 tokens. The tokens are one UMMA's N, or two of up to 256 each.
+// Shared memory by token capacity.
 template <int CAP>
 struct Lay {
     static constexpr bool kPair = CAP >= 256;

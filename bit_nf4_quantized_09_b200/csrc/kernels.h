@@ -289,7 +289,7 @@ cudaError_t merge_tc_init_device();
 
 // -------------------------------------------------- rows grouped by expert --
 // Tiles of the grouped matmuls: 256 weight rows x up to `cap` token rows of
-// one expert (64 or 256). `offsets`: device int32 [E + 1], or nullptr for one
+// one expert (64, 256 or 512). `offsets`: device int32 [E + 1], or nullptr for one
 // expert that owns every row. With cap 64 the tiles of the last round may be
 // shared among the `ctas` CTAs; a shared tile goes through `part`, 2 ctas slots
 // of part_rows x 256 words (part_rows at least the rows of a tile), and
@@ -315,10 +315,11 @@ struct ExpertGemmArgs {
     uint64_t timeout_ns;
 };
 
-// act: X or dY {red, M}, lact: sT or sU {r, M}, both box {64, 16 or 64 (cap
-// 256)} SW128; codes {K/2, N, E}: forward box {32, 256, 1} SW32, dX box
-// {128, 64, 1} SW128; lw: forward B {r, N, E} box {64, 256, 1}, dX A
-// {K, r, E} box {64, 64, 1}, SW128.
+// act: X or dY {red, M}, lact: sT or sU {r, M}, both box {64, 16} SW128; codes
+// {K/2, N, E}: forward box {32, 256, 1} SW32, dX box {128, 64, 1} SW128; lw:
+// forward B {r, N, E} box {64, 256, 1}, dX A {K, r, E} box {64, 64, 1}, SW128.
+// Caps 256 and 512 (pairs of CTAs): act and lact box {64, 64}; codes: forward
+// box {32, 128, 1}, dX {64, 64, 1} SW64; lw: forward box {64, 128, 1}.
 cudaError_t launch_expert_gemm(bool trans_w, const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact,
                                const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl,
                                cudaStream_t st);
@@ -396,8 +397,8 @@ struct Int8GemmArgs {
     int* status;
     uint64_t timeout_ns;
 };
-// x: token codes {K, M} box {128, 16 or 64 (cap 256)}, w: {K, N, E} box
-// {128, 256, 1}, both SW128.
+// x: token codes {K, M} box {128, 16}, or {128, 64} from cap 256 on; w: {K, N, E}
+// box {128, 256, 1}, of cap 512 (pairs of CTAs) {128, 128, 1}; both SW128.
 cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, bool pdl,
                              cudaStream_t st);
 cudaError_t int8_init_device();

@@ -17,9 +17,9 @@
 // tile's steps leaves its partial sums in a slot of global memory and takes a
 // ticket; the last one to come adds the parts in CTA order (whoever it is, the
 // order is the same) and writes the tile. Nobody waits for another CTA. Tiles
-// of 256 tokens are always taken whole: a part of 256 KB costs more to write
-// and read than a round left partly idle (722 us whole, 756 us shared on 8192
-// rows).
+// of 256 and 512 tokens are always taken whole: a part of 256 KB costs more to
+// write and read than a round left partly idle (on single CTAs 722 us whole, 756
+// us shared on 8192 rows). Where tiles run on pairs of CTAs, `CTA` is a pair.
 //
 // Offsets are read on the device only, so they are made safe there: clamped to
 // [0, M] and to their running maximum. Rows outside [o_0, o_E) belong to no
