@@ -1412,6 +1412,14 @@ void few_rows_plan(GroupPlan& p, int64_t M, int E, int64_t N) {
     p.part_bytes = up256(static_cast<size_t>(2 * kPlanSms) * p.part_rows * 256 * 4);
 }
 
+// What the tickets and parts of any batch of up to M rows take, whatever its
+// plan: a workspace made for the largest batch serves the smaller ones.
+size_t plan_bound(int64_t M, int E, int64_t cols) {
+    const int64_t act = std::min<int64_t>(E, M), few = std::min<int64_t>(M, 12 * E) / 8;
+    return up256(static_cast<size_t>((std::max(M / 64, few) + act) * cdiv(cols, 256)) * 4) +
+           up256(static_cast<size_t>(2 * kPlanSms) * std::min<int64_t>(std::max<int64_t>(M, 16), 64) * 256 * 4);
+}
+
 // M rows over E experts: 32-bit row numbers and tile numbers.
 bool rows_ok(int64_t M, int E, int64_t cols) {
     return M <= (int64_t(1) << 30) && (M / 64 + E) * cdiv(cols, 256) < (int64_t(1) << 31);
@@ -1451,6 +1459,7 @@ ExpertLayout expert_layout(int op, int64_t M, int64_t N, int64_t K, int r, int E
         L.sU = L.total;
         L.total += up256(static_cast<size_t>(M) * kTermsU * r * 2);
     }
+    L.total += plan_bound(M, E, op == QLORA_OP_BWD ? K : N) - L.plan.tickets_bytes - L.plan.part_bytes;
     return L;
 }
 
@@ -1575,7 +1584,7 @@ Int8Layout int8_layout(int64_t M, int64_t N, int64_t K, int E) {
     L.part = L.header;
     L.xq = L.part + L.plan.part_bytes;
     L.xs = L.xq + up256(static_cast<size_t>(M) * K);
-    L.total = L.xs + up256(static_cast<size_t>(M) * 4);
+    L.total = L.xs + up256(static_cast<size_t>(M) * 4) + plan_bound(M, E, N) - L.plan.tickets_bytes - L.plan.part_bytes;
     return L;
 }
 

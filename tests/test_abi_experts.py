@@ -33,6 +33,28 @@ def test_workspaces(q):
         assert q.workspace_bytes_int8(*bad) == 0, bad
 
 
+@pytest.mark.parametrize("N,K,r,E", [(512, 512, 16, 4), (11008, 4096, 64, 8), (8, 64, 8, 1), (264, 320, 8, 512),
+                                     (2056, 1088, 32, 16)])
+def test_workspaces_of_large_batches_serve_small_ones(q, N, K, r, E):
+    L = q.lib()
+    w = weight(q, N=E * N, K=K)
+    w8 = q.Int8WeightC(P, P, E * N, K)
+    sizes = [1, 2, 7, 8, 9, 15, 16, 17, 48, 63, 64, 65, 96, 97, 250, 700, 1500, 4000, 6145, 9000, 70000]
+    last = [0, 0, 0]
+    for M in sizes:
+        now = [q.workspace_bytes_experts(q.OP_FWD, M, N, K, r, E), q.workspace_bytes_experts(q.OP_BWD, M, N, K, r, E),
+               q.workspace_bytes_int8(M, N, K, E)]
+        assert all(a >= b for a, b in zip(now, last)), (M, now, last)
+        last = now
+        # enough for the call itself, which ends on an injected failure
+        q.set_option(q.OPT_FAIL_LAUNCHES, 3)
+        got = [L.qlora_linear_fwd_experts(P, M, ctypes.byref(w), E, P, P, P, r, 16.0, P, None, P, now[0], None),
+               L.qlora_linear_bwd_experts(P, P, M, ctypes.byref(w), E, P, P, P, r, 16.0, P, P, P, P, P, now[1], None),
+               L.qlora_linear_int8_experts(P, M, ctypes.byref(w8), E, P, P, P, now[2], None)]
+        q.set_option(q.OPT_FAIL_LAUNCHES, 0)
+        assert got == [-6, -6, -6], (M, got)
+
+
 def test_forward_and_backward_refusals(q):
     L = q.lib()
     ws = q.workspace_bytes_experts(q.OP_FWD, 64, 512, 512, 16, 4)

@@ -364,6 +364,66 @@ def test_other_stream_and_captured_replay(q):
     assert q.device_status(ws) == 0 and q.device_status(wsb) == 0
 
 
+@pytest.mark.parametrize("counts", [[1, 0, 2], [30, 45, 20], [300, 40, 513]], ids=["few", "small", "pairs"])
+def test_two_streams_at_once(q, counts):
+    """Two streams run forwards and backwards of different batches at the same
+    time, each with workspaces of its own."""
+    ts = [case(counts, N=1032, K=2048, r=16, seed=s) for s in (71, 72)]
+    ref = [run(q, t) for t in ts]
+    q.set_check_device_status(False)
+    state = []
+    for t in ts:
+        off = torch.tensor(t["off"], dtype=torch.int32, device="cuda")
+        ws = [torch.empty(q.workspace_bytes_experts(op, t["M"], t["N"], t["K"], t["r"], t["E"]), dtype=torch.uint8,
+                          device="cuda") for op in (q.OP_FWD, q.OP_BWD)]
+        state.append((quantised(q, t), [t[k].cuda() for k in ("X", "A", "B", "dY")], off, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    out = [[], []]
+    for _ in range(4):
+        for i, (w, (X, A, B, dY), off, ws, s) in enumerate(state):
+            with torch.cuda.stream(s):
+                Y, sT = q.linear_fwd_experts(X, w, A, B, off, ts[i]["E"], ts[i]["alpha"], ws=ws[0])
+                dX, dA, dB = q.linear_bwd_experts(dY, X, w, A, B, off, ts[i]["E"], ts[i]["alpha"], sT=sT, ws=ws[1])
+                out[i].append(dict(Y=Y, sT=sT, dX=dX, dA=dA, dB=dB))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(q.device_status(x) == 0 for x in state[i][3])
+        for got in out[i]:
+            for k in got:
+                assert torch.equal(got[k], ref[i][k]), (i, k)
+
+
+def test_graphs_that_share_a_workspace(q):
+    """Two graphs captured with one workspace, replayed in turn on one stream; the
+    workspace is the larger batch's."""
+    ts = [case([300, 0, 513], N=264, K=448, r=16, seed=81), case([2, 1, 0], N=264, K=448, r=16, seed=82)]
+    ref = [run(q, t) for t in ts]
+    q.set_check_device_status(False)
+    n = max(q.workspace_bytes_experts(op, ts[0]["M"], 264, 448, 16, 3) for op in (q.OP_FWD, q.OP_BWD))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    graphs, outs, keep = [], [], []
+    for t in ts:
+        w, off = quantised(q, t), torch.tensor(t["off"], dtype=torch.int32, device="cuda")
+        X, A, B, dY = (t[k].cuda() for k in ("X", "A", "B", "dY"))
+        keep.append((w, off, X, A, B, dY))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            Y, sT = q.linear_fwd_experts(X, w, A, B, off, 3, t["alpha"], ws=ws)
+            dX, dA, dB = q.linear_bwd_experts(dY, X, w, A, B, off, 3, t["alpha"], sT=sT, ws=ws)
+        graphs.append(g)
+        outs.append(dict(Y=Y, sT=sT, dX=dX, dA=dA, dB=dB))
+    for _ in range(2):
+        for i in range(2):
+            for v in outs[i].values():
+                v.zero_()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert q.device_status(ws) == 0
+            for k, v in outs[i].items():
+                assert torch.equal(v, ref[i][k]), (i, k)
+
+
 # ------------------------------------------------------------------- order --
 
 def order_ref(ids, E):
