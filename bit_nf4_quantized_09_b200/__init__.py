@@ -481,11 +481,19 @@ def linear_bwd_group(dY: torch.Tensor, X: torch.Tensor, group: list, A: torch.Te
 
 def _want(t: torch.Tensor | None, what: str, where: str, shape: tuple, dtype, device):
     """Raises unless t is a contiguous tensor of this shape, type and device."""
-    if t is None or t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+    if t is None or t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}" + (
             "" if t.is_contiguous() else ", not contiguous")
         raise QLoraError(-2 if t is not None and t.dtype == dtype and t.device == device else -1, where,
                          f"{what}: a contiguous {dtype} {tuple(shape)} on {device} is wanted, got {got}")
+
+
+def _out(t: torch.Tensor | None, what: str, where: str, shape: tuple, dtype, device) -> torch.Tensor:
+    """An output: the caller's tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _want(t, what, where, shape, dtype, device)
+    return t
 
 
 def _on(device, call, *args):
@@ -498,10 +506,14 @@ def _on(device, call, *args):
         return call(*args, _stream(device))
 
 
-def _ws_on(nbytes: int, device, ws: torch.Tensor | None, where: str) -> torch.Tensor:
-    if ws is not None and (ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous()):
+def _ws_on(nbytes, device, ws: torch.Tensor | None, where: str) -> torch.Tensor:
+    """The caller's workspace (the call itself checks its size), or a new one of
+    nbytes() bytes."""
+    if ws is None:
+        return _ws(nbytes(), device)
+    if ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
         raise QLoraError(-1, where, f"workspace: a contiguous uint8 tensor on {device} is wanted")
-    return _ws(nbytes, device, ws)
+    return ws
 
 
 def _check_on(ws: torch.Tensor, where: str, M: int):
@@ -539,15 +551,9 @@ def expert_order(ids: torch.Tensor, E: int, order: torch.Tensor | None = None, o
     _want(ids, "ids", where, (M,), torch.int32, dev)
     if not 1 <= E <= 512:
         raise QLoraError(-1, where, f"E = {E}")
-    if order is None:
-        order = torch.empty_like(ids)
-    else:
-        _want(order, "order", where, (M,), torch.int32, dev)
-    if offsets is None:
-        offsets = ids.new_empty(E + 1)
-    else:
-        _want(offsets, "offsets", where, (E + 1,), torch.int32, dev)
-    _check(_on(dev, lib().qlora_expert_order, _ptr(ids), M, E, _ptr(order), _ptr(offsets)), where)
+    order = torch.empty_like(ids) if order is None else _out(order, "order", where, (M,), torch.int32, dev)
+    offsets = ids.new_empty(E + 1) if offsets is None else _out(offsets, "offsets", where, (E + 1,), torch.int32, dev)
+    _check(_on(dev, lib().qlora_expert_order, ids.data_ptr(), M, E, order.data_ptr(), offsets.data_ptr()), where)
     return order, offsets
 
 
@@ -581,15 +587,14 @@ def linear_fwd_experts(X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: torch.
     held (a Y or sT allocated here holds nothing there)."""
     where = "qlora_linear_fwd_experts"
     M, N, K, r, dev = _expert_shapes(where, X, w, A, B, offsets, E)
-    Y = Y if Y is not None else torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-    _want(Y, "Y", where, (M, N), torch.bfloat16, dev)
+    Y = _out(Y, "Y", where, (M, N), torch.bfloat16, dev)
     if save_sT:
-        sT = sT if sT is not None else torch.empty(M, 2 * r, dtype=torch.bfloat16, device=dev)
-        _want(sT, "sT", where, (M, 2 * r), torch.bfloat16, dev)
-    ws = _ws_on(workspace_bytes_experts(OP_FWD, M, N, K, r, E), dev, ws, where)
+        sT = _out(sT, "sT", where, (M, 2 * r), torch.bfloat16, dev)
+    ws = _ws_on(lambda: workspace_bytes_experts(OP_FWD, M, N, K, r, E), dev, ws, where)
     v = w.c_view()
-    _check(_on(dev, lib().qlora_linear_fwd_experts, _ptr(X), M, ctypes.byref(v), E, _ptr(offsets), _ptr(A), _ptr(B), r,
-               float(alpha), _ptr(Y), _ptr(sT) if save_sT else None, _ptr(ws), ws.numel()), where)
+    _check(_on(dev, lib().qlora_linear_fwd_experts, X.data_ptr(), M, ctypes.byref(v), E, offsets.data_ptr(), A.data_ptr(),
+               B.data_ptr(), r, float(alpha), Y.data_ptr(), sT.data_ptr() if save_sT else None, ws.data_ptr(), ws.numel()),
+           where)
     _check_on(ws, where, M)
     return Y, (sT if save_sT else None)
 
@@ -606,16 +611,14 @@ def linear_bwd_experts(dY: torch.Tensor, X: torch.Tensor, w: NF4Weight, A: torch
     _want(dY, "dY", where, (M, N), torch.bfloat16, dev)
     if sT is not None:
         _want(sT, "sT", where, (M, 2 * r), torch.bfloat16, dev)
-    dX = dX if dX is not None else torch.empty(M, K, dtype=torch.bfloat16, device=dev)
-    dA = dA if dA is not None else torch.empty(E * r, K, dtype=torch.float32, device=dev)
-    dB = dB if dB is not None else torch.empty(E * N, r, dtype=torch.float32, device=dev)
-    _want(dX, "dX", where, (M, K), torch.bfloat16, dev)
-    _want(dA, "dA", where, (E * r, K), torch.float32, dev)
-    _want(dB, "dB", where, (E * N, r), torch.float32, dev)
-    ws = _ws_on(workspace_bytes_experts(OP_BWD, M, N, K, r, E), dev, ws, where)
+    dX = _out(dX, "dX", where, (M, K), torch.bfloat16, dev)
+    dA = _out(dA, "dA", where, (E * r, K), torch.float32, dev)
+    dB = _out(dB, "dB", where, (E * N, r), torch.float32, dev)
+    ws = _ws_on(lambda: workspace_bytes_experts(OP_BWD, M, N, K, r, E), dev, ws, where)
     v = w.c_view()
-    _check(_on(dev, lib().qlora_linear_bwd_experts, _ptr(dY), _ptr(X), M, ctypes.byref(v), E, _ptr(offsets), _ptr(A),
-               _ptr(B), r, float(alpha), _ptr(sT), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel()), where)
+    _check(_on(dev, lib().qlora_linear_bwd_experts, dY.data_ptr(), X.data_ptr(), M, ctypes.byref(v), E, offsets.data_ptr(),
+               A.data_ptr(), B.data_ptr(), r, float(alpha), None if sT is None else sT.data_ptr(), dX.data_ptr(),
+               dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), ws.numel()), where)
     _check_on(ws, where, M)
     return dX, dA, dB
 
@@ -671,11 +674,11 @@ def _int8_call(where, X, w, E, Y, ws, *group):
     _want(X, "X", where, (M, w.K), torch.bfloat16, dev)
     if w.codes.device != dev:
         raise QLoraError(-1, where, f"the weight is on {w.codes.device}, X on {dev}")
-    Y = Y if Y is not None else torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-    _want(Y, "Y", where, (M, N), torch.bfloat16, dev)
-    ws = _ws_on(workspace_bytes_int8(M, N, w.K, E), dev, ws, where)
+    Y = _out(Y, "Y", where, (M, N), torch.bfloat16, dev)
+    ws = _ws_on(lambda: workspace_bytes_int8(M, N, w.K, E), dev, ws, where)
     v = w.c_view()
-    _check(_on(dev, getattr(lib(), where), _ptr(X), M, ctypes.byref(v), *group, _ptr(Y), _ptr(ws), ws.numel()), where)
+    _check(_on(dev, getattr(lib(), where), X.data_ptr(), M, ctypes.byref(v), *group, Y.data_ptr(), ws.data_ptr(), ws.numel()),
+           where)
     _check_on(ws, where, M)
     return Y
 
