@@ -10,12 +10,13 @@
 // shared memory: lanes with equal ids find each other by one vote per bit of
 // the id, and the lowest of them adds their number (no atomics: a fixed
 // result). A scan over the warps, the CTAs of the cluster (through distributed
-// shared memory) and the ids turns the counts into first places. Pass 2 reads
-// the ids again (L2) and writes each row to its place.
+// shared memory) and the ids turns the counts into first places. Pass 2 writes
+// each row to its place: what it needs is in registers for pieces of up to 256
+// rows; the ids of longer ones are read again (L2).
 //
 // Bound by latency: 8 bytes per row move. 32768 ids over 64 experts: 53 us with
-// one CTA and match instructions, 12 us with the cluster and votes; 16 ids over
-// 8 experts 4.8 us, about what a launch takes.
+// one CTA and match instructions, 12 us with the cluster and votes, 8 us with the
+// keys and places kept; 16 ids over 8 experts 2.7 us, about what a launch takes.
 #include <algorithm>
 
 #include "kernels.h"
@@ -60,24 +61,34 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
         const int id = __ldg(ids + row);
         return id >= 0 && id < E ? id : E;
     };
+    // Pass 1. The keys of a piece of up to 32 kAhead rows, and each row's place
+    // among the piece's rows of its id, stay in registers for pass 2.
+    int key[kAhead], place[kAhead];
     for (int b = lo; b < hi; b += 32 * kAhead) {
-        int key[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) key[j] = key_of(b + 32 * j + lane);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
+            const int row = b + 32 * j + lane;
+            if (row - lane >= hi) break;  // the same for the whole warp
             const unsigned same = same_key(key[j], bits);
-            if (b + 32 * j + lane < hi && lane == __ffs(same) - 1) mine[key[j]] += __popc(same);
+            const int first = row < hi ? mine[key[j]] : 0;
+            place[j] = first + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (row < hi && lane == __ffs(same) - 1) mine[key[j]] = first + __popc(same);
             __syncwarp();
         }
     }
     __syncthreads();
-    // an id's places by warp, then its total in this CTA
-    int total = 0;
+    // an id's places by warp, and its total in this CTA
+    int total = 0, by_warp[kMaxWarps];
     if (tid < H) {
-        for (int w = 0; w < kWarps; ++w) {
-            const int n = hist[w * H + tid];
-            hist[w * H + tid] = total;
+#pragma unroll
+        for (int w = 0; w < kMaxWarps; ++w) by_warp[w] = w < kWarps ? hist[w * H + tid] : 0;
+#pragma unroll
+        for (int w = 0; w < kMaxWarps; ++w) {
+            const int n = by_warp[w];
+            by_warp[w] = total;
             total += n;
         }
         totals[tid] = total;
@@ -111,11 +122,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
     if (tid < H) {
         const int start = warp_sum[warp] + incl - total;
         if (cta == 0) offsets[tid] = start;
-        for (int w = 0; w < kWarps; ++w) hist[w * H + tid] += start + before;
+#pragma unroll
+        for (int w = 0; w < kMaxWarps; ++w)
+            if (w < kWarps) hist[w * H + tid] = start + before + by_warp[w];
     }
     __syncthreads();
+    // Pass 2
+    if (per <= 32 * kAhead) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int row = lo + 32 * j + lane;
+            if (row < hi) order[mine[key[j]] + place[j]] = row;
+        }
+        return;
+    }
     for (int b = lo; b < hi; b += 32 * kAhead) {
-        int key[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) key[j] = key_of(b + 32 * j + lane);
 #pragma unroll

@@ -444,6 +444,18 @@ def test_order(q, M, E):
     assert offsets.tolist() == rf
 
 
+@pytest.mark.parametrize("M,E", [(4097, 512), (65536, 64), (65537, 3), (150001, 20)])
+def test_order_of_long_batches(q, M, E):
+    """Pieces of up to 256 rows per warp, and longer ones."""
+    g = torch.Generator().manual_seed(M)
+    ids = torch.randint(-1, E + 1, (M,), generator=g, dtype=torch.int32)
+    order, offsets = q.expert_order(ids.cuda(), E)
+    torch.cuda.synchronize()
+    key = torch.where((ids >= 0) & (ids < E), ids, torch.full_like(ids, E)).long()
+    assert torch.equal(order.cpu().long(), torch.sort(key, stable=True).indices)
+    assert offsets.tolist() == [int((key < e).sum()) for e in range(E + 1)]
+
+
 def test_order_of_one_expert_and_none(q):
     for v in (0, 2, -1):
         ids = torch.full((777,), v, dtype=torch.int32, device="cuda")
