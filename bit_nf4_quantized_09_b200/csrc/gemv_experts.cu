@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(Lay<MT>::kThreads, 1)
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
                     const uint2 wa = lds64(st + coff[jj]), wb = lds64(st + coff[jj] + 1024u);
-                    const uint2 va = lds64(st + coff[jj] + 2048u), vb = lds64(st + coff[jj] + 3072u);
+                    const uint2 va = lds64(st + coff[jj] + 2048u), vb = lds64(st + coff[jj] + 2048u + 1024u);
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         uint4 x[MT];

@@ -15,9 +15,11 @@
 //     before: 2^-17 and 2^-25 relative instead of bf16's 2^-9; the gradients
 //     run one UMMA per term into the same accumulator, which costs little
 //     beside reading X and dY once;
-//   - every 512 reduction elements the accumulator is read out and added to
-//     fp32 registers (round to nearest), two TMEM buffers in turn, so the
-//     tensor core never waits for it.
+//   - every 512 reduction elements (128 for sT and sU: at 512 as many of their
+//     first terms round the other way as in a plain fp32 sum, at 128 half of
+//     those, in the same time) the accumulator is read out and added to fp32
+//     registers (round to nearest), two TMEM buffers in turn, so the tensor core
+//     never waits for it.
 //
 // Both kernels read X and dY once (2 bytes per token and column) and are bound by
 // the latency of their loads at the bytes in flight that the stages hold: sT of
@@ -34,7 +36,8 @@ namespace qlora {
 namespace {
 
 constexpr int kThreads = 192;
-constexpr int kFlush = 8;             // 64-deep steps between read-outs
+constexpr int kFlush = 8;             // 64-deep steps between read-outs of the gradients
+constexpr int kDownFlush = 2;         // and of sT and sU
 constexpr uint32_t kABytes = 128 * 64 * 2;
 constexpr uint32_t kTmemCols = 128;   // two accumulators of up to 64 columns
 constexpr int kMaxStages = 8;
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     volatile int* abort_flag = &bars.abort_flag;
     const int KT = static_cast<int>((a.red + 63) / 64);
     const int steps = y < KT ? (KT - y + S - 1) / S : 0;
-    const int chunks = (steps + kFlush - 1) / kFlush;
+    const int chunks = (steps + kDownFlush - 1) / kDownFlush;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -178,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t bk = static_cast<uint32_t>(kBMn ? 16 * NR * 2 : 32) / 16;
         bool ok = true;
         for (int i = 0; ok && i < steps; ++i) {
-            const int s = i % stages, chunk = i / kFlush, p = chunk & 1;
-            if (i % kFlush == 0 && chunk >= 2)
+            const int s = i % stages, chunk = i / kDownFlush, p = chunk & 1;
+            if (i % kDownFlush == 0 && chunk >= 2)
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(bars.acc_free + p, static_cast<uint32_t>((chunk >> 1) - 1) & 1u, tmo,
                                                        a.status));
             ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bars.full + s, static_cast<uint32_t>(i / stages) & 1u, tmo, a.status));
@@ -189,9 +192,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint64_t ad = ad0 + static_cast<uint32_t>(s) * (stage / 16), bd = bd0 + static_cast<uint32_t>(s) * (stage / 16);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_f16(tmem + p * 64, ad + kk * 2, bd + kk * bk, idesc, (i % kFlush > 0 || kk > 0) ? 1u : 0u);
+                    umma_f16(tmem + p * 64, ad + kk * 2, bd + kk * bk, idesc, (i % kDownFlush > 0 || kk > 0) ? 1u : 0u);
                 umma_commit(bars.empty + s);
-                if (i % kFlush == kFlush - 1 || i == steps - 1) umma_commit(bars.acc_full + p);
+                if (i % kDownFlush == kDownFlush - 1 || i == steps - 1) umma_commit(bars.acc_full + p);
             }
             __syncwarp();
         }
