@@ -1504,7 +1504,7 @@ qlora_status expert_down(bool bwd, const uint16_t* act, int64_t M, int64_t red, 
 // Y (forward) or dX of the experts' rows.
 qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_nf4_weight* w, int64_t N, int E,
                            const int32_t* offsets, const uint16_t* rank_in, int terms, const uint16_t* rank_w, int r,
-                           uint16_t* out, uint8_t* base, const ExpertLayout& L, int sms, bool pdl, cudaStream_t st) {
+                           uint16_t* out, uint8_t* base, const ExpertLayout& L, int sms, cudaStream_t st) {
     const int64_t K = w->K, red = dx ? N : K, cols = dx ? K : N;
     const GroupPlan& p = L.plan;
     ExpertGemmArgs a{};
@@ -1556,7 +1556,7 @@ qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_
                   CU_TENSOR_MAP_SWIZZLE_128B, "B", E);
     }
     if (injected_failure()) return QLORA_ERR_CUDA;
-    QLORA_LAUNCH(launch_expert_gemm(dx, t_act, t_codes, t_lact, t_lw, a, tables(), pdl, st), 1,
+    QLORA_LAUNCH(launch_expert_gemm(dx, t_act, t_codes, t_lact, t_lw, a, tables(), st), 1,
                  dx ? "expert dX" : "expert forward");
     return QLORA_OK;
 }
@@ -1630,7 +1630,7 @@ qlora_status int8_impl(const uint16_t* X, int64_t M, const qlora_int8_weight* w,
     a.status = reinterpret_cast<int*>(base);
     a.timeout_ns = timeout_ns();
     if (injected_failure()) return QLORA_ERR_CUDA;
-    QLORA_LAUNCH(launch_int8_gemm(tx, tw, a, true, st), 1, "int8 matmul");
+    QLORA_LAUNCH(launch_int8_gemm(tx, tw, a, st), 1, "int8 matmul");
     return QLORA_OK;
 }
 
@@ -1701,7 +1701,7 @@ qlora_status qlora_linear_fwd_experts(const uint16_t* X, int64_t M, const qlora_
     if ((s = expert_down(false, X, M, w->K, A, E, offsets, r, alpha / static_cast<float>(r), kTermsT, sT, status, L.header,
                          st)) != QLORA_OK)
         return s;
-    return expert_matmul(false, X, M, w, N, E, offsets, sT, kTermsT, B, r, Y, base, L, sms, true, st);
+    return expert_matmul(false, X, M, w, N, E, offsets, sT, kTermsT, B, r, Y, base, L, sms, st);
 }
 
 qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int64_t M, const qlora_nf4_weight* w, int E,
@@ -1742,10 +1742,10 @@ qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int
         return s;
     if ((s = expert_down(true, dY, M, N, B, E, offsets, r, scale, kTermsU, sU, status, sT_in ? L.header : 0, st)) != QLORA_OK)
         return s;
-    if ((s = expert_matmul(true, dY, M, w, N, E, offsets, sU, kTermsU, A, r, dX, base, L, sms, false, st)) != QLORA_OK)
+    if ((s = expert_matmul(true, dY, M, w, N, E, offsets, sU, kTermsU, A, r, dX, base, L, sms, st)) != QLORA_OK)
         return s;
     // dA and dB need only sU and sT: as dX's programmatic dependent their CTAs
-    // start on the SMs that dX leaves idle
+    // start on the SMs that dX leaves idle, once dX's have waited for sU
     CUtensorMap tx, tdy, tsu, tst;
     QLORA_MAP(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, K, M, K * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "X^T");
     QLORA_MAP(&tdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, N, M, N * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "dY^T");
@@ -1768,7 +1768,7 @@ qlora_status qlora_linear_bwd_experts(const uint16_t* dY, const uint16_t* X, int
     g.status = status;
     g.timeout_ns = timeout_ns();
     if (injected_failure()) return QLORA_ERR_CUDA;
-    QLORA_LAUNCH(launch_expert_grads(tx, tdy, tsu, tst, g, true, st), 1, "expert gradients");
+    QLORA_LAUNCH(launch_expert_grads(tx, tdy, tsu, tst, g, st), 1, "expert gradients");
     return QLORA_OK;
 }
 

@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap tm_lact, const __grid_constant__ CUtensorMap tm_lw,
                 const ExpertGemmArgs a, const Nf4Tables tab) {
     using L = Lay<CAP>;
-    asm volatile("griddepcontrol.launch_dependents;");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     TileSched& sched = *reinterpret_cast<TileSched*>(smem + L::kOffSched);
@@ -213,7 +212,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     // sT or sU of the preceding launch, of which this one may
                     // be a programmatic dependent
-                    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+                    if (!waited) {
+                        asm volatile("griddepcontrol.wait;" ::: "memory");
+                        // behind dX come the gradients, which read sU too
+                        asm volatile("griddepcontrol.launch_dependents;");
+                    }
                     waited = true;
                     load(&tm_lact, s, 0);
                 }
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool kTransW, bool kNoDq, int CAP>
 cudaError_t launch_one(const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact, const CUtensorMap& lw,
-                       const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl, cudaStream_t st) {
+                       const ExpertGemmArgs& a, const Nf4Tables& tab, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
     cfg.blockDim = dim3(kThreads);
@@ -609,24 +612,24 @@ cudaError_t launch_one(const CUtensorMap& act, const CUtensorMap& codes, const C
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 2 : 1;
+    cfg.numAttrs = 2;
     if (Lay<CAP>::kPair) cfg.gridDim.x &= ~1u;
     return cudaLaunchKernelEx(&cfg, expert_gemm<kTransW, kNoDq, CAP>, act, codes, lact, lw, a, tab);
 }
 
 template <bool kTransW, int CAP>
 cudaError_t launch_cap(const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact, const CUtensorMap& lw,
-                       const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl, cudaStream_t st) {
-    return a.c.absmax ? launch_one<kTransW, true, CAP>(act, codes, lact, lw, a, tab, pdl, st)
-                      : launch_one<kTransW, false, CAP>(act, codes, lact, lw, a, tab, pdl, st);
+                       const ExpertGemmArgs& a, const Nf4Tables& tab, cudaStream_t st) {
+    return a.c.absmax ? launch_one<kTransW, true, CAP>(act, codes, lact, lw, a, tab, st)
+                      : launch_one<kTransW, false, CAP>(act, codes, lact, lw, a, tab, st);
 }
 
 template <bool kTransW>
 cudaError_t launch_dir(const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact, const CUtensorMap& lw,
-                       const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl, cudaStream_t st) {
-    if (a.cap == 64) return launch_cap<kTransW, 64>(act, codes, lact, lw, a, tab, pdl, st);
-    if (a.cap == 256) return launch_cap<kTransW, 256>(act, codes, lact, lw, a, tab, pdl, st);
-    return launch_cap<kTransW, 512>(act, codes, lact, lw, a, tab, pdl, st);
+                       const ExpertGemmArgs& a, const Nf4Tables& tab, cudaStream_t st) {
+    if (a.cap == 64) return launch_cap<kTransW, 64>(act, codes, lact, lw, a, tab, st);
+    if (a.cap == 256) return launch_cap<kTransW, 256>(act, codes, lact, lw, a, tab, st);
+    return launch_cap<kTransW, 512>(act, codes, lact, lw, a, tab, st);
 }
 
 template <bool kTransW, bool kNoDq, int CAP>
@@ -653,12 +656,11 @@ cudaError_t expert_gemm_init_device() {
 }
 
 cudaError_t launch_expert_gemm(bool trans_w, const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact,
-                               const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl,
-                               cudaStream_t st) {
+                               const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, cudaStream_t st) {
     if (a.E < 1 || a.E > kMaxExperts || a.ctas < 2 || (a.cap != 64 && a.cap != 256 && a.cap != 512) || a.rank_cols < 1 || a.rank_cols > 64)
         return cudaErrorInvalidValue;
-    return trans_w ? launch_dir<true>(act, codes, lact, lw, a, tab, pdl, st)
-                   : launch_dir<false>(act, codes, lact, lw, a, tab, pdl, st);
+    return trans_w ? launch_dir<true>(act, codes, lact, lw, a, tab, st)
+                   : launch_dir<false>(act, codes, lact, lw, a, tab, st);
 }
 
 }  // namespace qlora

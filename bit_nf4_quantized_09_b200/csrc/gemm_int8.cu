@@ -553,7 +553,7 @@ cudaError_t launch_quantize(const void* X, int64_t rows, int64_t K, int8_t* code
 }
 
 template <int CAP>
-cudaError_t launch_one(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, bool pdl, cudaStream_t st) {
+cudaError_t launch_one(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
     cfg.blockDim = dim3(kThreads);
@@ -567,7 +567,7 @@ cudaError_t launch_one(const CUtensorMap& x, const CUtensorMap& w, const Int8Gem
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 2 : 1;
+    cfg.numAttrs = 2;
     if (Lay<CAP>::kPair) cfg.gridDim.x &= ~1u;
     return cudaLaunchKernelEx(&cfg, int8_gemm<CAP>, x, w, a);
 }
@@ -585,12 +585,11 @@ cudaError_t int8_init_device() {
                                 static_cast<int>(Lay<64>::kBytes));
 }
 
-cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, bool pdl,
-                             cudaStream_t st) {
+cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, cudaStream_t st) {
     if (a.E < 1 || a.E > kMaxExperts || a.ctas < 2 || (a.cap != 64 && a.cap != 256 && a.cap != 512))
         return cudaErrorInvalidValue;
-    if (a.cap == 512) return launch_one<512>(x, w, a, pdl, st);
-    return a.cap == 256 ? launch_one<256>(x, w, a, pdl, st) : launch_one<64>(x, w, a, pdl, st);
+    if (a.cap == 512) return launch_one<512>(x, w, a, st);
+    return a.cap == 256 ? launch_one<256>(x, w, a, st) : launch_one<64>(x, w, a, st);
 }
 
 cudaError_t launch_quantize_rows(const void* X, bool bf16, int64_t rows, int64_t K, int8_t* codes, float* scale,

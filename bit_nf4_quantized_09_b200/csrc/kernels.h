@@ -321,8 +321,7 @@ struct ExpertGemmArgs {
 // Caps 256 and 512 (pairs of CTAs): act and lact box {64, 64}; codes: forward
 // box {32, 128, 1}, dX {64, 64, 1} SW64; lw: forward box {64, 128, 1}.
 cudaError_t launch_expert_gemm(bool trans_w, const CUtensorMap& act, const CUtensorMap& codes, const CUtensorMap& lact,
-                               const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, bool pdl,
-                               cudaStream_t st);
+                               const CUtensorMap& lw, const ExpertGemmArgs& a, const Nf4Tables& tab, cudaStream_t st);
 cudaError_t expert_gemm_init_device();
 // The forward in tiles of few rows (cap 8 or 16): x box {64, cap} SW128,
 // codes {K/2, N, E} box {128, 256, 1} SW128. A programmatic dependent of the
@@ -376,7 +375,7 @@ struct ExpertGradArgs {
 // x {K, M}, dy {N, M}, su {terms_u r, M}, st {terms_t r, M}: all box {64, 64}
 // SW128.
 cudaError_t launch_expert_grads(const CUtensorMap& x, const CUtensorMap& dy, const CUtensorMap& su,
-                                const CUtensorMap& st_, ExpertGradArgs a, bool pdl, cudaStream_t st);
+                                const CUtensorMap& st_, ExpertGradArgs a, cudaStream_t st);
 cudaError_t expert_rank_init_device();
 
 cudaError_t launch_expert_order(const int* ids, int M, int E, int* order, int* offsets, cudaStream_t st);
@@ -399,8 +398,7 @@ struct Int8GemmArgs {
 };
 // x: token codes {K, M} box {128, 16}, or {128, 64} from cap 256 on; w: {K, N, E}
 // box {128, 256, 1}, of cap 512 (pairs of CTAs) {128, 128, 1}; both SW128.
-cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, bool pdl,
-                             cudaStream_t st);
+cudaError_t launch_int8_gemm(const CUtensorMap& x, const CUtensorMap& w, const Int8GemmArgs& a, cudaStream_t st);
 cudaError_t int8_init_device();
 // X: fp32 or bf16 [rows, K], K % 16 == 0. clear: words that the launch zeroes.
 cudaError_t launch_quantize_rows(const void* X, bool bf16, int64_t rows, int64_t K, int8_t* codes, float* scale,

@@ -601,7 +601,7 @@ cudaError_t launch_expert_down_few(const uint16_t* X, const uint16_t* A, const E
 }
 
 cudaError_t launch_expert_grads(const CUtensorMap& x, const CUtensorMap& dy, const CUtensorMap& su, const CUtensorMap& st_,
-                                ExpertGradArgs a, bool pdl, cudaStream_t st) {
+                                ExpertGradArgs a, cudaStream_t st) {
     const int boxes = (std::max(a.terms_u, a.terms_t) * a.r + 63) / 64;
     if (a.r < 8 || boxes < 1 || boxes > 3 || a.E < 1 || a.E > kMaxExperts || a.ctas < 1) return cudaErrorInvalidValue;
     a.stages = static_cast<int>(std::min<size_t>(kMaxStages, kGradSmem / (kABytes + boxes * kBoxBytes)));
@@ -616,7 +616,7 @@ cudaError_t launch_expert_grads(const CUtensorMap& x, const CUtensorMap& dy, con
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, expert_grads, x, dy, su, st_, a);
 }
 
