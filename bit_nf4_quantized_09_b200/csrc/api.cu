@@ -1378,7 +1378,8 @@ GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps, bool pairs) 
     auto consider = [&](int cap, int units, double least, double rows_per_step) {
         const int64_t per = cdiv(E > 1 && !pairs ? avg * 5 / 4 : avg, cap);
         const double step = std::max(least, static_cast<double>(avg) / per / rows_per_step);
-        const double cost = static_cast<double>(cdiv(tiles_w * act * per, units) * steps) * step;
+        // a pair's tile ends with three steps' worth of rank-r term and epilogue
+        const double cost = static_cast<double>(cdiv(tiles_w * act * per, units) * (steps + (pairs ? 3 : 0))) * step;
         if (cost < best) {
             best = cost;
             p.cap = cap;
@@ -1516,6 +1517,7 @@ qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_
     a.out_cols = cols;
     a.red = red;
     a.rank_cols = r;
+    a.rank_terms = red < 1024 ? 2 : 1;  // what one term leaves of a short reduction's result (gemm_experts.cu)
     a.rank_x = rank_in;
     a.rank_w = rank_w;
     a.rank_ld = static_cast<int64_t>(terms) * r;
@@ -1542,8 +1544,8 @@ qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_
     const uint32_t box = pair ? 64 : 16, wrows = pair ? 128 : 256;
     QLORA_MAP(&t_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, red, M, red * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B,
               dx ? "dY" : "X");
-    // the first term of sT (sU): bf16 as the output is
-    QLORA_MAP(&t_lact, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_in, r, M, static_cast<uint64_t>(terms) * r * 2, 64, box,
+    // the first two terms of sT (sU)
+    QLORA_MAP(&t_lact, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank_in, 2 * r, M, static_cast<uint64_t>(terms) * r * 2, 64, box,
               CU_TENSOR_MAP_SWIZZLE_128B, dx ? "sU" : "sT");
     if (dx) {
         QLORA_MAP(&t_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, N, K / 2, wrows / 2, 64,

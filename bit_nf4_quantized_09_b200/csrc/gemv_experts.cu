@@ -349,14 +349,16 @@ __global__ void __launch_bounds__(Lay<MT>::kThreads, 1)
             if (tl.k_hi == steps) {
                 // the rank-r term, by the CTA that has the tile's last step
                 asm volatile("griddepcontrol.wait;" ::: "memory");  // sT of the preceding launch
-                for (int k0 = 0; k0 < a.rank_cols; k0 += 16) {
-                    const int j0 = k0 + 2 * q, j1 = j0 + 8;
+                // (both terms of sT with the same rows of B)
+                for (int k1 = 0; k1 < 2 * a.rank_cols; k1 += min(16, a.rank_cols)) {
+                    const int term = k1 >= a.rank_cols ? a.rank_cols : 0;
+                    const int j0 = k1 - term + 2 * q, j1 = j0 + 8;
                     const bool has1 = j1 < a.rank_cols;
                     uint32_t x0[MT], x1[MT];
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
                         const bool tok = g + 8 * t < tl.rows;
-                        const uint16_t* x = a.rank_x + static_cast<int64_t>(tl.row0 + (tok ? g + 8 * t : 0)) * a.rank_ld;
+                        const uint16_t* x = a.rank_x + static_cast<int64_t>(tl.row0 + (tok ? g + 8 * t : 0)) * a.rank_ld + term;
                         x0[t] = tok ? __ldcg(reinterpret_cast<const uint32_t*>(x + j0)) : 0u;
                         x1[t] = tok && has1 ? __ldcg(reinterpret_cast<const uint32_t*>(x + j1)) : 0u;
                     }
