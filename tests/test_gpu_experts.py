@@ -188,6 +188,30 @@ def test_pairs_against_fp64(q, name):
         assert torch.equal(a[k], b[k]), k
 
 
+@pytest.mark.parametrize("counts,N,K,r", [([5, 2], 136, 64, 8), ([40, 30], 264, 128, 16), ([300, 200], 520, 960, 32),
+                                          ([700, 513], 392, 64, 64), ([3, 9], 264, 2048, 64)])
+def test_rank_r_terms_are_not_rounded_away(q, counts, N, K, r):
+    """On short reductions, and in the forward of few rows, sT and sU enter Y and
+    dX as two bf16 terms: what they leave is 2^-8 of 2^-8 of them."""
+    t = case(counts, N=N, K=K, r=r)
+    g = run(q, t)
+    What = what_of(t["W"], True)
+    s = t["alpha"] / r
+    for e in range(t["E"]):
+        m = slice(t["off"][e], t["off"][e + 1])
+        We, A, B = What[e * N:(e + 1) * N], f64(t["A"][e * r:(e + 1) * r]), f64(t["B"][e * N:(e + 1) * N])
+        X, dY = f64(t["X"][m]), f64(t["dY"][m])
+        sT, sTa = s * X @ A.T, s * np.abs(X) @ np.abs(A).T
+        Y = X @ We.T + sT @ B.T
+        within("Y", f64(g["Y"][m]), Y, 2.0 ** -8 * np.abs(Y) + (2.0 ** -16 + acc(r)) * np.abs(sT) @ np.abs(B).T
+               + acc(K) * (np.abs(X) @ np.abs(We).T + sTa @ np.abs(B).T))
+        if N < 1024:
+            sU, sUa = s * dY @ B, s * np.abs(dY) @ np.abs(B)
+            dX = dY @ We + sU @ A
+            within("dX", f64(g["dX"][m]), dX, 2.0 ** -8 * np.abs(dX) + (2.0 ** -16 + acc(r)) * np.abs(sU) @ np.abs(A)
+                   + acc(N) * (np.abs(dY) @ np.abs(We) + sUa @ np.abs(A)))
+
+
 @pytest.mark.parametrize("counts", [[3, 5, 1], [9, 14, 6]], ids=["8", "16"])
 def test_few_rows_do_not_leak(q, counts):
     """As for many rows: NaN and infinities stay in their own rows."""
