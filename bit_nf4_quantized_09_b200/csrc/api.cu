@@ -1374,7 +1374,8 @@ GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps, bool pairs) 
     const int64_t avg = std::max<int64_t>(1, cdiv(M, act)), tiles_w = cdiv(cols, 256);
     const int64_t t64 = tiles_w * act * cdiv(pairs ? avg * 3 / 2 : avg, 64);
     const double whole64 = static_cast<double>(cdiv(t64, kPlanSms) * steps);
-    double best = std::min(whole64, static_cast<double>(t64) * steps / kPlanSms + kFixUp);
+    const int fix_up = pairs ? kFixUp : int8_fix_up(static_cast<int>(std::min<int64_t>(M, 64)), static_cast<int>(steps));
+    double best = std::min(whole64, static_cast<double>(t64) * steps / kPlanSms + fix_up);
     auto consider = [&](int cap, int units, double least, double rows_per_step) {
         const int64_t per = cdiv(E > 1 && !pairs ? avg * 5 / 4 : avg, cap);
         const double step = std::max(least, static_cast<double>(avg) / per / rows_per_step);

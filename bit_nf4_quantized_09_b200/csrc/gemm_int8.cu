@@ -30,8 +30,8 @@
 // Measured, with the quantiser: 4096 x 11008 x 4096 135 us (2.7 Pop/s, the tensor
 // pipe 76 % busy; 139 us in tiles of 256), 8192 rows of 16 experts of 4096 x 4096
 // 134 us (143 us), both bound by the tensor pipe, its clock under load and the
-// rounds of whole tiles. One token, 22016 x 8192: 39 us, 4.6 TB/s, bound by the
-// weight's stream and some 10 us of launches, quantising and meeting parts.
+// rounds of whole tiles. One token, 22016 x 8192: 37 us, 4.9 TB/s, bound by the
+// weight's stream and some 8 us of launches and quantising.
 #include "kernels.h"
 #include "tiles.cuh"
 
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if (L::kPair) cluster_sync();  // the partner's barriers are initialised before any remote arrival
     const uint32_t tmem = *tmem_slot;
-    const Ranges ranges(sched.base[a.E] * tiles_w, KT, units, CAP == 64);
+    const Ranges ranges(sched.base[a.E] * tiles_w, KT, units, CAP == 64, int8_fix_up(static_cast<int>(a.M), KT));
     SegIter<> it(sched, ranges, unit, tiles_w);
     Tile tl;
 

@@ -218,6 +218,14 @@ struct Tile {
 // range of fewer than four steps is not worth a CTA.
 constexpr int kFixUp = 8, kMinSteps = 4;
 
+// Of the 8-bit product, whose steps are a third as long and whose parts of up to
+// 64 rows take longer to join than a few, in its steps; and a quarter of the
+// tile's steps, since a stream of weights that fills the memory's rate gains
+// nothing by more CTAs. Whole and shared: 8 x 64 x 4096 12.9 and 10.8 us, 64 x 64
+// x 4096 15.8 and 17.0, 1 x 22016 x 8192 37.0 and 39.5, 100 x 11008 x 4096 20.0
+// and 29.7.
+__host__ __device__ inline int int8_fix_up(int M, int steps) { return 16 + (M < 64 ? M : 64) / 4 + steps / 4; }
+
 // The share-out: `tiles` tiles of `steps` reduction steps over P CTAs. Tiles
 // below `whole` are taken whole; the steps of the others (units in all) go in
 // ranges to Q CTAs, each with at least one step, so that all of the CTAs
