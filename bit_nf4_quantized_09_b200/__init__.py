@@ -138,8 +138,10 @@ def _after_call(ws: torch.Tensor, where: str, M: int = 1):
 
 try:
     _raw_stream = torch._C._cuda_getCurrentRawStream  # fast path: the handle without a Stream object
+    _current_device = torch._C._cuda_getDevice        # for callers that hold a CUDA tensor
 except AttributeError:  # pragma: no cover
     _raw_stream = None
+    _current_device = torch.cuda.current_device
 
 
 def _stream(device=None) -> int:
@@ -149,6 +151,10 @@ def _stream(device=None) -> int:
                                                                   torch.cuda.current_device())
         return _raw_stream(idx)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _addr(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -215,8 +221,8 @@ class NF4Weight:
         return self.absmax is None
 
     def c_view(self) -> Nf4WeightC:
-        key = tuple(t.data_ptr() if t is not None else 0
-                    for t in (self.codes, self.qabsmax, self.s2, self.mean, self.absmax)) + (self.N, self.K)
+        p = _addr
+        key = (p(self.codes), p(self.qabsmax), p(self.s2), p(self.mean), p(self.absmax), self.N, self.K)
         cached = self.__dict__.get("_c_view")
         if cached is None or cached[0] != key:
             cached = (key, Nf4WeightC(_ptr(self.codes), _ptr(self.qabsmax), _ptr(self.s2), _ptr(self.mean),
@@ -488,10 +494,11 @@ def _want(t: torch.Tensor | None, what: str, where: str, shape: tuple, dtype, de
                          f"{what}: a contiguous {dtype} {tuple(shape)} on {device} is wanted, got {got}")
 
 
-def _out(t: torch.Tensor | None, what: str, where: str, shape: tuple, dtype, device) -> torch.Tensor:
-    """An output: the caller's tensor, checked, or a new one."""
+def _out(t: torch.Tensor | None, what: str, where: str, shape: tuple, dtype, device, like=None) -> torch.Tensor:
+    """An output: the caller's tensor, checked, or a new one (`like`: a contiguous
+    tensor of that shape and device, which takes less time to follow)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device) if like is None else torch.empty_like(like, dtype=dtype)
     _want(t, what, where, shape, dtype, device)
     return t
 
@@ -500,7 +507,7 @@ def _on(device, call, *args):
     """The call with the tensors' device current, on that device's current stream."""
     if device.type != "cuda":
         raise QLoraError(-1, "device", f"the tensors are on {device}; a CUDA device is wanted (there is no CPU path)")
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         return call(*args, _stream(device))
     with torch.cuda.device(device):
         return call(*args, _stream(device))
@@ -611,9 +618,9 @@ def linear_bwd_experts(dY: torch.Tensor, X: torch.Tensor, w: NF4Weight, A: torch
     _want(dY, "dY", where, (M, N), torch.bfloat16, dev)
     if sT is not None:
         _want(sT, "sT", where, (M, 2 * r), torch.bfloat16, dev)
-    dX = _out(dX, "dX", where, (M, K), torch.bfloat16, dev)
-    dA = _out(dA, "dA", where, (E * r, K), torch.float32, dev)
-    dB = _out(dB, "dB", where, (E * N, r), torch.float32, dev)
+    dX = _out(dX, "dX", where, (M, K), torch.bfloat16, dev, X)
+    dA = _out(dA, "dA", where, (E * r, K), torch.float32, dev, A)
+    dB = _out(dB, "dB", where, (E * N, r), torch.float32, dev, B)
     ws = _ws_on(lambda: workspace_bytes_experts(OP_BWD, M, N, K, r, E), dev, ws, where)
     v = w.c_view()
     _check(_on(dev, lib().qlora_linear_bwd_experts, dY.data_ptr(), X.data_ptr(), M, ctypes.byref(v), E, offsets.data_ptr(),
