@@ -1518,7 +1518,6 @@ qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_
     a.out_cols = cols;
     a.red = red;
     a.rank_cols = r;
-    a.rank_terms = red < 1024 ? 2 : 1;  // what one term leaves of a short reduction's result (gemm_experts.cu)
     a.rank_x = rank_in;
     a.rank_w = rank_w;
     a.rank_ld = static_cast<int64_t>(terms) * r;

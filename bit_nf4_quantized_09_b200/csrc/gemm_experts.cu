@@ -11,10 +11,11 @@
 // Operands. The weight is the UMMA's M side (256 output columns a tile) and the
 // tokens its N side (a multiple of 16, of 32 on pairs), so a tile costs what its
 // expert's rows cost: an expert with 40 rows runs N = 48. The rank-r term (sT .
-// B_e^T, sU . A_e) is one more reduction step of the same accumulators, its
-// operands loaded by TMA: the bf16 rounding of sT or sU, and on reductions below
-// 1024, where that rounding shows in the result (error 0.0024 instead of 0.0017
-// at K = 64, r = 8), a second step with the rounding of what the first leaves.
+// B_e^T, sU . A_e) is two more reduction steps of the same accumulators, their
+// operands loaded by TMA: the bf16 rounding of sT or sU, then that of what it
+// leaves. How far one rounding shows in the result depends on the adapter's part
+// of it and not on the shapes, so both steps always run (2^-17 of |sT| |B|
+// instead of 2^-9; one step of 66 at K = 4096).
 //
 // Tiles of up to 64 tokens run on single CTAs, two UMMAs of M = 128 at a time.
 // Tiles of up to 256 or 512 tokens run on pairs of CTAs (a cluster of two on
@@ -62,6 +63,7 @@ constexpr int kGroups = 4, kGroupWarps = 4;
 constexpr int kWarpX = 16, kWarpC = 17, kWarpMma = 18;
 constexpr int kThreads = (kWarpMma + 1) * 32;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kRankSteps = 2;  // the first two terms of sT or sU
 
 // Shared memory by token capacity.
 template <int CAP>
@@ -172,8 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     SegIter<> it(sched, ranges, unit, tiles_w);
     Tile tl;
     // steps of a segment: its reduction steps, and the rank-r steps behind a tile's last
-    const int rank_steps = a.rank_terms;
-    auto steps_of = [&](const Tile& s) { return s.k_hi - s.k_lo + (s.k_hi == KT ? rank_steps : 0); };
+    auto steps_of = [&](const Tile& s) { return s.k_hi - s.k_lo + (s.k_hi == KT ? kRankSteps : 0); };
 
     if (warp == kWarpX) {
         // ------------------------------------------- token-tile producer --

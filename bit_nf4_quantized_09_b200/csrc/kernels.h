@@ -302,7 +302,6 @@ struct ExpertGemmArgs {
     int64_t out_cols;     // N (forward) or K (dX)
     int64_t red;          // K (forward) or N (dX)
     int rank_cols;        // r
-    int rank_terms;       // terms of rank_in that are used: 1 or 2
     const uint16_t* rank_x;  // few rows: sT, rows rank_ld apart, and B of every expert
     const uint16_t* rank_w;
     int64_t rank_ld;

@@ -306,10 +306,9 @@ qlora_status qlora_expert_order(const int32_t* ids, int64_t M, int E, int32_t* o
  * in one call; N % 8 == 0). A: bf16 [E r, K] (the A_e stacked); B: bf16 [E N, r];
  * r in {8, 16, 32, 64}. X: bf16 [M, K]; Y, dY: bf16 [M, N]; dX: bf16 [M, K].
  * sT_save (may be NULL): bf16 [M, 2 r]: columns [0, r) the rounding of sT,
- * columns [r, 2 r) that of what it leaves, so that dB keeps fp32 accuracy; the
- * rank-r terms of Y and dX use both where K (N for dX) < 1024 or an expert has a
- * few rows, else the first. The backward takes the forward's
- * sT_save as sT, or NULL to recompute it.
+ * columns [r, 2 r) that of what it leaves, so that dB keeps fp32 accuracy. Y
+ * uses both and dX the first two terms of sU, whatever the batch. The backward
+ * takes the forward's sT_save as sT, or NULL to recompute it.
  * dA: fp32 [E r, K], dB: fp32 [E N, r], overwritten; zeros for an expert
  * without rows. M == 0: the forward is a no-op, the backward writes zeros.
  * The workspace size comes from qlora_workspace_bytes_experts (N, K of one

@@ -212,6 +212,36 @@ def test_rank_r_terms_are_not_rounded_away(q, counts, N, K, r):
                    + acc(N) * (np.abs(dY) @ np.abs(We) + sUa @ np.abs(A)))
 
 
+@pytest.mark.parametrize("counts,N,K,r", [([20, 20], 1096, 2048, 8), ([130, 77], 1024, 1024, 32),
+                                          ([300, 200] * 8, 1032, 1088, 64), ([5, 2], 1024, 1024, 16)])
+def test_strong_adapter_on_long_reductions(q, counts, N, K, r):
+    """sT and sU are 257 and 256 times a power of two by turns (257 does not fit
+    bf16's 8 bits), the adapter's other factor cancels all but their difference,
+    the base weight is zero: every product and sum is exact, and so is the result
+    where two terms of sT and sU reach Y and dX; one term gives zeros."""
+    E, M = len(counts), sum(counts)
+    g = torch.Generator().manual_seed(r)
+    ones = lambda n: torch.stack([torch.randperm(n, generator=g) < 257 - j % 2 for j in range(E * r)]).float()  # noqa: E731
+    power = lambda n: torch.tensor([1.0, -2.0, 0.5, 4.0])[torch.randint(4, (n,), generator=g)]  # noqa: E731
+    sign = torch.tensor([1.0, -1.0] * (r // 2))
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    w = q.quantize_nf4(torch.zeros(E * N, K, device="cuda"))
+    expert = torch.repeat_interleave(torch.arange(E), torch.tensor(counts))
+    bf = lambda t: t.bfloat16().cuda()  # noqa: E731
+    # Y[m, n] = x[m] b[n] (257 - 256) r / 2
+    x, b = power(M), power(E * N)
+    Y, sT = q.linear_fwd_experts(bf(x[:, None].expand(M, K)), w, bf(ones(K)), bf(b[:, None] * sign), off, E, float(r))
+    t = sT.float().cpu()
+    assert torch.equal(t[:, :r] + t[:, r:], x[:, None] * (256.5 + 0.5 * sign))
+    assert torch.equal(Y.float().cpu(), x[:, None] * b.reshape(E, N)[expert] * (r / 2))
+    # dX[m, k] = y[m] a[k] (257 - 256) r / 2
+    y, a = power(M), power(E * K).reshape(E, K)
+    B = ones(N).reshape(E, r, N).transpose(1, 2).reshape(E * N, r)
+    A = (sign[None, :, None] * a[:, None, :]).reshape(E * r, K)
+    dX, _, _ = q.linear_bwd_experts(bf(y[:, None].expand(M, N)), bf(torch.zeros(M, K)), w, bf(A), bf(B), off, E, float(r))
+    assert torch.equal(dX.float().cpu(), y[:, None] * a[expert] * (r / 2))
+
+
 @pytest.mark.parametrize("counts", [[3, 5, 1], [9, 14, 6]], ids=["8", "16"])
 def test_few_rows_do_not_leak(q, counts):
     """As for many rows: NaN and infinities stay in their own rows."""
