@@ -147,12 +147,20 @@ struct TileSched {          // in shared memory, one per CTA
     int base[kMaxExperts + 1];  // token tiles of the experts before e; base[E] = all
 };
 
+// The words that a thread of a grid zeroes: first, first + stride, ... In 64
+// bits: a grid of a CTA per row has more threads than an int counts from 2^23
+// rows on.
+struct ClearShare {
+    int64_t first, stride;
+    __host__ __device__ ClearShare(int cta, int ctas, int thread, int threads)
+        : first(static_cast<int64_t>(cta) * threads + thread), stride(static_cast<int64_t>(ctas) * threads) {}
+};
+
 // CTA `cta` of `ctas` zeroes its share of `words` words: the first kernel of a
 // call clears the status word and the tickets for the kernels behind it.
 __device__ __forceinline__ void clear_words(int* p, int words, int cta, int ctas) {
-    for (int i = cta * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x); i < words;
-         i += ctas * static_cast<int>(blockDim.x))
-        p[i] = 0;
+    const ClearShare s(cta, ctas, static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x));
+    for (int64_t i = s.first; i < words; i += s.stride) p[i] = 0;
 }
 
 // Inclusive scans over a warp.

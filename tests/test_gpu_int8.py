@@ -199,3 +199,19 @@ def test_train_merge_and_serve_a_layer_of_experts(q):
     back = torch.empty_like(Y8)
     back[order.long()] = Y8
     assert torch.equal(back.reshape(T, 2, N)[0, 0], Y8[(order == 0).nonzero()[0, 0]])
+
+
+def test_more_rows_than_an_int_counts_threads(q):
+    """A CTA of 128 threads per row: 2^24 rows and some have more than 2^31
+    threads."""
+    M, N, K = (1 << 24) + 137, 8, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    X = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    W = torch.randn(N, K, generator=g, device="cuda") * 0.02
+    w, rows8 = q.quantize_int8(W), q.quantize_int8(X)
+    Y = q.linear_int8(X, w)
+    for m in (slice(0, 1 << 20), slice((1 << 23) - 300, (1 << 23) + 300), slice((1 << 24) - 300, M)):
+        x = X[m].cpu()
+        codes, scale = quantised(x)
+        assert torch.equal(rows8.codes[m].cpu(), codes) and torch.equal(rows8.scale[m].cpu(), scale)
+        assert torch.equal(Y[m].cpu(), product(x, *quantised(W.cpu())))
