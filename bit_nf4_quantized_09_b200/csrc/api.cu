@@ -1422,9 +1422,12 @@ size_t plan_bound(int64_t M, int E, int64_t cols) {
            up256(static_cast<size_t>(2 * kPlanSms) * std::min<int64_t>(std::max<int64_t>(M, 16), 64) * 256 * 4);
 }
 
-// M rows over E experts: 32-bit row numbers and tile numbers.
+// M rows over E experts, `cols` rows or columns of an expert's weight, whichever
+// are more: the kernels hold row, column and tile numbers in 32 bits, and step
+// past the last by up to a tile.
 bool rows_ok(int64_t M, int E, int64_t cols) {
-    return M <= (int64_t(1) << 30) && (M / 64 + E) * cdiv(cols, 256) < (int64_t(1) << 31);
+    constexpr int64_t kMost = int64_t(1) << 30;
+    return M <= kMost && cols <= kMost && (M / 64 + E) * cdiv(cols, 256) < (int64_t(1) << 31);
 }
 
 // Block numbers of a stacked weight are 32 bits (137 GB of codes).

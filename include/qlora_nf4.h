@@ -285,7 +285,8 @@ qlora_status qlora_linear_bwd_group(const uint16_t* dY, const uint16_t* X, int64
  * there they are clamped to [0, M] and to their running maximum. Rows before
  * offsets[0] and from offsets[E] on belong to no expert: their outputs (Y, sT,
  * dX) are left as they were, and whatever their inputs hold reaches no result.
- * 1 <= E <= 512. */
+ * 1 <= E <= 512; M, and the rows and columns of one expert's weight, at most
+ * 2^30. */
 
 /* Row order of a batch by expert id: a stable counting sort.
  *   order[j]: the row at place j when rows stand by id, rows of one id in their

@@ -194,3 +194,33 @@ def test_expert_weight_views(q):
     for bad in ((stack(128, 64, True), 1, 2), (w, 2, 2), (w, -1, 2), (w, 0, 3)):
         with pytest.raises(q.QLoraError):
             q.expert_weight(*bad)
+
+
+@pytest.mark.parametrize("N,K", [((1 << 30) + 8, 64), (1 << 31, 64), ((1 << 32) - 8, 64), (8, (1 << 30) + 64),
+                                 (8, 1 << 31), (64, 1 << 32)])
+def test_more_columns_than_32_bit_numbers_hold(q, N, K):
+    """Rows and columns of an expert are 32-bit numbers in the kernels, with room for
+    a tile behind the last: wider weights are refused before anything runs."""
+    L = q.lib()
+    w = weight(q, N=N, K=K)
+    for op in (q.OP_FWD, q.OP_BWD):
+        assert q.workspace_bytes_experts(op, 4, N, K, 16, 1) == 0
+    big = 1 << 62
+    q.set_option(q.OPT_FAIL_LAUNCHES, 3)                 # nothing reaches a GPU where it is accepted
+    try:
+        assert L.qlora_linear_fwd_experts(P, 4, ctypes.byref(w), 1, P, P, P, 16, 16.0, P, None, P, big, None) == -2
+        assert L.qlora_linear_bwd_experts(P, P, 4, ctypes.byref(w), 1, P, P, P, 16, 16.0, P, P, P, P, P, big, None) == -2
+        if K <= 131072:
+            w8 = q.Int8WeightC(P, P, N, K)
+            assert L.qlora_linear_int8(P, 4, ctypes.byref(w8), P, P, big, None) == -2
+            assert L.qlora_linear_int8_experts(P, 4, ctypes.byref(w8), 1, P, P, P, big, None) == -2
+            assert q.workspace_bytes_int8(4, N, K) == 0
+    finally:
+        q.set_option(q.OPT_FAIL_LAUNCHES, 0)
+
+
+def test_widest_weights_are_accepted(q):
+    for N, K in ((1 << 30, 64), (8, 1 << 30)):
+        assert q.workspace_bytes_experts(q.OP_FWD, 4, N, K, 16, 1) > 0
+        assert q.workspace_bytes_experts(q.OP_BWD, 4, N, K, 16, 1) > 0
+    assert q.workspace_bytes_int8(4, 1 << 30, 64) > 0
