@@ -1567,6 +1567,7 @@ qlora_status expert_matmul(bool dx, const uint16_t* act, int64_t M, const qlora_
 }
 
 constexpr int64_t kInt8MaxK = 131072;  // 127 * 127 * K < 2^31
+constexpr int64_t kInt8MaxQuantisedK = int64_t(1) << 33;
 
 qlora_status check_int8_weight(const qlora_int8_weight* w) {
     if (!w || !w->codes || !w->scale) return QLORA_ERR_INVALID_ARG;
@@ -1642,7 +1643,8 @@ qlora_status int8_impl(const uint16_t* X, int64_t M, const qlora_int8_weight* w,
 qlora_status quantize_int8_any(const void* W, bool bf16, int64_t N, int64_t K, int8_t* codes, float* scale,
                                void* stream) {
     if (!W || !codes || !scale) return QLORA_ERR_INVALID_ARG;
-    if (N <= 0 || K <= 0 || K % 16 != 0 || N > 0x7FFFFFFF) return QLORA_ERR_BAD_SHAPE;
+    // rows are CTAs; a row's vectors of eight have 32-bit numbers
+    if (N <= 0 || K <= 0 || K % 16 != 0 || N > 0x7FFFFFFF || K > kInt8MaxQuantisedK) return QLORA_ERR_BAD_SHAPE;
     if (!aligned16(W) || !aligned16(codes) || !aligned16(scale)) return QLORA_ERR_MISALIGNED;
     if (injected_failure()) return QLORA_ERR_CUDA;
     const qlora_status s = device_ready(nullptr);

@@ -335,7 +335,8 @@ typedef struct {
     int64_t       K;
 } qlora_int8_weight;
 
-/* Quantise the rows of W (fp32 or bf16 [N, K], device; K % 16 == 0) to 8 bits:
+/* Quantise the rows of W (fp32 or bf16 [N, K], device; N < 2^31, K % 16 == 0,
+ * K <= 2^33) to 8 bits:
  *   scale[n] = fp32( a / 127 ),  codes[n, k] = 127 W[n, k] / a  rounded to the
  * nearest integer, halves to even (of the exact quotient), a = max_k |W[n, k]|.
  * A row of zeros has scale 0 and codes 0; a row that holds a NaN or an infinity

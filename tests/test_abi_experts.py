@@ -224,3 +224,15 @@ def test_widest_weights_are_accepted(q):
         assert q.workspace_bytes_experts(q.OP_FWD, 4, N, K, 16, 1) > 0
         assert q.workspace_bytes_experts(q.OP_BWD, 4, N, K, 16, 1) > 0
     assert q.workspace_bytes_int8(4, 1 << 30, 64) > 0
+
+
+def test_quantiser_refuses_rows_it_cannot_number(q):
+    """The quantiser numbers a row's vectors of eight in 32 bits: 2^33 columns."""
+    L = q.lib()
+    for entry in (L.qlora_quantize_int8, L.qlora_quantize_int8_bf16):
+        for K, want in ((1 << 33, -6), ((1 << 33) + 16, -2), (1 << 34, -2), (1 << 40, -2)):
+            q.set_option(q.OPT_FAIL_LAUNCHES, 1)
+            try:
+                assert entry(P, 1, K, P, P, None) == want, K
+            finally:
+                q.set_option(q.OPT_FAIL_LAUNCHES, 0)
