@@ -7,8 +7,10 @@
 // qw, ws: the weight's (one scale per output channel). This is how the 16-bit
 // weight an adapter was merged into is served in fewer bits ("ta-paperlens
 // QLoRA explainer", 落とし穴: merging into the 4-bit weight loses the update).
-// The int32 sums are exact (K <= 131072 keeps |sum| < 2^31); the only
-// roundings are the scales' product, one fp32 product and the bf16 result.
+// The int32 sums are exact (K <= 131072 keeps |sum| < 2^31); the roundings are
+// the sum's to fp32 (none below 2^24), the scales' product, its product with the
+// sum and the bf16 result. Where the scales' product is no normal fp32 number the
+// sum is multiplied by one scale after the other (`scaled`).
 //
 // The weight is the UMMA's M side (256 channels a tile), the tokens its N side,
 // as in the NF4 expert matmul, so ragged experts and single tokens pay for the
@@ -85,6 +87,20 @@ __device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t a_desc, u
 // accumulator (format 2), both K-major, dense, wrapping.
 __device__ __forceinline__ uint32_t idesc_i8(int M, int N) {
     return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// s xs ws, by the scales' product. Where that underflows or overflows, by one
+// scale after the other: s xs loses nothing in fp32's subnormals (s is an integer),
+// and cannot overflow where xs ws underflows (|s| < 2^31, ws >= 2^-149), so only
+// results that leave fp32's range themselves do so, and a sum of zero stays zero.
+__device__ __forceinline__ float scaled(float s, float xs, float ws) {
+    const float p = xs * ws;
+    const bool one = (fabsf(p) < 1.17549435e-38f && xs != 0.0f && ws != 0.0f) || fabsf(p) > 3.40282347e+38f;
+    return s * (one ? xs : p) * (one ? ws : 1.0f);
+}
+// A scale whose product with another such one is normal or zero (or NaN, which stays so).
+__device__ __forceinline__ bool middling(float v) {
+    return v == 0.0f || !(fabsf(v) < 1.08420217e-19f || fabsf(v) > 9.22337204e+18f);  // 2^-63, 2^63
 }
 
 template <int CAP>
@@ -260,10 +276,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         int n = 0;
         while (ok && it.next(tl)) {
-            if (static_cast<int>(threadIdx.x) < tl.rows) xs_s[threadIdx.x] = __ldcg(a.xs + tl.row0 + threadIdx.x);
+            float x = 0.0f;
+            if (static_cast<int>(threadIdx.x) < tl.rows) xs_s[threadIdx.x] = x = __ldcg(a.xs + tl.row0 + threadIdx.x);
             const int64_t wrow = static_cast<int64_t>(tl.e) * a.N;
             const float ws = __ldg(a.ws + wrow + min(tl.w0 + nl, static_cast<int>(a.N) - 1));
-            ok = all_ok(ok, kEpiWarps * 32);
+            // whether every product of two of the tile's scales may be made first
+            const bool plain = all_ok(middling(x) && middling(ws), kEpiWarps * 32);
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc, static_cast<uint32_t>(n) & 1u, tmo, a.status)) && ok;
             tc_fence_after();
             const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * 256;
@@ -281,10 +299,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t r[32];
                         tmem_ld32(trow + c, r);
                         tmem_ld_wait();
+                        const float* xs = xs_s + tok0 + c;
+                        if (plain) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                r[i] = __float_as_uint(__int2float_rn(static_cast<int>(r[i])) * (xs[i] * ws));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                r[i] = __float_as_uint(scaled(__int2float_rn(static_cast<int>(r[i])), xs[i], ws));
+                        }
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            const float y0 = __int2float_rn(static_cast<int>(r[i])) * (xs_s[tok0 + c + i] * ws);
-                            const float y1 = __int2float_rn(static_cast<int>(r[i + 1])) * (xs_s[tok0 + c + i + 1] * ws);
+                            const float y0 = __uint_as_float(r[i]), y1 = __uint_as_float(r[i + 1]);
                             const float got = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? y0 : y1, 1);
                             y[k][i / 2] = (lane & 1) ? pack_bf16x2(got, y1) : pack_bf16x2(y0, got);
                         }
@@ -327,8 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (threadIdx.x == 0) pending->push(tl);
             }
             ++n;
-            // the warps leave together (they meet at barriers); this one also
-            // ends the reads of this tile's token scales
+            // the warps leave together (they meet at barriers), `ok` is the same for
+            // all from here to the next wait; this one also ends the reads of this
+            // tile's token scales
             ok = all_ok(ok, kEpiWarps * 32);
         }
         // the tiles shared with other CTAs: their last CTA to come here finishes them
@@ -351,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                   __ldg(ws + nc + 3));
                                     const float x = __ldcg(a.xs + p.row0 + tok);
                                     *reinterpret_cast<uint2*>(out + tok * a.N + nc) =
-                                        make_uint2(pack_bf16x2(__int2float_rn(v.x) * (x * w4.x), __int2float_rn(v.y) * (x * w4.y)),
-                                                   pack_bf16x2(__int2float_rn(v.z) * (x * w4.z), __int2float_rn(v.w) * (x * w4.w)));
+                                        make_uint2(pack_bf16x2(scaled(__int2float_rn(v.x), x, w4.x), scaled(__int2float_rn(v.y), x, w4.y)),
+                                                   pack_bf16x2(scaled(__int2float_rn(v.z), x, w4.z), scaled(__int2float_rn(v.w), x, w4.w)));
                                 });
             }
         }

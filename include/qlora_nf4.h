@@ -347,7 +347,8 @@ qlora_status qlora_quantize_int8_bf16(const uint16_t* W, int64_t N, int64_t K, i
 
 /* Y = bf16( xs[m] scale[n] sum_k qx[m, k] codes[n, k] ), qx and xs the rows of X
  * (bf16 [M, K]) quantised as above, one scale per token; the integer sums are
- * exact. A token row with a NaN or an infinity gives a NaN row of Y and touches
+ * exact, and only a result outside fp32's range underflows or overflows, whatever
+ * the two scales' product does. A token row with a NaN or an infinity gives a NaN row of Y and touches
  * no other. qlora_linear_int8_experts: w stacks the weights of E experts (E N
  * rows, N % 8 == 0), rows of X and Y grouped by offsets as above; rows of no
  * expert are left as they were. Workspace: qlora_workspace_bytes_int8 (N, K of

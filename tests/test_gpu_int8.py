@@ -215,3 +215,41 @@ def test_more_rows_than_an_int_counts_threads(q):
         codes, scale = quantised(x)
         assert torch.equal(rows8.codes[m].cpu(), codes) and torch.equal(rows8.scale[m].cpu(), scale)
         assert torch.equal(Y[m].cpu(), product(x, *quantised(W.cpu())))
+
+
+@pytest.mark.parametrize("counts,N,K", [([9], 8, 4096), ([40], 520, 512), ([90] * 6, 5000, 336), ([1000], 12808, 256)],
+                         ids=["shared_64", "tiles_of_64", "tiles_of_256", "tiles_of_512"])
+def test_scales_whose_product_is_no_normal_number(q, counts, N, K):
+    """Tiny and huge rows on both sides: xs ws leaves fp32's normal range where the
+    sum times both does not, and a sum of zero stays zero. Where the product is
+    normal the bits are those of the definition; elsewhere the sum's rounding and
+    two products (2^-24 each) and the bf16 result (2^-8), or half of the least
+    bf16 step, 2^-134, and overflow to infinity."""
+    E, M = len(counts), sum(counts)
+    X, W = rows(M, K, M + 3), rows(E * N, K, N + 4, torch.float32)
+    X[0::7] *= 2.0 ** -76
+    W[0::5] *= 2.0 ** -70
+    X[1::7] *= 2.0 ** 76
+    W[1::5] *= 2.0 ** 70
+    X[1::7] = X[1, :1].abs()                     # equal tokens against alternating signs: sums of zero
+    W[1::5] = W[1, :1].abs() * (1 - 2.0 * (torch.arange(K) % 2))
+    w = q.quantize_int8(W.cuda())
+    off = np.concatenate([[0], np.cumsum(counts)])
+    Y = q.linear_int8(X.cuda(), w) if E == 1 else q.linear_int8_experts(
+        X.cuda(), w, torch.tensor(off, dtype=torch.int32, device="cuda"), E)
+    codes, scale = quantised(W)
+    odd = 0
+    for e in range(E):
+        m, n = slice(off[e], off[e + 1]), slice(e * N, (e + 1) * N)
+        qx, xs = quantised(X[m])
+        s, p = qx.double() @ codes[n].double().t(), xs[:, None] * scale[n][None]
+        normal = (p >= 2.0 ** -126) & torch.isfinite(p)
+        got = Y[m].cpu()
+        assert torch.equal(got[normal], product(X[m], codes[n], scale[n])[normal]), e
+        ref = s * xs.double()[:, None] * scale[n].double()[None]
+        big = ref.abs() >= 3.4e38                # above the largest bf16 number, 3.39e38
+        assert torch.equal(got[~normal & big].double(), ref[~normal & big].sign() * float("inf")), e
+        ok = (got.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -22) * ref.abs() + 2.0 ** -134
+        assert ok[~normal & ~big].all(), (e, int((~ok & ~normal & ~big).sum()))
+        odd += int((~normal).sum())
+    assert odd > 0
