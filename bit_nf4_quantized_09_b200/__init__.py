@@ -643,7 +643,8 @@ class Int8Weight:
     def c_view(self) -> Int8WeightC:
         key = (self.codes.data_ptr(), self.scale.data_ptr(), self.N, self.K)
         cached = self.__dict__.get("_c_view")
-        if cached is None or cached[0] != key:
+        # (a tensor put in another's place at the same address has to be contiguous too)
+        if cached is None or cached[0] != key or not (self.codes.is_contiguous() and self.scale.is_contiguous()):
             _want(self.codes, "codes", "Int8Weight", (self.N, self.K), torch.int8, self.codes.device)
             _want(self.scale, "scale", "Int8Weight", (self.N,), torch.float32, self.codes.device)
             cached = (key, Int8WeightC(_ptr(self.codes), _ptr(self.scale), self.N, self.K))

@@ -236,3 +236,19 @@ def test_quantiser_refuses_rows_it_cannot_number(q):
                 assert entry(P, 1, K, P, P, None) == want, K
             finally:
                 q.set_option(q.OPT_FAIL_LAUNCHES, 0)
+
+
+def test_int8_weight_checks_replaced_tensors(q):
+    """A weight keeps its C view while its tensors stay where they are; a tensor
+    put in one's place at the same address, but strided, is refused as it is at
+    the first call."""
+    w8 = q.Int8Weight(torch.zeros(64, 64, dtype=torch.int8), torch.zeros(64), 64, 64)
+    first = w8.c_view()
+    assert w8.c_view() is first
+    w8.codes = w8.codes.t()
+    with pytest.raises(q.QLoraError):
+        w8.c_view()
+    w8.codes = w8.codes.t()
+    w8.scale = torch.as_strided(w8.scale, (64,), (0,))
+    with pytest.raises(q.QLoraError):
+        w8.c_view()
