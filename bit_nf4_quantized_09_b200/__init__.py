@@ -569,8 +569,29 @@ def workspace_bytes_experts(op: int, M: int, N: int, K: int, r: int, E: int) -> 
     return int(lib().qlora_workspace_bytes_experts(op, M, N, K, r, E))
 
 
+def _stack_view(w: NF4Weight, where: str, dev) -> Nf4WeightC:
+    """The C view of a stacked weight whose parts have the sizes, types and device
+    that the kernels read (looked at once for a view)."""
+    v = w.c_view()
+    seen = w.__dict__.get("_checked")
+    if seen is None or seen[0] is not v or seen[1] != dev:
+        nb = w.N * w.K // 64
+        parts = [("codes", w.codes, nb * 32, torch.uint8)]
+        if w.double_quant:
+            parts += [("qabsmax", w.qabsmax, nb, torch.uint8), ("s2", w.s2, -(-nb // 256), torch.float32),
+                      ("mean", w.mean, 1, torch.float32)]
+        else:
+            parts.append(("absmax", w.absmax, nb, torch.float32))
+        for what, t, n, dtype in parts:
+            if t is None or t.dtype is not dtype or t.device != dev or t.numel() < n:
+                got = "None" if t is None else f"{t.numel()} of {t.dtype} on {t.device}"
+                raise QLoraError(-1, where, f"the weight's {what}: {n} of {dtype} on {dev} are wanted, got {got}")
+        w.__dict__["_checked"] = (v, dev)
+    return v
+
+
 def _expert_shapes(where, X, w, A, B, offsets, E):
-    """(M, N, K, r, device) of an expert call, its inputs checked."""
+    """(M, N, K, r, device, C view of the weight) of an expert call, its inputs checked."""
     dev = X.device
     if X.dim() != 2 or A.dim() != 2 or not 1 <= E <= 512 or w.N % E or A.shape[0] % E:
         raise QLoraError(-2, where, f"X {tuple(X.shape)}, A {tuple(A.shape)}, weight {w.N} x {w.K}, E = {E}")
@@ -579,9 +600,7 @@ def _expert_shapes(where, X, w, A, B, offsets, E):
     _want(A, "A", where, (E * r, K), torch.bfloat16, dev)
     _want(B, "B", where, (E * N, r), torch.bfloat16, dev)
     _want(offsets, "offsets", where, (E + 1,), torch.int32, dev)
-    if w.codes.device != dev:
-        raise QLoraError(-1, where, f"the weight is on {w.codes.device}, X on {dev}")
-    return M, N, K, r, dev
+    return M, N, K, r, dev, _stack_view(w, where, dev)
 
 
 def linear_fwd_experts(X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, E: int,
@@ -593,12 +612,11 @@ def linear_fwd_experts(X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: torch.
     sT: bf16 [M, 2 r], a sum of two terms. Rows of no expert keep what Y and sT
     held (a Y or sT allocated here holds nothing there)."""
     where = "qlora_linear_fwd_experts"
-    M, N, K, r, dev = _expert_shapes(where, X, w, A, B, offsets, E)
+    M, N, K, r, dev, v = _expert_shapes(where, X, w, A, B, offsets, E)
     Y = _out(Y, "Y", where, (M, N), torch.bfloat16, dev)
     if save_sT:
         sT = _out(sT, "sT", where, (M, 2 * r), torch.bfloat16, dev)
     ws = _ws_on(lambda: workspace_bytes_experts(OP_FWD, M, N, K, r, E), dev, ws, where)
-    v = w.c_view()
     _check(_on(dev, lib().qlora_linear_fwd_experts, X.data_ptr(), M, ctypes.byref(v), E, offsets.data_ptr(), A.data_ptr(),
                B.data_ptr(), r, float(alpha), Y.data_ptr(), sT.data_ptr() if save_sT else None, ws.data_ptr(), ws.numel()),
            where)
@@ -614,7 +632,7 @@ def linear_bwd_experts(dY: torch.Tensor, X: torch.Tensor, w: NF4Weight, A: torch
     sT as it returned it, or None to recompute it. An expert without rows gets
     zero gradients; rows of no expert keep what dX held."""
     where = "qlora_linear_bwd_experts"
-    M, N, K, r, dev = _expert_shapes(where, X, w, A, B, offsets, E)
+    M, N, K, r, dev, v = _expert_shapes(where, X, w, A, B, offsets, E)
     _want(dY, "dY", where, (M, N), torch.bfloat16, dev)
     if sT is not None:
         _want(sT, "sT", where, (M, 2 * r), torch.bfloat16, dev)
@@ -622,7 +640,6 @@ def linear_bwd_experts(dY: torch.Tensor, X: torch.Tensor, w: NF4Weight, A: torch
     dA = _out(dA, "dA", where, (E * r, K), torch.float32, dev, A)
     dB = _out(dB, "dB", where, (E * N, r), torch.float32, dev, B)
     ws = _ws_on(lambda: workspace_bytes_experts(OP_BWD, M, N, K, r, E), dev, ws, where)
-    v = w.c_view()
     _check(_on(dev, lib().qlora_linear_bwd_experts, dY.data_ptr(), X.data_ptr(), M, ctypes.byref(v), E, offsets.data_ptr(),
                A.data_ptr(), B.data_ptr(), r, float(alpha), None if sT is None else sT.data_ptr(), dX.data_ptr(),
                dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), ws.numel()), where)

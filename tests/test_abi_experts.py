@@ -252,3 +252,23 @@ def test_int8_weight_checks_replaced_tensors(q):
     w8.scale = torch.as_strided(w8.scale, (64,), (0,))
     with pytest.raises(q.QLoraError):
         w8.c_view()
+
+
+@pytest.mark.parametrize("part,value,what", [
+    ("codes", torch.zeros(64 * 64 - 1, dtype=torch.uint8), "codes"), ("qabsmax", torch.zeros(127, dtype=torch.uint8), "qabsmax"),
+    ("s2", torch.zeros(0), "s2"), ("mean", torch.zeros(1, dtype=torch.float64), "mean"),
+    ("s2", torch.zeros(1, device="meta"), "s2"), ("absmax", torch.zeros(127), "absmax")])
+def test_parts_of_a_stacked_weight_are_checked(q, part, value, what):
+    """A part that is too small, of another type or on another device would be read
+    out of range by the kernels."""
+    E, N, K, r, M = 2, 64, 64, 8, 5
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    parts = dict(codes=torch.zeros(E * N * K // 2, dtype=torch.uint8), qabsmax=torch.zeros(E * N, dtype=torch.uint8),
+                 s2=torch.zeros(1), mean=torch.zeros(1), absmax=None)
+    if part == "absmax":
+        parts |= dict(qabsmax=None, s2=None, mean=None)
+    w = q.NF4Weight(N=E * N, K=K, **{**parts, part: value})
+    with pytest.raises(q.QLoraError, match=f"weight's {what}"):
+        q.linear_fwd_experts(bf(M, K), w, bf(E * r, K), bf(E * N, r), torch.zeros(E + 1, dtype=torch.int32), E, 16.0)
+    with pytest.raises(q.QLoraError, match=f"weight's {what}"):
+        q.linear_bwd_experts(bf(M, N), bf(M, K), w, bf(E * r, K), bf(E * N, r), torch.zeros(E + 1, dtype=torch.int32), E, 16.0)
