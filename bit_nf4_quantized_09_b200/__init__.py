@@ -81,6 +81,8 @@ _SIGNATURES = {
     "qlora_quantize_int8": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "qlora_quantize_int8_bf16": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "qlora_workspace_bytes_int8": (_sz, [_i64, _i64, _i64, _int]),
+    "qlora_tile_rows_experts": (_int, [_int, _i64, _i64, _i64, _int]),
+    "qlora_tile_rows_int8": (_int, [_i64, _i64, _i64, _int]),
     "qlora_linear_int8": (_int, [_vp, _i64, _w8p, _vp, _vp, _sz, _vp]),
     "qlora_linear_int8_experts": (_int, [_vp, _i64, _w8p, _int, _vp, _vp, _vp, _sz, _vp]),
     "qlora_nf4_tables": (_int, [ctypes.POINTER(_f32), ctypes.POINTER(_f32)]),
@@ -569,6 +571,12 @@ def workspace_bytes_experts(op: int, M: int, N: int, K: int, r: int, E: int) -> 
     return int(lib().qlora_workspace_bytes_experts(op, M, N, K, r, E))
 
 
+def tile_rows_experts(op: int, M: int, N: int, K: int, E: int) -> int:
+    """The most rows of a tile that these sizes choose in an expert call (8, 16, 64, 256
+    or 512; N and K are one expert's), 0 for refused sizes: a diagnostic for tests."""
+    return int(lib().qlora_tile_rows_experts(op, M, N, K, E))
+
+
 def _stack_view(w: NF4Weight, where: str, dev) -> Nf4WeightC:
     """The C view of a stacked weight whose parts have the sizes, types and device
     that the kernels read (looked at once for a view)."""
@@ -689,6 +697,11 @@ def quantize_int8(W: torch.Tensor, out: Int8Weight | None = None) -> Int8Weight:
 def workspace_bytes_int8(M: int, N: int, K: int, E: int = 1) -> int:
     """Workspace of linear_int8 (E = 1) and linear_int8_experts; N and K are one expert's."""
     return int(lib().qlora_workspace_bytes_int8(M, N, K, E))
+
+
+def tile_rows_int8(M: int, N: int, K: int, E: int = 1) -> int:
+    """As tile_rows_experts, of linear_int8 (E = 1) and linear_int8_experts: 64, 256 or 512."""
+    return int(lib().qlora_tile_rows_int8(M, N, K, E))
 
 
 def _int8_call(where, X, w, E, Y, ws, *group):

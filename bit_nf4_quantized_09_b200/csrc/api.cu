@@ -1794,6 +1794,14 @@ size_t qlora_workspace_bytes_int8(int64_t M, int64_t N, int64_t K, int E) {
     return int8_layout(M, N, K, E).total;
 }
 
+int qlora_tile_rows_experts(int op, int64_t M, int64_t N, int64_t K, int E) {
+    return M > 0 && qlora_workspace_bytes_experts(op, M, N, K, 8, E) > 0 ? expert_layout(op, M, N, K, 8, E).plan.cap : 0;
+}
+
+int qlora_tile_rows_int8(int64_t M, int64_t N, int64_t K, int E) {
+    return M > 0 && qlora_workspace_bytes_int8(M, N, K, E) > 0 ? int8_layout(M, N, K, E).plan.cap : 0;
+}
+
 qlora_status qlora_linear_int8(const uint16_t* X, int64_t M, const qlora_int8_weight* w, uint16_t* Y, void* ws,
                                size_t ws_bytes, void* stream) {
     const qlora_status s = check_int8_weight(w);

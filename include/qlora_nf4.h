@@ -360,6 +360,14 @@ qlora_status qlora_linear_int8(const uint16_t* X, int64_t M, const qlora_int8_we
 qlora_status qlora_linear_int8_experts(const uint16_t* X, int64_t M, const qlora_int8_weight* w, int E,
                                        const int32_t* offsets, uint16_t* Y, void* ws, size_t ws_bytes, void* stream);
 
+/* The most token rows of a tile in the calls grouped by expert, as these sizes
+ * choose it (a diagnostic: tests assert with it which kernel a case reaches). Experts:
+ * 8 or 16 (forward, registers of mma.sync), 64 (single CTAs, tiles may be shared
+ * out), 256 or 512 (pairs of CTAs). 8-bit: 64, 256 (single CTAs), 512 (pairs). 0 for
+ * sizes that the calls refuse. */
+int qlora_tile_rows_experts(int op, int64_t M, int64_t N, int64_t K, int E);
+int qlora_tile_rows_int8(int64_t M, int64_t N, int64_t K, int E);
+
 /* Host copies of the library's own NF4 tables: levels[16] (fp32, ascending)
  * and thresholds[15] (the fp32 decision points between neighbouring levels).
  * Computed on the host at load time, independently of any test code. */

@@ -55,6 +55,22 @@ def test_workspaces_of_large_batches_serve_small_ones(q, N, K, r, E):
         assert got == [-6, -6, -6], (M, got)
 
 
+def test_tile_rows(q):
+    """Plans on both sides of the rules' borders, as measured in their comments, and 0
+    for what the calls refuse."""
+    f = lambda M, op=q.OP_FWD: q.tile_rows_experts(op, M, 4096, 4096, 8)  # noqa: E731
+    assert [f(48), f(49), f(96), f(97), f(320)] == [8, 16, 16, 64, 64]
+    assert f(600) in (64, 256) and f(1024) == 256 and f(4096) == 512
+    assert f(48, q.OP_BWD) == 64
+    assert q.tile_rows_int8(600, 4096, 4096, 8) == 256 and q.tile_rows_int8(64, 4096, 4096, 8) == 64
+    assert q.tile_rows_int8(200, 11008, 4096) == 512 and q.tile_rows_int8(1, 22016, 8192) == 64
+    for bad in ((q.OP_QUANTIZE, 9, 512, 512, 4), (q.OP_FWD, 0, 512, 512, 4), (q.OP_FWD, 9, 12, 512, 4), (q.OP_BWD, 9, 512, 500, 4),
+                (q.OP_FWD, 9, 512, 512, 0), (q.OP_FWD, 1 << 31, 512, 512, 4)):
+        assert q.tile_rows_experts(*bad) == 0, bad
+    for bad in ((0, 512, 512, 1), (9, 12, 512, 1), (9, 512, 520, 1), (9, 512, 512, 513)):
+        assert q.tile_rows_int8(*bad) == 0, bad
+
+
 def test_forward_and_backward_refusals(q):
     L = q.lib()
     ws = q.workspace_bytes_experts(q.OP_FWD, 64, 512, 512, 16, 4)

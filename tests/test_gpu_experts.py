@@ -188,6 +188,36 @@ def test_pairs_against_fp64(q, name):
         assert torch.equal(a[k], b[k]), k
 
 
+# every instantiation of the matmul, by the tile rows that the sizes choose for the
+# forward and for dX: both storages, tiles of 64 whole, shared out and both in one call
+TILES = {
+    "64_shared": (64, 256, dict(counts=[33, 64, 17], N=264, K=960, r=16)),
+    "64_shared_fp32": (64, 256, dict(counts=[33, 64, 17], N=264, K=960, r=8, dq=False, lead=2)),
+    "64_whole_and_shared": (64, 64, dict(counts=[14] * 60 + [1, 27] * 8, N=264, K=1088, r=16)),
+    "64_whole_and_shared_fp32": (64, 64, dict(counts=[14] * 60 + [1, 27] * 8, N=264, K=1088, r=32, dq=False)),
+    "512_and_64_shared": (512, 64, dict(counts=[200, 100, 350, 1], N=8008, K=1024, r=8)),
+    "512_and_64_shared_fp32": (512, 64, dict(counts=[200, 100, 350, 1], N=8008, K=1024, r=64, dq=False)),
+    "64_and_512": (64, 512, dict(counts=[600, 290, 31], N=520, K=20032, r=16, pad=2)),
+    "64_and_512_fp32": (64, 512, dict(counts=[600, 290, 31], N=520, K=20032, r=32, dq=False)),
+    "512_both": (512, 512, dict(counts=[513, 300, 257, 1, 0, 1024, 512, 290, 31], N=1032, K=1088, r=64)),
+    "256_both": (256, 256, dict(counts=[600, 290, 31], N=2440, K=2112, r=8)),
+    "256_both_fp32": (256, 256, dict(counts=[600, 290, 31], N=2440, K=2112, r=16, dq=False)),
+}
+
+
+@pytest.mark.parametrize("name", TILES)
+def test_tiles_against_fp64(q, name):
+    fwd, dx, sizes = TILES[name]
+    t = case(**sizes)
+    assert q.tile_rows_experts(q.OP_FWD, t["M"], t["N"], t["K"], t["E"]) == fwd
+    assert q.tile_rows_experts(q.OP_BWD, t["M"], t["N"], t["K"], t["E"]) == dx
+    a = run(q, t)
+    compare(t, a)
+    b = run(q, t)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+
+
 @pytest.mark.parametrize("counts,N,K,r", [([5, 2], 136, 64, 8), ([40, 30], 264, 128, 16), ([300, 200], 520, 960, 32),
                                           ([700, 513], 392, 64, 64), ([3, 9], 264, 2048, 64)])
 def test_rank_r_terms_are_not_rounded_away(q, counts, N, K, r):

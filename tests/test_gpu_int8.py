@@ -201,6 +201,42 @@ def test_train_merge_and_serve_a_layer_of_experts(q):
     assert torch.equal(back.reshape(T, 2, N)[0, 0], Y8[(order == 0).nonzero()[0, 0]])
 
 
+@pytest.mark.parametrize("tile,counts,N,K", [
+    (64, [64, 64, 64], 264, 8208), (64, [20] * 75, 520, 1040), (64, [16, 17, 64, 65, 256, 257, 300, 1], 2056, 4112),
+    (256, [90] * 6, 5000, 336), (256, [16, 17, 64, 65, 256, 257, 300, 1], 4104, 336), (256, [48, 15, 160, 129, 0, 256], 10248, 336),
+    (512, [512, 513, 100, 257], 12808, 208), (512, [288, 289, 320, 31], 12808, 336)])
+def test_tiles_bit_exact(q, tile, counts, N, K):
+    """Every tile size, with counts around the granularities of its tokens, a weight
+    tile that N ends in and a reduction that is no whole number of steps; rows of
+    nobody on both sides."""
+    E, M = len(counts), sum(counts) + 5
+    assert q.tile_rows_int8(M, N, K, E) == tile
+    X, W = rows(M, K, M), rows(E * N, K, N, torch.float32, 0.02)
+    X[:2], X[M - 3:] = float("nan"), float("inf")
+    off = np.concatenate([[0], np.cumsum(counts)]) + 2
+    w = q.quantize_int8(W.cuda())
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    Y = [torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for y in Y:
+        q.linear_int8_experts(X.cuda(), w, offsets, E, Y=y)
+    codes, scale = quantised(W)
+    ref = torch.full((M, N), 7.0, dtype=torch.bfloat16)
+    for e in range(E):
+        m, n = slice(off[e], off[e + 1]), slice(e * N, (e + 1) * N)
+        ref[m] = product(X[m], codes[n], scale[n])
+    for y in Y:
+        assert torch.equal(y.cpu(), ref)
+
+
+@pytest.mark.parametrize("tile,M,N,K", [(64, 100, 1000, 336), (256, 200, 40000, 144), (256, 130, 40008, 336),
+                                        (512, 600, 5000, 336), (512, 257, 40008, 144)])
+def test_dense_tiles_bit_exact(q, tile, M, N, K):
+    assert q.tile_rows_int8(M, N, K) == tile
+    X, W = rows(M, K, M + 1), rows(N, K, N + 2, torch.float32, 0.02)
+    Y = q.linear_int8(X.cuda(), q.quantize_int8(W.cuda()))
+    assert torch.equal(Y.cpu(), product(X, *quantised(W)))
+
+
 def test_more_rows_than_an_int_counts_threads(q):
     """A CTA of 128 threads per row: 2^24 rows and some have more than 2^31
     threads."""
@@ -217,15 +253,16 @@ def test_more_rows_than_an_int_counts_threads(q):
         assert torch.equal(Y[m].cpu(), product(x, *quantised(W.cpu())))
 
 
-@pytest.mark.parametrize("counts,N,K", [([9], 8, 4096), ([40], 520, 512), ([90] * 6, 5000, 336), ([1000], 12808, 256)],
-                         ids=["shared_64", "tiles_of_64", "tiles_of_256", "tiles_of_512"])
-def test_scales_whose_product_is_no_normal_number(q, counts, N, K):
+@pytest.mark.parametrize("tile,counts,N,K", [(64, [9], 8, 4096), (64, [40], 520, 512), (256, [90] * 6, 5000, 336),
+                                             (512, [1000], 12808, 256)], ids=["64_shared", "64", "256", "512"])
+def test_scales_whose_product_is_no_normal_number(q, tile, counts, N, K):
     """Tiny and huge rows on both sides: xs ws leaves fp32's normal range where the
     sum times both does not, and a sum of zero stays zero. Where the product is
     normal the bits are those of the definition; elsewhere the sum's rounding and
     two products (2^-24 each) and the bf16 result (2^-8), or half of the least
     bf16 step, 2^-134, and overflow to infinity."""
     E, M = len(counts), sum(counts)
+    assert q.tile_rows_int8(M, N, K, E) == tile
     X, W = rows(M, K, M + 3), rows(E * N, K, N + 4, torch.float32)
     X[0::7] *= 2.0 ** -76
     W[0::5] *= 2.0 ** -70
