@@ -1405,6 +1405,10 @@ GroupPlan group_plan(int64_t M, int E, int64_t cols, int64_t steps, bool pairs) 
 // 4096 x 4096, in tiles of 8, of 16, and of 64 by UMMA: 48 rows 41, 43 and 50
 // us, 64 rows 49, 43 and 51 us, 96 rows 59, 50 and 52 us, 128 rows 71, 57 and
 // 52 us (experts differ in rows, and one row too many decodes a tile twice).
+// The mean says nothing of the skew, which the host does not know: with all rows
+// in one of the 8 experts these tiles and those of 64 take 21 and 27 us (16
+// rows), 29 and 37 us (64), 35.2 and 34.6 us (96: each weight decoded six times,
+// of one expert); with half of them there 33.5 and 46, 39 and 47.5, 48.8 and 49.2 us.
 void few_rows_plan(GroupPlan& p, int64_t M, int E, int64_t N) {
     const int64_t act = std::max<int64_t>(1, std::min<int64_t>(E, M)), avg = std::max<int64_t>(1, cdiv(M, act));
     if (avg > 12) return;
@@ -1488,7 +1492,7 @@ qlora_status expert_down(bool bwd, const uint16_t* act, int64_t M, int64_t red, 
     a.status = status;
     a.timeout_ns = timeout_ns();
     if (injected_failure()) return QLORA_ERR_CUDA;
-    if (!bwd && M <= kDownFewRows) {
+    if (!bwd && M <= kDownFewRows && M * r * red <= kDownFewWork) {
         QLORA_LAUNCH(launch_expert_down_few(act, b, a, st), 1, "expert down-projection");
         return QLORA_OK;
     }

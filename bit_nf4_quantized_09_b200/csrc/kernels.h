@@ -353,8 +353,16 @@ struct ExpertDownArgs {
 cudaError_t launch_expert_down(bool b_mn, const CUtensorMap& act, const CUtensorMap& b, ExpertDownArgs a, int tiles,
                                cudaStream_t st);
 // The same with b = A for at most kDownFewRows rows, without tensor cores (the
-// tile fields of the arguments are not read).
+// tile fields of the arguments are not read). It reads 2.25 rows r K bytes
+// through L2, where the tensor-core kernel has a latency that hardly grows with
+// the rows, so it is taken up to kDownFewWork of that product. Measured, forwards of 8
+// experts with it and with the other, 4096 x 11008: 2 rows (r = 16) 30.5 and 39.3
+// us, 56 rows (r = 64, product 39.5 million) 93.9 and 93.4 us, 64 rows (45 million)
+// 101.0 and 93.6 us; 1024 x 11008: 56 rows 40.1 and 45.4, 64 rows 43.6 and 45.4 us,
+// 96 rows (68 million) 46.4 and 47.4 us; 4096 x 4096: 64 rows (17 million) 43.4 and
+// 44.2 us, 128 rows (34 million) 55.6 and 53.6 us, r = 8 49.0 and 51.6 us.
 constexpr int kDownFewRows = 128;
+constexpr int64_t kDownFewWork = int64_t(40) << 20;
 cudaError_t launch_expert_down_few(const uint16_t* X, const uint16_t* A, const ExpertDownArgs& a, cudaStream_t st);
 
 // dA[e] = (sum of sU's terms)^T X, dB[e] = dY^T (sum of sT's terms) over the

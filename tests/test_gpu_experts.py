@@ -200,6 +200,10 @@ TILES = {
     "64_and_512": (64, 512, dict(counts=[600, 290, 31], N=520, K=20032, r=16, pad=2)),
     "64_and_512_fp32": (64, 512, dict(counts=[600, 290, 31], N=520, K=20032, r=32, dq=False)),
     "512_both": (512, 512, dict(counts=[513, 300, 257, 1, 0, 1024, 512, 290, 31], N=1032, K=1088, r=64)),
+    # forwards of few rows behind each of the two down-projections
+    "16_tensor_down": (16, 64, dict(counts=[8, 0, 11, 7, 30, 1, 6, 3], N=72, K=11008, r=64)),
+    "8_tensor_down": (8, 64, dict(counts=[5] * 12, N=40, K=11008, r=64, lead=1, pad=2)),
+    "16_core_down": (16, 64, dict(counts=[8, 0, 11, 7, 30, 1, 6, 3], N=72, K=4096, r=64)),
     "256_both": (256, 256, dict(counts=[600, 290, 31], N=2440, K=2112, r=8)),
     "256_both_fp32": (256, 256, dict(counts=[600, 290, 31], N=2440, K=2112, r=16, dq=False)),
 }
