@@ -1357,13 +1357,14 @@ namespace {
 // 0.44 us), by the tiles of experts somewhat above the mean.
 // NF4: tiles of 256 and 512 run on pairs of CTAs (`pairs`), where a step takes
 // the decoding of half a weight tile, 0.35 us, or its tokens' UMMAs. Measured,
-// forward, 8 experts of 4096 x 4096, tiles of 64, 256 and 512 rows: 320 rows 54,
-// 60 and 61 us; 600 rows 81, 61 and 62; 1024 rows 116, 63 and 67; 2048 rows 180,
-// 88 and 86; 4096 rows 318, 153 and 130.
+// forward, 8 experts of 4096 x 4096, tiles of 64, 256 and 512 rows: 320 rows 53,
+// 58 and 60 us; 600 rows 84, 59 and 60; 1024 rows 119, 62 and 66; 2048 rows 174,
+// 88 and 80; 4096 rows 321, 145 and 128.
 // 8-bit: tiles of 512 run on pairs, of 256 on single CTAs. Measured, 64, 256 and
-// 512 rows: 600 rows of 8 experts of 4096 x 4096 48, 39 and 43 us; 3000 rows 84,
-// 65 and 68; 8192 rows of 16 experts (143 and 135); one weight of 11008 x 4096,
-// 200 rows 41, 34 and 29, 4096 rows (139 and 135).
+// 512 rows: 600 rows of 8 experts of 4096 x 4096 48, 39 and 43 us where most
+// experts have more than 64, 37, 42 and 43 where few have; 3000 rows 78, 71 and 76;
+// 8192 rows of 16 experts 188, 146 and 136; one weight of 11008 x 4096, 100 rows
+// 19, 24 and 21, 200 rows 30, 31 and 29, 4096 rows 211, 141 and 136.
 struct GroupPlan {
     int cap = 64, part_rows = 0;
     size_t tickets_bytes = 0, part_bytes = 0;

@@ -34,19 +34,20 @@
 //   warp 18     TMEM owner, UMMA issuer
 // The producers and the issuer run on warp-uniform values and issue under
 // elect_one(): from one lane of a divergent branch a step of copies cost 570
-// cycles (8192 rows 663 us, 635 us without).
+// cycles (8192 rows, with one rank-r step, 663 us, 635 us without).
 // Block constants are read from the stored form by the threads that use them;
 // no transposed copy of an expert stack's constants is written, most of which
 // few tokens would not use.
 //
 // Bounds, with the down-projection. 8192 rows over 8 experts of 11008 x 4096
-// (r = 64): 632 us, 1194 TFLOP/s, the tensor pipe 81 % busy at the 1.55 GHz that
-// full load leaves; on single CTAs, which decode each weight twice as often, 715
-// us (ALU pipe 66 % busy, tensor pipe 68 %). dX of 4096 x 11008: 550 us of 718
-// for the backward. 1543 rows over 13 experts of 2056 x 4096: 65 us, bound by
-// decoding (a step of 128 x 64 weights per CTA every 0.35 us, the ALU pipe 61 %
-// busy). 160 rows over 8 experts of 4096 x 4096 (tiles of 64): 54 us, a step of
-// 256 x 64 weights every 0.67 us.
+// (r = 64): 645 us, 1170 TFLOP/s (613 us in the first calls, before the clock falls
+// to the 1.48 GHz that the power limit leaves; 654 us after seconds of them), the
+// tensor pipe 81 % busy; on single CTAs, which decode each weight twice as often,
+// 715 us (ALU pipe 66 % busy, tensor pipe 68 %). dX of 4096 x 11008: 533 us at 1.59
+// GHz, of 720 to 728 for the backward. 1543 rows over 13 experts of 2056 x 4096: 65
+// us, bound by decoding (a step of 128 x 64 weights per CTA every 0.35 us, the ALU
+// pipe 61 % busy). 160 rows over 8 experts of 4096 x 4096 (tiles of 64): 52 us, a
+// step of 256 x 64 weights every 0.67 us.
 //
 // The work is dealt out in whole tiles and ranges of reduction steps (tiles.cuh);
 // parts of a tile meet in global memory, in a fixed order: results are bitwise

@@ -29,11 +29,14 @@
 // The work is dealt out in whole tiles and ranges of reduction steps (tiles.cuh);
 // the int32 parts of a tile meet in global memory.
 //
-// Measured, with the quantiser: 4096 x 11008 x 4096 135 us (2.7 Pop/s, the tensor
-// pipe 76 % busy; 139 us in tiles of 256), 8192 rows of 16 experts of 4096 x 4096
-// 134 us (143 us), both bound by the tensor pipe, its clock under load and the
-// rounds of whole tiles. One token, 22016 x 8192: 37 us, 4.9 TB/s, bound by the
-// weight's stream and some 8 us of launches and quantising.
+// Measured, with the quantiser, among calls that go on for seconds, at the 1.58 and
+// 1.52 GHz that the power limit leaves: 4096 x 11008 x 4096 156 us (2.37 Pop/s),
+// 8192 rows of 16 experts of 4096 x 4096 152 to 155 us (1.76 Pop/s). In bursts of 40
+// ms, at 1.8 to 1.9 GHz, 135 and 132 us (141 and 146 us in tiles of 256). The
+// product alone, at 1.84 GHz: 120 us, the tensor pipe 76 % busy. Both are bound by
+// the tensor pipe, its clock and the rounds of whole tiles. One token, 22016 x 8192:
+// 37 us, 4.9 TB/s, bound by the weight's stream and some 8 us of launches and
+// quantising.
 #include "kernels.h"
 #include "tiles.cuh"
 

@@ -2,7 +2,7 @@
 // tiles of up to 16 rows.
 //
 // With a handful of rows per expert every weight is decoded for a few tokens
-// only, and the decoding (what bounds gemm_experts.cu there: 3.4 integer
+// only, and the decoding (what bounds gemm_experts.cu there: 2.75 integer
 // instructions per weight, then a trip through shared memory to the UMMA) is
 // the whole cost. Here the weights never leave registers: mma.m16n8k16 takes
 // them as its A operand straight from the decoder, tokens are its N side (8 or
@@ -39,11 +39,14 @@
 //
 // Measured, with the down-projection: two experts of 11008 x 4096 with a row
 // each 33 us (47.5 MB, 1.4 TB/s; 42 us by UMMA), 64 rows over 8 experts of 4096
-// x 11008 91 us (191.9 MB, 2.1 TB/s; 121 us by UMMA). A step takes 1.4 to 1.7
-// us for 256 x 256 weights (2.9 cycles of the SM for 64 weights); launch and
-// first copies 7 us, the meeting of shared tiles 5 us. 16 decoding warps
-// instead of 8 (two groups, steps in turn) have 96 registers each and were
-// slower: 37 and 103 us.
+// x 11008 90 us (191.9 MB, 2.1 TB/s; 121 us by UMMA). By timestamps a step takes
+// 1.6 us (1.7 in tiles of 16) for 256 x 256 weights (about 3 cycles of the SM for
+// 64 weights). Two rows: a CTA's first stage stands 6 us after the first CTA starts
+// (11 us where the down-projection held its SM), nine steps take 14.5 us, the
+// meeting of shared tiles 2 us. 64 rows: most CTAs start 12 us after the first,
+// behind the down-projection's, the first copies take 4.5 us, 37 steps 62 us, the
+// meeting 2.5 to 4 us. 16 decoding warps instead of 8 (two groups, steps in turn)
+// have 96 registers each and were slower: 37 and 103 us.
 #include "kernels.h"
 #include "tiles.cuh"
 

@@ -313,8 +313,9 @@ qlora_status qlora_expert_order(const int32_t* ids, int64_t M, int E, int32_t* o
  * dA: fp32 [E r, K], dB: fp32 [E N, r], overwritten; zeros for an expert
  * without rows. M == 0: the forward is a no-op, the backward writes zeros.
  * The workspace size comes from qlora_workspace_bytes_experts (N, K of one
- * expert); it does not fall with M, so the largest batch's serves smaller ones. Sums have a fixed order: equal calls give equal bits. Errors,
- * asynchrony and ownership as for qlora_linear_fwd/bwd. */
+ * expert); it does not fall with M, so the largest batch's serves smaller ones.
+ * Sums have a fixed order: equal calls give equal bits. Errors, asynchrony and
+ * ownership as for qlora_linear_fwd/bwd. */
 size_t qlora_workspace_bytes_experts(int op, int64_t M, int64_t N, int64_t K, int r, int E);
 qlora_status qlora_linear_fwd_experts(const uint16_t* X, int64_t M, const qlora_nf4_weight* w, int E,
                                       const int32_t* offsets, const uint16_t* A, const uint16_t* B, int r, float alpha,
@@ -348,12 +349,13 @@ qlora_status qlora_quantize_int8_bf16(const uint16_t* W, int64_t N, int64_t K, i
 /* Y = bf16( xs[m] scale[n] sum_k qx[m, k] codes[n, k] ), qx and xs the rows of X
  * (bf16 [M, K]) quantised as above, one scale per token; the integer sums are
  * exact, and only a result outside fp32's range underflows or overflows, whatever
- * the two scales' product does. A token row with a NaN or an infinity gives a NaN row of Y and touches
- * no other. qlora_linear_int8_experts: w stacks the weights of E experts (E N
- * rows, N % 8 == 0), rows of X and Y grouped by offsets as above; rows of no
- * expert are left as they were. Workspace: qlora_workspace_bytes_int8 (N, K of
- * one expert; E = 1 for qlora_linear_int8; it does not fall with M); it holds the quantised tokens, so
- * two calls that may overlap need one each. M == 0 is a no-op. */
+ * the two scales' product does. A token row with a NaN or an infinity gives a NaN
+ * row of Y and touches no other. qlora_linear_int8_experts: w stacks the weights of
+ * E experts (E N rows, N % 8 == 0), rows of X and Y grouped by offsets as above;
+ * rows of no expert are left as they were. Workspace: qlora_workspace_bytes_int8 (N,
+ * K of one expert; E = 1 for qlora_linear_int8; it does not fall with M); it holds
+ * the quantised tokens, so two calls that may overlap need one each. M == 0 is a
+ * no-op. */
 size_t qlora_workspace_bytes_int8(int64_t M, int64_t N, int64_t K, int E);
 qlora_status qlora_linear_int8(const uint16_t* X, int64_t M, const qlora_int8_weight* w, uint16_t* Y, void* ws,
                                size_t ws_bytes, void* stream);
