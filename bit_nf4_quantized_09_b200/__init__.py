@@ -584,16 +584,16 @@ def _stack_view(w: NF4Weight, where: str, dev) -> Nf4WeightC:
     seen = w.__dict__.get("_checked")
     if seen is None or seen[0] is not v or seen[1] != dev:
         nb = w.N * w.K // 64
-        parts = [("codes", w.codes, nb * 32, torch.uint8)]
+        byte, fp32 = (torch.uint8, torch.float8_e4m3fn), (torch.float32,)
+        parts = [("codes", w.codes, nb * 32, byte)]
         if w.double_quant:
-            parts += [("qabsmax", w.qabsmax, nb, torch.uint8), ("s2", w.s2, -(-nb // 256), torch.float32),
-                      ("mean", w.mean, 1, torch.float32)]
+            parts += [("qabsmax", w.qabsmax, nb, byte), ("s2", w.s2, -(-nb // 256), fp32), ("mean", w.mean, 1, fp32)]
         else:
-            parts.append(("absmax", w.absmax, nb, torch.float32))
-        for what, t, n, dtype in parts:
-            if t is None or t.dtype is not dtype or t.device != dev or t.numel() < n:
+            parts.append(("absmax", w.absmax, nb, fp32))
+        for what, t, n, types in parts:
+            if t is None or t.dtype not in types or t.device != dev or t.numel() < n:
                 got = "None" if t is None else f"{t.numel()} of {t.dtype} on {t.device}"
-                raise QLoraError(-1, where, f"the weight's {what}: {n} of {dtype} on {dev} are wanted, got {got}")
+                raise QLoraError(-1, where, f"the weight's {what}: {n} of {types[0]} on {dev} are wanted, got {got}")
         w.__dict__["_checked"] = (v, dev)
     return v
 

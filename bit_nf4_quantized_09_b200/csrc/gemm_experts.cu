@@ -14,8 +14,8 @@
 // B_e^T, sU . A_e) is two more reduction steps of the same accumulators, their
 // operands loaded by TMA: the bf16 rounding of sT or sU, then that of what it
 // leaves. How far one rounding shows in the result depends on the adapter's part
-// of it and not on the shapes, so both steps always run (2^-17 of |sT| |B|
-// instead of 2^-9; one step of 66 at K = 4096).
+// of it and not on the shapes, so both steps always run (2^-16 of |sT| |B|
+// at most instead of 2^-8; one step of 66 at K = 4096).
 //
 // Tiles of up to 64 tokens run on single CTAs, two UMMAs of M = 128 at a time.
 // Tiles of up to 256 or 512 tokens run on pairs of CTAs (a cluster of two on

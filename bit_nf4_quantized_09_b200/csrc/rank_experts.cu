@@ -12,7 +12,7 @@
 // the fp32 gradients at fp32 accuracy:
 //   - sT and sU leave as sums of bf16 numbers (two for sT, which is kept
 //     between the passes; three for sU), each rounding the rest of the one
-//     before: 2^-17 and 2^-25 relative instead of bf16's 2^-9; the gradients
+//     before: 2^-16 and 2^-24 relative at most instead of bf16's 2^-8; the gradients
 //     run one UMMA per term into the same accumulator, which costs little
 //     beside reading X and dY once;
 //   - every 512 reduction elements (128 for sT and sU: at 512 as many of their
