@@ -618,7 +618,8 @@ def linear_fwd_experts(X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: torch.
     [offsets[e], offsets[e + 1]) gives Y[m] = X[m] deq(W_e)^T + sT[m] B_e^T, sT[m] =
     (alpha/r) X[m] A_e^T. A: bf16 [E r, K]; B: bf16 [E N, r]; offsets: int32 [E + 1];
     sT: bf16 [M, 2 r], a sum of two terms. Rows of no expert keep what Y and sT
-    held (a Y or sT allocated here holds nothing there)."""
+    held (a Y or sT allocated here holds nothing there). Outputs may not overlap
+    inputs."""
     where = "qlora_linear_fwd_experts"
     M, N, K, r, dev, v = _expert_shapes(where, X, w, A, B, offsets, E)
     Y = _out(Y, "Y", where, (M, N), torch.bfloat16, dev)
@@ -638,7 +639,8 @@ def linear_bwd_experts(dY: torch.Tensor, X: torch.Tensor, w: NF4Weight, A: torch
                        dB: torch.Tensor | None = None, ws: torch.Tensor | None = None):
     """(dX bf16 [M, K], dA fp32 [E r, K], dB fp32 [E N, r]) of linear_fwd_experts;
     sT as it returned it, or None to recompute it. An expert without rows gets
-    zero gradients; rows of no expert keep what dX held."""
+    zero gradients; rows of no expert keep what dX held. Outputs may not overlap
+    inputs."""
     where = "qlora_linear_bwd_experts"
     M, N, K, r, dev, v = _expert_shapes(where, X, w, A, B, offsets, E)
     _want(dY, "dY", where, (M, N), torch.bfloat16, dev)

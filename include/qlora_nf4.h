@@ -314,8 +314,9 @@ qlora_status qlora_expert_order(const int32_t* ids, int64_t M, int E, int32_t* o
  * without rows. M == 0: the forward is a no-op, the backward writes zeros.
  * The workspace size comes from qlora_workspace_bytes_experts (N, K of one
  * expert); it does not fall with M, so the largest batch's serves smaller ones.
- * Sums have a fixed order: equal calls give equal bits. Errors, asynchrony and
- * ownership as for qlora_linear_fwd/bwd. */
+ * Sums have a fixed order: equal calls give equal bits. No output may overlap an
+ * input or another output: tiles are written while others still read. Errors,
+ * asynchrony and ownership as for qlora_linear_fwd/bwd. */
 size_t qlora_workspace_bytes_experts(int op, int64_t M, int64_t N, int64_t K, int r, int E);
 qlora_status qlora_linear_fwd_experts(const uint16_t* X, int64_t M, const qlora_nf4_weight* w, int E,
                                       const int32_t* offsets, const uint16_t* A, const uint16_t* B, int r, float alpha,
